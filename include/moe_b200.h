@@ -448,6 +448,156 @@ MOE_API moe_status moe_ep_reorder(int32_t world, int32_t local_experts, const in
                                   const void* src, void* dst, int32_t to_expert_major, void* stream);
 
 /*
+ * Training the layer: backward passes and gradient clipping. The pages give
+ * the forward and the loss-free balancing of training; the gradients below
+ * are the forward's equations differentiated. A step of one layer, x -> y
+ * with the output gradient dy:
+ *   forward   moe_route_train, moe_dispatch_rows, moe_experts_train (routed
+ *             rows; and the shared MLP as one group of its own), moe_combine
+ *   backward  moe_combine_backward, moe_experts_backward (routed rows; shared
+ *             MLP on dy itself), moe_route_backward, moe_dispatch_backward
+ *   update    moe_grad_norm, moe_grad_clip, moe_bias_update
+ * The selection itself has no gradient, nor has b. All calls are
+ * deterministic (no order-dependent atomics), asynchronous on `stream`, and
+ * can be captured into a CUDA graph. A buffer is read only as an input or
+ * written only as an output unless stated; inputs and outputs must not overlap.
+ */
+
+/*
+ * moe_experts that also keeps what its backward needs: the pre-activations
+ * g = W1 x and u = W3 x of every row.
+ *   gu [rows, 2 d_ff] out, cfg->dtype, 16-byte aligned: a row's g, then its u
+ * Other arguments, workspace and errors as for moe_experts. bf16: h is
+ * computed from the unrounded g and u with the hardware exponential (where
+ * moe_experts uses the hardware tanh), so y may differ from moe_experts' in
+ * its last bit.
+ */
+MOE_API moe_status moe_experts_train(const moe_cfg* cfg, int64_t rows, const int32_t* counts, const void* x_rows,
+                                     const float* gate_rows, const void* W1, const void* W3, const void* W2,
+                                     void* y_rows, void* gu, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Backward of moe_experts_train. For each row, with h = silu(g) u,
+ * q = W2^T dy and s = sigmoid(g):
+ *   dgate = q . h
+ *   du = gate q g s          dg = gate q u s (1 + g (1 - s))
+ *   dx = W1^T dg + W3^T du
+ * and for each group, summed over its rows:
+ *   dW1 = dg x^T   dW3 = du x^T   dW2 = dy (gate h)^T
+ *   counts, x_rows, gate_rows (or NULL), W1, W3, W2   as in the forward
+ *   gu         [rows, 2 d_ff] as moe_experts_train wrote it
+ *   dy_rows    [rows, d]
+ *   dx_rows    [rows, d] out, or NULL to skip
+ *   dgate_rows [rows] fp32 out, or NULL to skip (with gate_rows NULL: the
+ *              gradient of a gate of 1)
+ *   dW1, dW3 [E, d_ff, d], dW2 [E, d, d_ff] out, all three or all NULL, of
+ *              type grad_dtype: MOE_F32, or MOE_BF16 when cfg->dtype is
+ *              MOE_BF16. A group without rows gets zeros.
+ *   accumulate nonzero: added to dW1, dW3 and dW2 instead of written (fp32
+ *              gradients only; MOE_ERR_UNSUPPORTED for bf16)
+ * bf16: products on the tensor cores with fp32 accumulation; dg, du and
+ * gate * h are rounded to bf16 as operands of the later products (one
+ * rounding each, as the forward rounds h), dgate is fp32 throughout. rows == 0
+ * zeroes the weight gradients (unless accumulating). Workspace:
+ * moe_experts_backward_workspace_size(cfg, rows) bytes; the device-status
+ * word as for moe_experts (counts that do not sum to rows: MOE_DEV_BAD_EXPERT,
+ * no row is computed and the weight gradients are those of no rows).
+ */
+MOE_API moe_status moe_experts_backward_workspace_size(const moe_cfg* cfg, int64_t rows, size_t* bytes);
+MOE_API moe_status moe_experts_backward(const moe_cfg* cfg, int64_t rows, const int32_t* counts, const void* x_rows,
+                                        const float* gate_rows, const void* W1, const void* W3, const void* W2,
+                                        const void* gu, const void* dy_rows, void* dx_rows, float* dgate_rows,
+                                        void* dW1, void* dW3, void* dW2, int32_t grad_dtype, int32_t accumulate,
+                                        void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Backward of moe_combine for its routed rows: dy_rows[slot_pos[t, i]] =
+ * dy[t] for every placed pair (dy [T, d], dy_rows [T*top_k, d], slot_pos as
+ * moe_dispatch_rows wrote it; rows that no pair names are left as they are).
+ * The shared rows' gradient is dy itself.
+ */
+MOE_API moe_status moe_combine_backward(const moe_cfg* cfg, int64_t T, const void* dy, const int32_t* slot_pos,
+                                        void* dy_rows, void* stream);
+
+/*
+ * Backward of the dispatch and of the layer's other uses of x:
+ * dx[t] = sum over i of dx_rows[slot_pos[t, i]] (ascending expert; -1
+ * skipped) + dx_shared[t] + dx_router[t] (each [T, d] or NULL), accumulated
+ * in fp32 in that order and rounded once.
+ */
+MOE_API moe_status moe_dispatch_backward(const moe_cfg* cfg, int64_t T, const void* dx_rows, const int32_t* slot_pos,
+                                         const void* dx_shared, const void* dx_router, void* dx, void* stream);
+
+/*
+ * moe_route that also keeps the logits z = x W_r^T for its backward.
+ *   logits [T, n_routed] fp32 out
+ * Same selection and gates as moe_route, bit for bit; same workspace.
+ */
+MOE_API moe_status moe_route_train(const moe_cfg* cfg, int64_t T, const void* x, const void* W_r, const float* b,
+                                   int32_t* topk_idx, float* gates, float* logits, void* ws, size_t ws_bytes,
+                                   void* stream);
+
+/*
+ * Backward of the router: the gradients of x and W_r from those of the gates.
+ * With s the scores of a token, Z their sum over its selection and c =
+ * route_scale: ds_j = (c / Z) (dG_j - sum_i dG_i s_i / Z) for normalised
+ * gates, c dG_j otherwise (j selected); dz_j = ds_j s_j (1 - s_j) for
+ * sigmoid, s_j (ds_j - sum_i ds_i s_i) for softmax scores;
+ * dx = dz W_r, dW_r = dz^T x.
+ *   x, W_r     as for moe_route; logits, topk_idx as moe_route_train wrote them
+ *   slot_pos   NULL: dgates is [T, top_k] in topk_idx's slot order. Otherwise
+ *              as moe_dispatch_rows wrote it, and dgates is [T*top_k] in
+ *              permuted order (moe_experts_backward's dgate_rows)
+ *   dx         [T, d] out, cfg->dtype, or NULL to skip
+ *   dW_r       [n_routed, d] out, or NULL; grad_dtype and accumulate as in
+ *              moe_experts_backward
+ * An index outside [0, n_routed) sets MOE_DEV_BAD_EXPERT and has no gradient.
+ * Workspace: moe_route_backward_workspace_size(cfg, T) bytes.
+ */
+MOE_API moe_status moe_route_backward_workspace_size(const moe_cfg* cfg, int64_t T, size_t* bytes);
+MOE_API moe_status moe_route_backward(const moe_cfg* cfg, int64_t T, const void* x, const void* W_r,
+                                      const float* logits, const int32_t* topk_idx, const float* dgates,
+                                      const int32_t* slot_pos, void* dx, void* dW_r, int32_t grad_dtype,
+                                      int32_t accumulate, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * One gradient tensor of moe_grad_norm and moe_grad_clip: numel contiguous
+ * elements of dtype MOE_F32 or MOE_BF16 at src (aligned to the element), in
+ * device memory. moe_grad_clip writes to dst; NULL or src itself: in place.
+ * dst must not overlap any other tensor's src or dst, nor src in part.
+ */
+typedef struct moe_grad_tensor {
+  const void* src;
+  void* dst;
+  int64_t numel;
+  int32_t dtype;
+  int32_t reserved; /* 0 */
+} moe_grad_tensor;
+
+/*
+ * sumsq[0] (fp64, device) = sum of the squares of all n tensors' elements
+ * (n == 0: 0). The array is read on the host during the call only. A job
+ * whose gradients are spread over ranks adds the ranks' sums (one all-reduce
+ * of this value) before moe_grad_clip. Workspace:
+ * moe_grad_norm_workspace_size(n) bytes.
+ */
+MOE_API moe_status moe_grad_norm_workspace_size(int32_t n, size_t* bytes);
+MOE_API moe_status moe_grad_norm(const moe_grad_tensor* tensors, int32_t n, double* sumsq, void* ws,
+                                 size_t ws_bytes, void* stream);
+
+/*
+ * dst = src * min(1, max_norm / norm) with norm = sqrt(sumsq[0]) (sumsq on
+ * the device, as moe_grad_norm wrote it), the product in fp32 and rounded
+ * once to the tensor's type. A norm that is not finite scales by 1: the
+ * gradients stay as they are and the caller sees it in norm_out. A tensor in
+ * place that needs no scaling is not touched.
+ *   max_norm   >= 0 (infinity: no clipping)
+ *   norm_out   [1] fp32 device, or NULL: the norm before clipping
+ */
+MOE_API moe_status moe_grad_clip(const moe_grad_tensor* tensors, int32_t n, const double* sumsq, float max_norm,
+                                 float* norm_out, void* stream);
+
+/*
  * Self-check of the failure path (no counterpart in the pages): launches a
  * one-warp kernel that waits, with the same bounded wait every pipeline in
  * the library uses, on a barrier that nothing ever completes. After the wait

@@ -24,7 +24,9 @@ STATUS_NAMES = {0: "MOE_OK", 1: "MOE_ERR_INVALID_ARG", 2: "MOE_ERR_UNSUPPORTED",
                 4: "MOE_ERR_CUDA", 5: "MOE_ERR_DEVICE"}
 EXPORTS = ["moe_workspace_size", "moe_workspace_size_host", "moe_route", "moe_dispatch", "moe_forward",
            "moe_forward_fp8", "moe_dispatch_rows", "moe_experts_workspace_size", "moe_experts", "moe_combine",
-           "moe_ep_reorder",
+           "moe_ep_reorder", "moe_experts_train", "moe_experts_backward_workspace_size", "moe_experts_backward",
+           "moe_combine_backward", "moe_dispatch_backward", "moe_route_train", "moe_route_backward_workspace_size",
+           "moe_route_backward", "moe_grad_norm_workspace_size", "moe_grad_norm", "moe_grad_clip",
            "moe_forward_host", "moe_forward_host_fp8", "moe_forward_host_async", "moe_forward_host_fp8_async",
            "moe_host_wait", "moe_workspace_release", "moe_device_status", "moe_set_stage_events", "moe_route_noalloc", "moe_bias_update", "moe_selftest_wait_timeout",
            "moe_status_string", "moe_last_cuda_error"]
@@ -45,6 +47,13 @@ class Fp8Matrix(ctypes.Structure):
     """moe_fp8_matrix of the C ABI: e4m3 codes and UE8M0 scales per 128 x 128 block."""
 
     _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p)]
+
+
+class GradTensor(ctypes.Structure):
+    """moe_grad_tensor of the C ABI: one gradient and where its clipped form goes."""
+
+    _fields_ = [("src", ctypes.c_void_p), ("dst", ctypes.c_void_p), ("numel", ctypes.c_int64),
+                ("dtype", ctypes.c_int32), ("reserved", ctypes.c_int32)]
 
 
 class MoeError(RuntimeError):
@@ -94,6 +103,19 @@ def lib() -> ctypes.CDLL:
         L.moe_experts.argtypes = [CFG, I64, P, P, P, P, P, P, P, P, SZ, P]
         L.moe_combine.argtypes = [CFG, I64, P, P, P, P, P]
         L.moe_ep_reorder.argtypes = [ctypes.c_int32, ctypes.c_int32, P, I64, P, P, ctypes.c_int32, P]
+        I32, SZP = ctypes.c_int32, ctypes.POINTER(SZ)
+        L.moe_experts_train.argtypes = [CFG, I64, P, P, P, P, P, P, P, P, P, SZ, P]
+        L.moe_experts_backward_workspace_size.argtypes = [CFG, I64, SZP]
+        L.moe_experts_backward.argtypes = [CFG, I64, P, P, P, P, P, P, P, P, P, P, P, P, P, I32, I32, P, SZ, P]
+        L.moe_combine_backward.argtypes = [CFG, I64, P, P, P, P]
+        L.moe_dispatch_backward.argtypes = [CFG, I64, P, P, P, P, P, P]
+        L.moe_route_train.argtypes = [CFG, I64, P, P, P, P, P, P, P, SZ, P]
+        L.moe_route_backward_workspace_size.argtypes = [CFG, I64, SZP]
+        L.moe_route_backward.argtypes = [CFG, I64, P, P, P, P, P, P, P, P, I32, I32, P, SZ, P]
+        GT = ctypes.POINTER(GradTensor)
+        L.moe_grad_norm_workspace_size.argtypes = [I32, SZP]
+        L.moe_grad_norm.argtypes = [GT, I32, P, P, SZ, P]
+        L.moe_grad_clip.argtypes = [GT, I32, P, ctypes.c_float, P, P]
         FP8P = ctypes.POINTER(Fp8Matrix)
         L.moe_forward_fp8.argtypes = [CFG, I64, P, P, P, FP8P, FP8P, FP8P, FP8P, FP8P, FP8P, P, P, P, P, SZ, P]
         L.moe_forward_host.argtypes = [CFG, I64, P, P, P, P, P, P, P, P, P, P, P, SZ, P]
@@ -270,6 +292,126 @@ def ep_reorder(world, local_experts, counts, row_bytes, src, dst, to_expert_majo
     """Rows between source-major and expert-major order of the blocks counts[world, local_experts]."""
     _check("moe_ep_reorder", lib().moe_ep_reorder(world, local_experts, _ptr(counts), row_bytes, _ptr(src), _ptr(dst),
                                                   int(bool(to_expert_major)), _stream(stream)))
+
+
+def experts_train(cfg, rows, counts, x_rows, gate_rows, W1, W3, W2, y_rows, gu, ws, ws_bytes=None, stream=None):
+    """experts() that also keeps the pre-activations gu [rows, 2 d_ff] for experts_backward."""
+    ws_bytes = ws.numel() * ws.element_size() if ws_bytes is None else ws_bytes
+    _check("moe_experts_train", lib().moe_experts_train(ctypes.byref(cfg), rows, _ptr(counts), _ptr(x_rows),
+                                                        _ptr(gate_rows), _ptr(W1), _ptr(W3), _ptr(W2), _ptr(y_rows),
+                                                        _ptr(gu), _ptr(ws), ws_bytes, _stream(stream)))
+
+
+def experts_backward_workspace_size(cfg: MoeCfg, rows: int) -> int:
+    n = ctypes.c_size_t(0)
+    _check("moe_experts_backward_workspace_size",
+           lib().moe_experts_backward_workspace_size(ctypes.byref(cfg), rows, ctypes.byref(n)))
+    return n.value
+
+
+def _grad_dtype(cfg, grad_dtype) -> int:
+    return cfg.dtype if grad_dtype is None else _lookup(_DTYPES, "grad_dtype", grad_dtype)
+
+
+def experts_backward(cfg, rows, counts, x_rows, gate_rows, W1, W3, W2, gu, dy_rows, dx_rows, dgate_rows, dW1, dW3,
+                     dW2, ws, grad_dtype=None, accumulate=False, ws_bytes=None, stream=None):
+    """Gradients of experts_train: of the rows, the gates and the weights
+    (dx_rows, dgate_rows, or all of dW1, dW3, dW2 may be None). grad_dtype is
+    the weight gradients' type ("bf16", "f32"; None: the layer's); fp32
+    gradients can be accumulated."""
+    ws_bytes = ws.numel() * ws.element_size() if ws_bytes is None else ws_bytes
+    _check("moe_experts_backward",
+           lib().moe_experts_backward(ctypes.byref(cfg), rows, _ptr(counts), _ptr(x_rows), _ptr(gate_rows), _ptr(W1),
+                                      _ptr(W3), _ptr(W2), _ptr(gu), _ptr(dy_rows), _ptr(dx_rows), _ptr(dgate_rows),
+                                      _ptr(dW1), _ptr(dW3), _ptr(dW2), _grad_dtype(cfg, grad_dtype),
+                                      int(bool(accumulate)), _ptr(ws), ws_bytes, _stream(stream)))
+
+
+def combine_backward(cfg, T, dy, slot_pos, dy_rows, stream=None):
+    """dy_rows[slot_pos[t, i]] = dy[t]: the output gradient of every permuted row."""
+    _check("moe_combine_backward", lib().moe_combine_backward(ctypes.byref(cfg), T, _ptr(dy), _ptr(slot_pos),
+                                                              _ptr(dy_rows), _stream(stream)))
+
+
+def dispatch_backward(cfg, T, dx_rows, slot_pos, dx_shared, dx_router, dx, stream=None):
+    """dx[t] = sum of the token's permuted rows + dx_shared[t] + dx_router[t] (either may be None)."""
+    _check("moe_dispatch_backward", lib().moe_dispatch_backward(ctypes.byref(cfg), T, _ptr(dx_rows), _ptr(slot_pos),
+                                                                _ptr(dx_shared), _ptr(dx_router), _ptr(dx),
+                                                                _stream(stream)))
+
+
+def route_train(cfg, T, x, W_r, b, topk_idx, gates, logits, ws, ws_bytes=None, stream=None):
+    """route() that also keeps the logits [T, n_routed] fp32 for route_backward."""
+    ws_bytes = ws.numel() * ws.element_size() if ws_bytes is None else ws_bytes
+    _check("moe_route_train", lib().moe_route_train(ctypes.byref(cfg), T, _ptr(x), _ptr(W_r), _ptr(b), _ptr(topk_idx),
+                                                    _ptr(gates), _ptr(logits), _ptr(ws), ws_bytes, _stream(stream)))
+
+
+def route_backward_workspace_size(cfg: MoeCfg, T: int) -> int:
+    n = ctypes.c_size_t(0)
+    _check("moe_route_backward_workspace_size",
+           lib().moe_route_backward_workspace_size(ctypes.byref(cfg), T, ctypes.byref(n)))
+    return n.value
+
+
+def route_backward(cfg, T, x, W_r, logits, topk_idx, dgates, slot_pos, dx, dW_r, ws, grad_dtype=None,
+                   accumulate=False, ws_bytes=None, stream=None):
+    """Gradients of the router's x and W_r (either may be None) from those of
+    the gates: dgates [T, k] in slot order with slot_pos None, else by permuted
+    row (experts_backward's dgate_rows) with dispatch_rows' slot_pos."""
+    ws_bytes = ws.numel() * ws.element_size() if ws_bytes is None else ws_bytes
+    _check("moe_route_backward",
+           lib().moe_route_backward(ctypes.byref(cfg), T, _ptr(x), _ptr(W_r), _ptr(logits), _ptr(topk_idx),
+                                    _ptr(dgates), _ptr(slot_pos), _ptr(dx), _ptr(dW_r),
+                                    _grad_dtype(cfg, grad_dtype), int(bool(accumulate)), _ptr(ws), ws_bytes,
+                                    _stream(stream)))
+
+
+class GradList:
+    """The gradients of one grad_norm / grad_clip call: contiguous fp32 or
+    bf16 tensors, and where their clipped forms go (dsts None: in place).
+    Holds references to the tensors; build it once and use it every step."""
+
+    def __init__(self, srcs, dsts=None):
+        import torch
+        dtypes = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16}
+        self.srcs = list(srcs)
+        self.dsts = self.srcs if dsts is None else list(dsts)
+        if len(self.dsts) != len(self.srcs):
+            raise ValueError(f"{len(self.srcs)} gradients but {len(self.dsts)} destinations")
+        self.table = (GradTensor * len(self.srcs))()
+        for entry, src, dst in zip(self.table, self.srcs, self.dsts):
+            if src.dtype not in dtypes or dst.dtype != src.dtype:
+                raise ValueError(f"gradients are fp32 or bf16, clipped into the same type: got {src.dtype}, {dst.dtype}")
+            if not src.is_contiguous() or not dst.is_contiguous() or dst.numel() != src.numel():
+                raise ValueError("a gradient and its destination are contiguous and of one size")
+            entry.src, entry.dst = src.data_ptr(), dst.data_ptr()
+            entry.numel, entry.dtype = src.numel(), dtypes[src.dtype]
+
+    def __len__(self):
+        return len(self.srcs)
+
+
+def grad_norm_workspace_size(grads) -> int:
+    """Workspace bytes of grad_norm for a GradList (or a number of tensors)."""
+    n = ctypes.c_size_t(0)
+    count = grads if isinstance(grads, int) else len(grads)
+    _check("moe_grad_norm_workspace_size", lib().moe_grad_norm_workspace_size(count, ctypes.byref(n)))
+    return n.value
+
+
+def grad_norm(grads: GradList, sumsq, ws, ws_bytes=None, stream=None):
+    """sumsq [1] fp64 = sum of the squares of every gradient's elements."""
+    ws_bytes = ws.numel() * ws.element_size() if ws_bytes is None else ws_bytes
+    _check("moe_grad_norm", lib().moe_grad_norm(grads.table, len(grads), _ptr(sumsq), _ptr(ws), ws_bytes,
+                                                _stream(stream)))
+
+
+def grad_clip(grads: GradList, sumsq, max_norm, norm_out=None, stream=None):
+    """Every gradient times min(1, max_norm / sqrt(sumsq)), into its destination;
+    norm_out [1] fp32 receives the norm before clipping."""
+    _check("moe_grad_clip", lib().moe_grad_clip(grads.table, len(grads), _ptr(sumsq), float(max_norm), _ptr(norm_out),
+                                                _stream(stream)))
 
 
 def forward_host(cfg, T, x_host, W_r, b, W1, W3, W2, Ws1, Ws3, Ws2, y_host, ws, ws_bytes=None,

@@ -14,7 +14,8 @@ LIB = os.path.join(HERE, "libmoe_b200.so")
 LIB_DEBUG = os.path.join(HERE, "libmoe_b200_debug.so")
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 SOURCES = ["moe_abi.cu", "router.cu", "tensor_map.cu", "dispatch.cu", "combine.cu", "expert_tc.cu", "expert_simt.cu",
-           "route_noalloc.cu", "bias_update.cu", "selftest.cu"]
+           "route_noalloc.cu", "bias_update.cu", "selftest.cu", "train_abi.cu", "train_simt.cu", "wgrad_tc.cu",
+           "route_bwd.cu", "grad_clip.cu"]
 FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a", "-O3", "-lineinfo", "-std=c++17",
          "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden"]
 

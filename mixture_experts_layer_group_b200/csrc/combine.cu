@@ -56,6 +56,7 @@ struct Io<float> {
 template <typename TE, int KMAX>
 __global__ void __launch_bounds__(256) combine_kernel(const uint4* __restrict__ y_rows,
                                                       const uint4* __restrict__ shared_rows,
+                                                      const uint4* __restrict__ more_rows,
                                                       const int32_t* __restrict__ slot_pos, int64_t T,
                                                       int k, int64_t R, int vecs, uint4* __restrict__ y) {
   constexpr int P = Io<TE>::kPerVec;
@@ -72,6 +73,8 @@ __global__ void __launch_bounds__(256) combine_kernel(const uint4* __restrict__ 
       for (int s = 0; s < KMAX; ++s)
         if (rows[s] >= 0) buf[s] = __ldg(y_rows + (int64_t)rows[s] * vecs + v);
       if (shared_rows) buf[KMAX] = __ldg(shared_rows + t * vecs + v);
+      uint4 more;
+      if (more_rows) more = __ldg(more_rows + t * vecs + v);
       float acc[P];
 #pragma unroll
       for (int i = 0; i < P; ++i) acc[i] = 0.f;
@@ -79,6 +82,7 @@ __global__ void __launch_bounds__(256) combine_kernel(const uint4* __restrict__ 
       for (int s = 0; s < KMAX; ++s)
         if (rows[s] >= 0) Io<TE>::add(buf[s], acc);
       if (shared_rows) Io<TE>::add(buf[KMAX], acc);
+      if (more_rows) Io<TE>::add(more, acc);
       y[t * vecs + v] = Io<TE>::pack(acc);
     }
   }
@@ -87,24 +91,25 @@ __global__ void __launch_bounds__(256) combine_kernel(const uint4* __restrict__ 
 }  // namespace
 
 cudaError_t launch_combine_rows(const Problem& p, const void* routed_rows, const void* shared_rows,
-                                const int32_t* slot_pos, void* y, cudaStream_t s) {
+                                const int32_t* slot_pos, void* y, cudaStream_t s, const void* more_rows) {
   const int vecs = (int)((int64_t)p.d * p.elem / 16);
   const int threads = vecs >= 256 ? 256 : (vecs >= 128 ? 128 : 64);
   int64_t cap = (int64_t)device_sm_count() * 16;
   unsigned blocks = (unsigned)(p.T < cap ? p.T : cap);
   const uint4* yr = (const uint4*)routed_rows;
   const uint4* ys = (const uint4*)shared_rows;
+  const uint4* ym = (const uint4*)more_rows;
   if (p.dtype == MOE_BF16) {
     if (p.k <= 8)
-      combine_kernel<__nv_bfloat16, 8><<<blocks, threads, 0, s>>>(yr, ys, slot_pos, p.T, p.k, p.R, vecs, (uint4*)y);
+      combine_kernel<__nv_bfloat16, 8><<<blocks, threads, 0, s>>>(yr, ys, ym, slot_pos, p.T, p.k, p.R, vecs, (uint4*)y);
     else
-      combine_kernel<__nv_bfloat16, kMaxTopK><<<blocks, threads, 0, s>>>(yr, ys, slot_pos, p.T, p.k, p.R, vecs,
+      combine_kernel<__nv_bfloat16, kMaxTopK><<<blocks, threads, 0, s>>>(yr, ys, ym, slot_pos, p.T, p.k, p.R, vecs,
                                                                         (uint4*)y);
   } else {
     if (p.k <= 8)
-      combine_kernel<float, 8><<<blocks, threads, 0, s>>>(yr, ys, slot_pos, p.T, p.k, p.R, vecs, (uint4*)y);
+      combine_kernel<float, 8><<<blocks, threads, 0, s>>>(yr, ys, ym, slot_pos, p.T, p.k, p.R, vecs, (uint4*)y);
     else
-      combine_kernel<float, kMaxTopK><<<blocks, threads, 0, s>>>(yr, ys, slot_pos, p.T, p.k, p.R, vecs, (uint4*)y);
+      combine_kernel<float, kMaxTopK><<<blocks, threads, 0, s>>>(yr, ys, ym, slot_pos, p.T, p.k, p.R, vecs, (uint4*)y);
   }
   return cudaGetLastError();
 }

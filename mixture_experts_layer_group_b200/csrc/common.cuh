@@ -185,6 +185,16 @@ MOE_DEV void tma_load_2d_pair(void* smem_dst, const void* tmap, uint32_t bar_clu
       : "memory");
 }
 
+// The same for a 3-D tensor map (c0 innermost).
+MOE_DEV void tma_load_3d_pair(void* smem_dst, const void* tmap, uint32_t bar_cluster, int32_t c0, int32_t c1,
+                              int32_t c2, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+      ".L2::cache_hint [%0], [%1, {%3, %4, %5}], [%2], %6;" ::"r"(smem_u32(smem_dst)),
+      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(bar_cluster), "r"(c0), "r"(c1), "r"(c2), "l"(policy)
+      : "memory");
+}
+
 // 2-D tiled store of a shared-memory box to global memory (bulk group). The
 // box start (c0, c1) must be non-negative and c0 a multiple of 16 bytes'
 // worth of elements; rows/columns beyond the tensor are clipped.
@@ -352,12 +362,31 @@ MOE_DEV uint64_t smem_desc_sw128(uint32_t smem_addr) {
   return d;
 }
 
+// The same for an MN-major operand tile: 128-byte rows hold 64 consecutive
+// elements of the M (or N) dimension at one k, 8 rows of consecutive k form a
+// 1024-byte swizzle atom. Leading byte offset: from one 64-element chunk of
+// M (N) to the next (`chunk_bytes`, the bytes of a 64 x K box); stride byte
+// offset: from 8 k to the next 8 (1024 B). Advancing K by 16 elements adds
+// 2048 B to the start address.
+MOE_DEV uint64_t smem_desc_sw128_mn(uint32_t smem_addr, uint32_t chunk_bytes) {
+  uint64_t d = 0;
+  d |= (uint64_t)((smem_addr & 0x3FFFFu) >> 4);
+  d |= (uint64_t)(chunk_bytes >> 4) << 16;
+  d |= (uint64_t)(1024u >> 4) << 32;
+  d |= (uint64_t)1u << 46;
+  d |= (uint64_t)2u << 61;
+  return d;
+}
+
 // Instruction descriptor, kind::f16: fp32 accumulator (bits [4,6) = 1), A and
 // B bf16 (bits [7,10) and [10,13) = 1), both K-major (bits 15, 16 = 0),
 // N >> 3 in bits [17,23), M >> 4 in bits [24,29).
 __host__ __device__ constexpr uint32_t idesc_bf16_f32(uint32_t M, uint32_t N) {
   return (1u << 4) | (1u << 7) | (1u << 10) | ((N >> 3) << 17) | ((M >> 4) << 24);
 }
+
+// Instruction-descriptor bits for an MN-major A or B operand.
+constexpr uint32_t kIdescAMn = 1u << 15, kIdescBMn = 1u << 16;
 
 // 32 lanes x 32 consecutive fp32 columns from tensor memory; thread i of the
 // warp receives row (lane base + i). The caller issues tmem_wait_ld() before
@@ -399,6 +428,16 @@ MOE_DEV void stmatrix_x4_trans(uint32_t smem_addr, uint32_t r0, uint32_t r1, uin
                : "memory");
 }
 
+// The mirror of stmatrix_x4_trans: thread 8 m + k gives the address of stored
+// row k of matrix m; thread i receives the pair (stored columns i / 4, stored
+// rows 2 (i % 4) + 0..1) of matrix m in register m.
+MOE_DEV void ldmatrix_x4_trans(uint32_t smem_addr, uint32_t& r0, uint32_t& r1, uint32_t& r2, uint32_t& r3) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r0), "=r"(r1), "=r"(r2), "=r"(r3)
+               : "r"(smem_addr)
+               : "memory");
+}
+
 MOE_DEV void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 
 // 32 lanes x 32 consecutive 32-bit columns to tensor memory: thread i of the
@@ -432,6 +471,11 @@ MOE_DEV uint32_t pack_bf16x2(float lo, float hi) {
 }
 
 MOE_DEV float silu_f32(float g) { return g / (1.0f + __expf(-g)); }
+
+// sigma(g) = 1 / (1 + e^-g) by the hardware exponential and division; 0 where
+// e^-g overflows.
+MOE_DEV float sigmoid_fast(float g) { return __fdividef(1.0f, 1.0f + __expf(-g)); }
+MOE_DEV float2 unpack_bf16x2(uint32_t v) { return __bfloat1622float2(*reinterpret_cast<__nv_bfloat162*>(&v)); }
 
 // silu(g) = g sigma(g) with sigma(g) = (1 + tanh(g / 2)) / 2 from the
 // hardware tanh approximation (one special-function op). tanh.approx has a

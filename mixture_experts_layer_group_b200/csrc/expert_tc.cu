@@ -103,10 +103,15 @@ constexpr int kASlotCols = 2 * kBK / 2;           // FP8: columns of one slot (t
 // memory (three slots, columns 320..511), from which the pair MMAs take A
 // (B, the token box, stays in the ring); the accumulators share columns
 // 0..319, so a unit covers at most 160 tokens.
-template <bool FP8>
+//
+// A wide plan (bf16 weights) gives every epilogue warp three transpose tiles
+// instead of one, out of the ring: the training forward stores g, u and h of
+// a block, the backward's first GEMM reads g and u and stores their gradients
+// and gate * h.
+template <bool FP8, bool WIDE = false>
 struct Plan;
 template <>
-struct Plan<false> {
+struct Plan<false, false> {
   static constexpr int kEpiWarps = 8;            // two per TMEM lane quadrant
   static constexpr int kCvtWarps = 4;            // (no converters; 4 keeps the arithmetic defined)
   static constexpr int kThreads = 64 + 32 * kEpiWarps;
@@ -116,9 +121,15 @@ struct Plan<false> {
   static constexpr int kTokAlign = 16;           // MMA N granule
   static constexpr uint32_t kAccCols = 512;      // accumulator columns: two buffers of 256
   static constexpr int kBarrierBytes = 512;
+  static constexpr int kTiles = 1;               // transpose tiles per epilogue warp
 };
 template <>
-struct Plan<true> {
+struct Plan<false, true> : Plan<false, false> {
+  static constexpr int kRingBytes = 44 * 4096;   // 176 KB
+  static constexpr int kTiles = 3;
+};
+template <>
+struct Plan<true, false> {
   static constexpr int kEpiWarps = 4;            // one per TMEM lane quadrant
   static constexpr int kCvtWarps = 8;            // two per TMEM lane quadrant: one per weight half
   static constexpr int kThreads = 64 + 32 * (kEpiWarps + kCvtWarps);
@@ -128,17 +139,20 @@ struct Plan<true> {
   static constexpr int kTokAlign = 32;           // N of an MMA with A in tensor memory
   static constexpr uint32_t kAccCols = 320;      // two buffers of 160; then the weight slots
   static constexpr int kBarrierBytes = 1024;
+  static constexpr int kTiles = 1;
 };
-template <bool FP8>
+template <class PL>
 __host__ __device__ constexpr int tile_bytes() {
-  return Plan<FP8>::kEpiWarps * kTileBytes;  // one transpose tile per epilogue warp
+  return PL::kEpiWarps * PL::kTiles * kTileBytes;
 }
-template <bool FP8>
+template <class PL>
 constexpr int smem_bytes() {
-  return Plan<FP8>::kRingBytes + tile_bytes<FP8>() + 1024 + Plan<FP8>::kBarrierBytes;
+  return PL::kRingBytes + tile_bytes<PL>() + 1024 + PL::kBarrierBytes;
 }
-static_assert(smem_bytes<false>() <= 232448 && smem_bytes<true>() <= 232448, "shared memory budget");
-static_assert(kMaxStageBytes * 3 <= Plan<false>::kRingBytes, "ring holds three full stages");
+static_assert(smem_bytes<Plan<false>>() <= 232448 && smem_bytes<Plan<true>>() <= 232448 &&
+                  smem_bytes<Plan<false, true>>() <= 232448,
+              "shared memory budget");
+static_assert(kMaxStageBytes * 3 <= Plan<false, true>::kRingBytes, "ring holds three full stages");
 static_assert((kA8Bytes + kMaxTokBytes) * 4 <= Plan<true>::kRingBytes, "FP8 ring holds four full stages");
 static_assert(Plan<false>::kEpiWarps % 4 == 0 && Plan<true>::kEpiWarps % 4 == 0, "whole quadrants");
 static_assert(Plan<true>::kCvtWarps == 8, "one converter warp per (TMEM lane quadrant, weight half)");
@@ -150,7 +164,12 @@ static_assert(kMaxTok % (2 * kTokBox) == 0 && Plan<false>::kChunk <= kMaxTok && 
                   Plan<true>::kChunk % Plan<true>::kTokAlign == 0,
               "token chunk");
 
-enum Mode : int { kSwiGLU = 0, kGateDown = 1 };
+// The forward's two GEMMs, the SwiGLU GEMM that also keeps g and u, and the
+// backward's two products on the weights (see BwdParams).
+enum Mode : int { kSwiGLU = 0, kGateDown = 1, kSwiGLUKeep = 2, kDh = 3, kDx = 4 };
+__host__ __device__ constexpr bool is_swiglu(int mode) { return mode == kSwiGLU || mode == kSwiGLUKeep; }
+__host__ __device__ constexpr bool is_bwd(int mode) { return mode == kDh || mode == kDx; }
+__host__ __device__ constexpr bool is_wide(int mode) { return mode == kSwiGLUKeep || mode == kDh; }
 
 struct TcParams {
   // bf16 weights: bf16 maps of 64 x 128 boxes (128-byte swizzle; the down
@@ -193,6 +212,42 @@ struct TcParams {
   int64_t tok_rows_routed, tok_rows_shared;
   int64_t a_rows_routed, a_rows_shared;
   int64_t out_rows_routed, out_rows_shared;
+};
+
+// The training modes' further parameters.
+//   kSwiGLUKeep  o_g, o_u: g and u halves of gu [R, 2 F]
+//   kDh  q^T = W2^T dy^T: A = W2 [N, d, F] taken MN-major (M = 512 of the F
+//        features, K = d), B = dy; epilogue dg, du, gate h -> o_g, o_u,
+//        o_routed and the partial gate gradients
+//   kDx  dx^T = W1^T dg^T + W3^T du^T: A = W1 then W3 [N, F, d] MN-major
+//        (M = 512 of the d columns), B = dg then du; K = F twice
+// A is one 3-D map per weight tensor (columns, rows of one expert, expert),
+// so a box past the expert's last row or column loads zeros.
+struct BwdParams : TcParams {
+  CUtensorMap b1[kTokMaps];  // du (kDx)
+  CUtensorMap o_g, o_u;
+  __nv_bfloat16* out_g;      // row stride ld_g
+  __nv_bfloat16* out_u;
+  int64_t ld_g;
+  const __nv_bfloat16* gu;   // [R, 2 F] (kDh)
+  float* part;               // [ceil(F / 32), R] partial gate gradients, or null (kDh)
+  int segments;              // K segments of k_routed each (kDx: 2; 1 elsewhere)
+};
+template <int MODE>
+struct ParamsOf {
+  using type = TcParams;
+};
+template <>
+struct ParamsOf<kSwiGLUKeep> {
+  using type = BwdParams;
+};
+template <>
+struct ParamsOf<kDh> {
+  using type = BwdParams;
+};
+template <>
+struct ParamsOf<kDx> {
+  using type = BwdParams;
 };
 
 struct Unit {
@@ -347,6 +402,15 @@ MOE_DEV void dequant16(const uint4 w, int sb, uint32_t (&o)[8]) {
 
 MOE_DEV int load_volatile(const int* p) { return *reinterpret_cast<const volatile int*>(p); }
 
+constexpr int kMnBox = 64 * kBK * 2;  // 8 KB: 64 weight columns x 64 k
+
+// K blocks of a unit: one segment of `seg` blocks, or the backward's several.
+template <int MODE, class P>
+MOE_DEV int k_blocks(const P& p, int seg) {
+  if constexpr (MODE == kDx) return seg * p.segments;
+  else return seg;
+}
+
 // Writes one 64-byte token-row segment (32 bf16 from the transpose tile),
 // or the first ncols of it at a ragged right edge.
 MOE_DEV void store_row32(__nv_bfloat16* dst, int ncols, const uint4 (&v)[4]) {
@@ -363,10 +427,11 @@ MOE_DEV void store_row32(__nv_bfloat16* dst, int ncols, const uint4 (&v)[4]) {
 }
 
 template <int MODE, bool FP8>
-__global__ void __launch_bounds__(Plan<FP8>::kThreads, 1) expert_gemm_tc_kernel(const __grid_constant__ TcParams p) {
-  using PL = Plan<FP8>;
+__global__ void __launch_bounds__(Plan<FP8>::kThreads, 1)
+    expert_gemm_tc_kernel(const __grid_constant__ typename ParamsOf<MODE>::type p) {
+  using PL = Plan<FP8, is_wide(MODE)>;
   constexpr int kRingBytes = PL::kRingBytes;
-  constexpr int kEpiWarps = PL::kEpiWarps, kCvtWarps = PL::kCvtWarps, kTBytes = tile_bytes<FP8>();
+  constexpr int kEpiWarps = PL::kEpiWarps, kCvtWarps = PL::kCvtWarps, kTBytes = tile_bytes<PL>();
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   float* tiles = reinterpret_cast<float*>(smem + kRingBytes);
@@ -383,14 +448,14 @@ __global__ void __launch_bounds__(Plan<FP8>::kThreads, 1) expert_gemm_tc_kernel(
   // rows 256 r .. 256 r + 255 of the unit's 512 output columns, one
   // contiguous 256-row box whose first and second 128 rows are halves 0 and
   // 1; so TMEM lane l of half h in CTA r is output column 256 r + 128 h + l.
-  const int rank_rows = (MODE == kSwiGLU ? 128 : 256) * (int)rank;
+  const int rank_rows = (is_swiglu(MODE) ? 128 : 256) * (int)rank;
   // Readers of each unit id in each CTA (producer or MMA issuer, epilogue
   // leader, FP8 converter leader). The pair's cross-CTA signals are
   // asynchronous stores that complete transaction bytes on the other CTA's
   // barrier (st.async): a blocking cluster-scope mbarrier arrive costs the
   // signalling thread about 1000 cycles.
   constexpr int kRingReaders = FP8 ? 3 : 2;
-  const int half_cols = MODE == kSwiGLU ? 0 : 128;
+  const int half_cols = is_swiglu(MODE) ? 0 : 128;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kSlots; ++s) {
@@ -421,7 +486,7 @@ __global__ void __launch_bounds__(Plan<FP8>::kThreads, 1) expert_gemm_tc_kernel(
   if (warp == 0 && lane == 0) {
     tma_prefetch_desc(&p.a0_routed);
     for (int m = 0; m < kTokMaps; ++m) tma_prefetch_desc(&p.b_routed[m]);
-    if (MODE == kSwiGLU) tma_prefetch_desc(&p.a1_routed);
+    if (is_swiglu(MODE) || MODE == kDx) tma_prefetch_desc(&p.a1_routed);
   }
   if (warp == 1) {
     tmem_alloc_pair(&sh.tmem_base, kTmemCols);
@@ -511,13 +576,14 @@ __global__ void __launch_bounds__(Plan<FP8>::kThreads, 1) expert_gemm_tc_kernel(
         if (u < 0) {
           // no units left for this CTA: the down GEMM may start on SMs as
           // they free up
-          if (MODE == kSwiGLU) griddep_launch_dependents();
+          if (is_swiglu(MODE)) griddep_launch_dependents();
           break;
         }
         const Unit un = decode_unit(p, u);
         const bool shared = un.g == p.N;
         const int K = shared ? p.k_shared : p.k_routed;
-        const int nk = (K + kBK - 1) / kBK;
+        const int seg = (K + kBK - 1) / kBK;  // K blocks of a segment
+        const int nk = k_blocks<MODE>(p, seg);
         const int half_n = mma_n<FP8>(un.ntok) / 2;  // token rows per CTA
         // one token box per stage, the smallest of 32 / 64 / 128 rows that
         // covers this CTA's rows (the TMA engine's cost is per box, so a
@@ -525,7 +591,8 @@ __global__ void __launch_bounds__(Plan<FP8>::kThreads, 1) expert_gemm_tc_kernel(
         const int tmap = half_n <= kTokBox ? 0 : (half_n <= 2 * kTokBox ? 1 : 2);
         const int nbox = 1 << tmap;  // in 32-row granules
         const uint32_t tx = PL::kABytes + nbox * kBoxBytes;
-        const int rowA = (shared ? 0 : un.g * p.a_rows_per_expert) + un.f * p.tile_cols + rank_rows;
+        // weight row (backward: first column of the expert's matrix)
+        const int rowA = (shared || is_bwd(MODE) ? 0 : un.g * p.a_rows_per_expert) + un.f * p.tile_cols + rank_rows;
         const int rowB = __ldg(p.grp_row0 + un.g) + un.tok0 + (int)rank * half_n;
         // the unit's rows lie inside the group and its tensors (TMA clips a
         // box that reaches past them, and the last column tile of a matrix
@@ -536,7 +603,7 @@ __global__ void __launch_bounds__(Plan<FP8>::kThreads, 1) expert_gemm_tc_kernel(
                                 rowA >= 0 && rowA < (shared ? p.a_rows_shared : p.a_rows_routed) + p.tile_cols,
                             p.status);
         const CUtensorMap* ta0 = shared ? &p.a0_shared : &p.a0_routed;
-        const CUtensorMap* ta1 = MODE == kSwiGLU ? (shared ? &p.a1_shared : &p.a1_routed) : ta0;
+        const CUtensorMap* ta1 = is_swiglu(MODE) ? (shared ? &p.a1_shared : &p.a1_routed) : ta0;
         const CUtensorMap* tb = shared ? &p.b_shared[tmap] : &p.b_routed[tmap];
         const uint64_t pol = un.nchunks == 1 ? pol_once : pol_last;
         for (int kc = 0; kc < nk; ++kc, ++fills) {
@@ -562,8 +629,19 @@ __global__ void __launch_bounds__(Plan<FP8>::kThreads, 1) expert_gemm_tc_kernel(
           } else {
             const uint32_t full_bar = in_first(&sh.full[s]);
             if (first) mbar_arrive_expect_tx(&sh.full[s], 2 * tx);  // this CTA's bytes and the peer's
+            if constexpr (is_bwd(MODE)) {
+              // 256 weight columns x 64 k as four 64 x 64 boxes (8 KB each, k-major rows of 128 bytes)
+              const bool second = MODE == kDx && kc >= seg;
+              const int k0 = (second ? kc - seg : kc) * kBK;
+              const CUtensorMap* ta = second ? &p.a1_routed : ta0;
+#pragma unroll
+              for (int c = 0; c < 4; ++c)
+                tma_load_3d_pair(a_dst + c * kMnBox, ta, full_bar, rowA + 64 * c, k0, un.g, pol);
+              tma_load_2d_pair(b_dst, second ? &p.b1[tmap] : tb, full_bar, k0, rowB, pol_last);
+              continue;
+            }
             tma_load_2d_pair(a_dst, ta0, full_bar, kc * kBK, rowA, pol);  // SwiGLU: 128 W1 rows; down: 256 rows
-            if (MODE == kSwiGLU) tma_load_2d_pair(a_dst + kHalfBytes, ta1, full_bar, kc * kBK, rowA, pol);
+            if (is_swiglu(MODE)) tma_load_2d_pair(a_dst + kHalfBytes, ta1, full_bar, kc * kBK, rowA, pol);
             tma_load_2d_pair(b_dst, tb, full_bar, kc * kBK, rowB, pol_last);
           }
         }
@@ -593,9 +671,9 @@ __global__ void __launch_bounds__(Plan<FP8>::kThreads, 1) expert_gemm_tc_kernel(
         if (u < 0) break;
         const Unit un = decode_unit(p, u);
         const int K = un.g == p.N ? p.k_shared : p.k_routed;
-        const int nk = (K + kBK - 1) / kBK;
+        const int nk = k_blocks<MODE>(p, (K + kBK - 1) / kBK);
         const int n = mma_n<FP8>(un.ntok);
-        const uint32_t idesc = idesc_bf16_f32(256, (uint32_t)n);
+        const uint32_t idesc = idesc_bf16_f32(256, (uint32_t)n) | (is_bwd(MODE) ? kIdescAMn : 0u);
         uint32_t mask, base, stride;
         plan.place(n, mask, base, stride);
         (void)MOE_IN_BOUNDS(n <= p.chunk_rows + PL::kTokAlign && base + stride + n <= PL::kAccCols, p.status);
@@ -631,6 +709,14 @@ __global__ void __launch_bounds__(Plan<FP8>::kThreads, 1) expert_gemm_tc_kernel(
               const uint64_t bdesc = smem_desc_sw128(b_addr + kk * 32);
               umma_bf16_pair_ts(d0, a_t + kk * 8, bdesc, idesc, (kc | kk) != 0);
               umma_bf16_pair_ts(d1, a_t + kBK / 2 + kk * 8, bdesc, idesc, (kc | kk) != 0);
+            }
+          } else if (is_bwd(MODE)) {
+#pragma unroll
+            for (int kk = 0; kk < kBK / 16; ++kk) {
+              const uint64_t bdesc = smem_desc_sw128(b_addr + kk * 32);
+              umma_bf16_pair(d0, smem_desc_sw128_mn(stage_addr + kk * 2048, kMnBox), bdesc, idesc, (kc | kk) != 0);
+              umma_bf16_pair(d1, smem_desc_sw128_mn(stage_addr + kHalfBytes + kk * 2048, kMnBox), bdesc, idesc,
+                             (kc | kk) != 0);
             }
           } else {
 #pragma unroll
@@ -668,7 +754,8 @@ __global__ void __launch_bounds__(Plan<FP8>::kThreads, 1) expert_gemm_tc_kernel(
     const int q = warp & 3;                  // TMEM lane quadrant this warp may access
     const int ew = warp - 2;                 // epilogue warp: its transpose tile
     const int sub = ew >> 2;                 // which of the quadrant's warps
-    __nv_bfloat16* tile = reinterpret_cast<__nv_bfloat16*>(reinterpret_cast<uint8_t*>(tiles) + ew * kTileBytes);
+    __nv_bfloat16* tile =
+        reinterpret_cast<__nv_bfloat16*>(reinterpret_cast<uint8_t*>(tiles) + ew * PL::kTiles * kTileBytes);
     const bool leader = threadIdx.x == 64;
     uint32_t uses[2] = {0u, 0u};
     AccPlan<PL::kAccCols> plan;
@@ -723,7 +810,7 @@ __global__ void __launch_bounds__(Plan<FP8>::kThreads, 1) expert_gemm_tc_kernel(
       const int64_t ld = shared ? p.ld_shared : p.ld_routed;
       const int cols = shared ? p.cols_shared : p.cols_routed;
       const uint32_t t_q = tmem_base + ((uint32_t)(q * 32) << 16) + base;
-      constexpr int kHalves = MODE == kSwiGLU ? 1 : 2;
+      constexpr int kHalves = is_swiglu(MODE) ? 1 : 2;
 #pragma unroll 1
       for (int hh = 0; hh < kHalves; ++hh) {
         // this warp's 32 output columns of the unit
@@ -734,7 +821,7 @@ __global__ void __launch_bounds__(Plan<FP8>::kThreads, 1) expert_gemm_tc_kernel(
           const int64_t row = row_base + tok;
           // gate of this lane's token, spread to the lanes that hold it below
           float my_gate = 1.0f;
-          if (MODE == kGateDown && !shared && p.gate_perm && tok < un.ntok &&
+          if ((MODE == kGateDown || MODE == kDh) && !shared && p.gate_perm && tok < un.ntok &&
               MOE_IN_BOUNDS(row < p.tok_rows_routed, p.status))
             my_gate = __ldg(p.gate_perm + row);
           // The block (32 features = this quadrant's TMEM lanes, x 32 tokens =
@@ -742,12 +829,59 @@ __global__ void __launch_bounds__(Plan<FP8>::kThreads, 1) expert_gemm_tc_kernel(
           // group r give this thread features 16 hf + 8 e + lane / 4 (e = 0, 1)
           // and tokens 8 r + 2 (lane % 4) + 0..1, packed as bf16 pairs.
           uint32_t pk[2][4][2];
+          uint32_t pg[2][4][2], pu[2][4][2];  // training: g and u (keep), or dg and du
           const int tq = 2 * (lane & 3);
+          const uint32_t tile_addr = smem_u32(tile);
+          // the shared-memory address of this lane's row for the transposing
+          // matrix moves: matrix m of (hf, rp) is column group r = 2 rp + m / 2
+          // and feature octet e = m % 2
+          auto mat_addr = [&](int i, int hf, int rp) {
+            const int m = lane >> 3, k = lane & 7;
+            const int t = 8 * (2 * rp + (m >> 1)) + k;  // token row this lane addresses
+            const int c = 2 * hf + (m & 1);             // feature chunk
+            return tile_addr + i * kTileBytes + t * 64 + ((c ^ ((t >> 1) & 3)) << 4);
+          };
+          if constexpr (MODE == kDh) {
+            // g and u of the block into tiles 0 and 1 (coalesced 16-byte loads,
+            // the tile's swizzle), then into the accumulator's layout
+            uint4 v[2][4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int t = 8 * i + (lane >> 2), c = c0 + 8 * (lane & 3);
+              const bool in = j0 + t < un.ntok && c < cols;  // 8 columns are all in or all out
+              const __nv_bfloat16* src = p.gu + (row_base + j0 + t) * 2 * cols + c;
+              v[0][i] = in ? __ldg(reinterpret_cast<const uint4*>(src)) : make_uint4(0, 0, 0, 0);
+              v[1][i] = in ? __ldg(reinterpret_cast<const uint4*>(src + cols)) : make_uint4(0, 0, 0, 0);
+            }
+            if (lane == 0) bulk_wait_group_read<0>();  // the previous block's stores have read the tiles
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int t = 8 * i + (lane >> 2);
+              const uint32_t at = tile_addr + t * 64 + (((lane & 3) ^ ((t >> 1) & 3)) << 4);
+              st_shared_v4(at, v[0][i]);
+              st_shared_v4(at + kTileBytes, v[1][i]);
+            }
+            __syncwarp();
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+              for (int rp = 0; rp < 2; ++rp) {
+                ldmatrix_x4_trans(mat_addr(0, hf, rp), pg[hf][2 * rp][0], pg[hf][2 * rp][1], pg[hf][2 * rp + 1][0],
+                                  pg[hf][2 * rp + 1][1]);
+                ldmatrix_x4_trans(mat_addr(1, hf, rp), pu[hf][2 * rp][0], pu[hf][2 * rp][1], pu[hf][2 * rp + 1][0],
+                                  pu[hf][2 * rp + 1][1]);
+              }
+            __syncwarp();
+          }
+          float dgate[4][2];  // kDh: sum over this lane's features of q h, per token
+#pragma unroll
+          for (int r = 0; r < 4; ++r) dgate[r][0] = dgate[r][1] = 0.f;
 #pragma unroll
           for (int hf = 0; hf < 2; ++hf) {
             uint32_t a[16];
             tmem_ld16x256b_x4(t_q + ((uint32_t)(16 * hf) << 16) + hh * stride + j0, a);
-            if (MODE == kSwiGLU) {
+            if (is_swiglu(MODE)) {
               uint32_t b[16];
               tmem_ld16x256b_x4(t_q + ((uint32_t)(16 * hf) << 16) + stride + j0, b);  // u of the same features
               tmem_wait_ld();
@@ -756,9 +890,42 @@ __global__ void __launch_bounds__(Plan<FP8>::kThreads, 1) expert_gemm_tc_kernel(
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                   const int x = 4 * r + 2 * e;
-                  pk[hf][r][e] = pack_bf16x2(silu_tanh(__uint_as_float(a[x])) * __uint_as_float(b[x]),
-                                             silu_tanh(__uint_as_float(a[x + 1])) * __uint_as_float(b[x + 1]));
+                  const float g0 = __uint_as_float(a[x]), g1 = __uint_as_float(a[x + 1]);
+                  const float u0 = __uint_as_float(b[x]), u1 = __uint_as_float(b[x + 1]);
+                  if (MODE == kSwiGLUKeep) {
+                    pg[hf][r][e] = pack_bf16x2(g0, g1);
+                    pu[hf][r][e] = pack_bf16x2(u0, u1);
+                    pk[hf][r][e] = pack_bf16x2(g0 * sigmoid_fast(g0) * u0, g1 * sigmoid_fast(g1) * u1);
+                  } else {
+                    pk[hf][r][e] = pack_bf16x2(silu_tanh(g0) * u0, silu_tanh(g1) * u1);
+                  }
                 }
+            } else if (MODE == kDh) {
+              tmem_wait_ld();
+#pragma unroll
+              for (int r = 0; r < 4; ++r) {
+                const float w0 = __shfl_sync(0xffffffffu, my_gate, 8 * r + tq);
+                const float w1 = __shfl_sync(0xffffffffu, my_gate, 8 * r + tq + 1);
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                  const int x = 4 * r + 2 * e;
+                  const float q[2] = {__uint_as_float(a[x]), __uint_as_float(a[x + 1])};
+                  const float2 g2 = unpack_bf16x2(pg[hf][r][e]), u2 = unpack_bf16x2(pu[hf][r][e]);
+                  const float gv[2] = {g2.x, g2.y}, uv[2] = {u2.x, u2.y}, gate[2] = {w0, w1};
+                  float og[2], ou[2], oh[2];
+#pragma unroll
+                  for (int z = 0; z < 2; ++z) {
+                    const float sg = sigmoid_fast(gv[z]), act = gv[z] * sg, h = act * uv[z], dh = gate[z] * q[z];
+                    dgate[r][z] = fmaf(q[z], h, dgate[r][z]);
+                    ou[z] = dh * act;
+                    og[z] = dh * uv[z] * fmaf(sg, gv[z] - act, sg);  // sg (1 + g (1 - sg))
+                    oh[z] = gate[z] * h;
+                  }
+                  pg[hf][r][e] = pack_bf16x2(og[0], og[1]);
+                  pu[hf][r][e] = pack_bf16x2(ou[0], ou[1]);
+                  pk[hf][r][e] = pack_bf16x2(oh[0], oh[1]);
+                }
+              }
             } else {
               tmem_wait_ld();
 #pragma unroll
@@ -773,24 +940,43 @@ __global__ void __launch_bounds__(Plan<FP8>::kThreads, 1) expert_gemm_tc_kernel(
               }
             }
           }
+          if constexpr (MODE == kDh) {
+            if (p.part && c0 < cols) {  // the block's 32 features of each token, in a fixed order
+#pragma unroll
+              for (int r = 0; r < 4; ++r)
+#pragma unroll
+                for (int z = 0; z < 2; ++z) {
+                  float v = dgate[r][z];
+                  v += __shfl_xor_sync(0xffffffffu, v, 4);
+                  v += __shfl_xor_sync(0xffffffffu, v, 8);
+                  v += __shfl_xor_sync(0xffffffffu, v, 16);
+                  const int t = j0 + 8 * r + tq + z;
+                  if (lane < 4 && t < un.ntok &&
+                      MOE_IN_BOUNDS(row_base + t < p.tok_rows_routed, p.status))
+                    p.part[(int64_t)(c0 >> 5) * p.tok_rows_routed + row_base + t] = v;
+                }
+            }
+          }
           // Transpose into this warp's [32 tokens][32 features] tile, 64-byte
           // swizzled (16-byte chunk c of token row t sits at chunk c ^ ((t >> 1) & 3)),
           // with four transposing matrix stores: matrix m of store (hf, rp) is
           // column group r = 2 rp + m / 2 and feature octet e = m % 2.
-          if (lane == 0) bulk_wait_group_read<0>();  // the previous block's store has read the tile
-          __syncwarp();
-          const uint32_t tile_addr = smem_u32(tile);
-          {
-            const int m = lane >> 3, k = lane & 7;
+          if (MODE != kDh) {
+            if (lane == 0) bulk_wait_group_read<0>();  // the previous block's store has read the tile
+            __syncwarp();
+          }
+          auto put = [&](int i, const uint32_t (&v)[2][4][2]) {
 #pragma unroll
             for (int hf = 0; hf < 2; ++hf)
 #pragma unroll
-              for (int rp = 0; rp < 2; ++rp) {
-                const int t = 8 * (2 * rp + (m >> 1)) + k;  // token row this lane addresses
-                const int c = 2 * hf + (m & 1);             // feature chunk
-                stmatrix_x4_trans(tile_addr + t * 64 + ((c ^ ((t >> 1) & 3)) << 4), pk[hf][2 * rp][0],
-                                  pk[hf][2 * rp][1], pk[hf][2 * rp + 1][0], pk[hf][2 * rp + 1][1]);
-              }
+              for (int rp = 0; rp < 2; ++rp)
+                stmatrix_x4_trans(mat_addr(i, hf, rp), v[hf][2 * rp][0], v[hf][2 * rp][1], v[hf][2 * rp + 1][0],
+                                  v[hf][2 * rp + 1][1]);
+          };
+          put(0, pk);
+          if constexpr (is_wide(MODE)) {
+            put(1, pg);
+            put(2, pu);
           }
           const bool full_block = j0 + 32 <= un.ntok && c0 + 32 <= cols;
           if (full_block) {
@@ -800,20 +986,31 @@ __global__ void __launch_bounds__(Plan<FP8>::kThreads, 1) expert_gemm_tc_kernel(
               (void)MOE_IN_BOUNDS(row_base + j0 < (shared ? p.out_rows_shared : p.out_rows_routed), p.status);
               tma_store_2d(shared ? &p.o_shared : &p.o_routed, tile, c0,
                            (int)(row_base + j0) + (shared ? p.out_row0_shared : 0));
+              if constexpr (is_wide(MODE)) {
+                tma_store_2d(&p.o_g, tile + kTileBytes / 2, c0, (int)(row_base + j0));
+                tma_store_2d(&p.o_u, tile + kTileBytes, c0, (int)(row_base + j0));
+              }
               bulk_commit_group();
             }
           } else {
             __syncwarp();
-            uint4 rowv[4];
+            auto store_row = [&](int i, __nv_bfloat16* base, int64_t row_len) {
+              uint4 rowv[4];
 #pragma unroll
-            for (int c = 0; c < 4; ++c)
-              rowv[c] = *reinterpret_cast<const uint4*>(reinterpret_cast<const uint8_t*>(tile) + lane * 64 +
-                                                        ((c ^ ((lane >> 1) & 3)) << 4));
-            // (columns at or past the matrix's width belong to a tile that
-            // reaches past it: nothing to store)
-            if (tok < un.ntok && c0 < cols &&
-                MOE_IN_BOUNDS(row < (shared ? p.out_rows_shared : p.out_rows_routed), p.status))
-              store_row32(out_base + row * ld + c0, cols - c0, rowv);
+              for (int c = 0; c < 4; ++c)
+                rowv[c] = *reinterpret_cast<const uint4*>(reinterpret_cast<const uint8_t*>(tile) + i * kTileBytes +
+                                                          lane * 64 + ((c ^ ((lane >> 1) & 3)) << 4));
+              // (columns at or past the matrix's width belong to a tile that
+              // reaches past it: nothing to store)
+              if (tok < un.ntok && c0 < cols &&
+                  MOE_IN_BOUNDS(row < (shared ? p.out_rows_shared : p.out_rows_routed), p.status))
+                store_row32(base + row * row_len + c0, cols - c0, rowv);
+            };
+            store_row(0, out_base, ld);
+            if constexpr (is_wide(MODE)) {
+              store_row(1, p.out_g, p.ld_g);
+              store_row(2, p.out_u, p.ld_g);
+            }
           }
         }
       }
@@ -971,6 +1168,21 @@ bool make_store_tmap(CUtensorMap* m, const void* base, uint64_t rows, uint64_t c
   return make_tmap_bf16_swz(m, base, rows, cols, 32, 32, 64);
 }
 
+// The same for one half (g or u) of gu [rows, 2 cols].
+bool make_half_tmap(CUtensorMap* m, const void* gu, int64_t rows, int cols, int half) {
+  const uint64_t dims[2] = {(uint64_t)cols, (uint64_t)rows}, stride[1] = {(uint64_t)cols * 4};
+  const uint32_t box[2] = {32, 32};
+  return make_tmap_nd(m, static_cast<const uint8_t*>(gu) + (int64_t)half * cols * 2, 2, 2, dims, stride, box, 64, false);
+}
+
+// A weight tensor [N, rows, cols] for the backward: boxes of 64 columns x 64
+// rows of one expert.
+bool make_weight_tmap(CUtensorMap* m, const void* base, uint64_t n, uint64_t rows, uint64_t cols) {
+  const uint64_t dims[3] = {cols, rows, n}, stride[2] = {cols * 2, rows * cols * 2};
+  const uint32_t box[3] = {64, (uint32_t)kBK, 1};
+  return make_tmap_nd(m, base, 2, 3, dims, stride, box, 128, true);
+}
+
 // FP8 weight codes: 64 bytes x box_rows rows, 64-byte swizzle (each
 // converter thread reads one row; a warp's 32 rows then cover all banks).
 bool make_tmap_codes(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols, uint32_t box_rows) {
@@ -978,7 +1190,7 @@ bool make_tmap_codes(CUtensorMap* m, const void* base, uint64_t rows, uint64_t c
 }
 
 template <int MODE, bool FP8>
-cudaError_t launch_one(const TcParams& prm, int max_units, cudaStream_t s, bool programmatic) {
+cudaError_t launch_one(const typename ParamsOf<MODE>::type& prm, int max_units, cudaStream_t s, bool programmatic) {
   // per device: the shared-memory opt-in done and the resident cluster count
   static std::mutex mu;
   static int max_clusters_of[kMaxDevices] = {};
@@ -995,7 +1207,7 @@ cudaError_t launch_one(const TcParams& prm, int max_units, cudaStream_t s, bool 
   attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.blockDim = dim3(Plan<FP8>::kThreads, 1, 1);
-  cfg.dynamicSmemBytes = smem_bytes<FP8>();
+  cfg.dynamicSmemBytes = (smem_bytes<Plan<FP8, is_wide(MODE)>>());
   cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
@@ -1004,7 +1216,7 @@ cudaError_t launch_one(const TcParams& prm, int max_units, cudaStream_t s, bool 
     std::lock_guard<std::mutex> lock(mu);
     if (max_clusters_of[dev] == 0) {
       cudaError_t e = cudaFuncSetAttribute(expert_gemm_tc_kernel<MODE, FP8>,
-                                           cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes<FP8>());
+                                           cudaFuncAttributeMaxDynamicSharedMemorySize, (smem_bytes<Plan<FP8, is_wide(MODE)>>()));
       if (e != cudaSuccess) return e;
       cfg.gridDim = dim3(2 * (device_sm_count() / 2), 1, 1);
       int n = 0;
@@ -1035,7 +1247,8 @@ cudaError_t launch_expert_gemms_tc(const Problem& p, const GemmArgs& a, cudaStre
   auto wmap = [&](CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols, uint32_t box_rows) {
     return fp8 ? make_tmap_codes(m, base, rows, cols, box_rows) : make_tmap(m, base, rows, cols, box_rows);
   };
-  TcParams g1{};
+  BwdParams gk{};  // the training forward's further stores
+  TcParams& g1 = gk;
   bool ok = wmap(&g1.a0_routed, a.W1, (uint64_t)p.N * p.F, p.d, 128) &&
             wmap(&g1.a1_routed, a.W3, (uint64_t)p.N * p.F, p.d, 128) &&
             wmap(&g1.a0_shared, a.Ws1, (uint64_t)p.nsF, p.d, 128) &&
@@ -1079,7 +1292,17 @@ cudaError_t launch_expert_gemms_tc(const Problem& p, const GemmArgs& a, cudaStre
   const int64_t max_cols1 = p.F > p.nsF ? p.F : p.nsF;
   const int64_t units1 = chunks_bound * ((max_cols1 + kTcBN1 - 1) / kTcBN1);
   const int grid1 = (int)(units1 < sms ? units1 : sms);
-  cudaError_t err = fp8 ? launch_one<kSwiGLU, true>(g1, grid1, s, false) : launch_one<kSwiGLU, false>(g1, grid1, s, false);
+  cudaError_t err;
+  if (a.gu) {
+    if (!make_half_tmap(&gk.o_g, a.gu, p.R, p.F, 0) || !make_half_tmap(&gk.o_u, a.gu, p.R, p.F, 1))
+      return cudaErrorInvalidValue;
+    gk.out_g = (__nv_bfloat16*)a.gu;
+    gk.out_u = gk.out_g + p.F;
+    gk.ld_g = 2 * (int64_t)p.F;
+    err = launch_one<kSwiGLUKeep, false>(gk, grid1, s, false);
+  } else {
+    err = fp8 ? launch_one<kSwiGLU, true>(g1, grid1, s, false) : launch_one<kSwiGLU, false>(g1, grid1, s, false);
+  }
   if (err == cudaSuccess && between) err = cudaEventRecord(between, s);
   if (err != cudaSuccess) return err;
 
@@ -1125,6 +1348,145 @@ cudaError_t launch_expert_gemms_tc(const Problem& p, const GemmArgs& a, cudaStre
   // the down GEMM overlaps the SwiGLU GEMM's drain unless an event must be
   // recorded between the two
   return fp8 ? launch_one<kGateDown, true>(g2, grid2, s, !between) : launch_one<kGateDown, false>(g2, grid2, s, !between);
+}
+
+int dgate_planes(const Problem& p) { return p.dtype == MOE_BF16 ? (p.F + 31) / 32 : (p.F + kSimtBN - 1) / kSimtBN; }
+
+cudaError_t launch_experts_backward_tc(const Problem& p, const ExpertsBwdArgs& a, cudaStream_t s) {
+  const int sms = device_sm_count();
+  cudaError_t err = cudaMemsetAsync(a.sched, 0, 4 * sizeof(int), s);
+  if (err != cudaSuccess) return err;
+  constexpr int cm = Plan<false>::kChunk;
+  const int64_t chunks_bound = (p.R + cm - 1) / cm + p.N;
+  auto grid_of = [&](int cols) {
+    const int64_t units = chunks_bound * ((cols + kTcBN2 - 1) / kTcBN2);
+    return (int)(units < sms ? units : sms);
+  };
+
+  BwdParams h{};
+  bool ok = make_weight_tmap(&h.a0_routed, a.W2, p.N, p.d, p.F) && make_token_tmaps(h.b_routed, a.dy_rows, p.R, p.d) &&
+            make_store_tmap(&h.o_routed, a.gh, p.R, p.F) && make_store_tmap(&h.o_g, a.dg, p.R, p.F) &&
+            make_store_tmap(&h.o_u, a.du, p.R, p.F);
+  if (!ok) return cudaErrorInvalidValue;
+  h.unit_base = a.unit_base1;
+  h.grp_row0 = a.grp_row0;
+  h.grp_rows = a.grp_rows;
+  h.sched = a.sched;
+  h.N = p.N;
+  h.k_routed = p.d;
+  h.cols_routed = p.F;
+  h.tile_cols = kTcBN2;
+  h.out_routed = (__nv_bfloat16*)a.gh;
+  h.ld_routed = p.F;
+  h.out_g = (__nv_bfloat16*)a.dg;
+  h.out_u = (__nv_bfloat16*)a.du;
+  h.ld_g = p.F;
+  h.gate_perm = a.gate_rows;
+  h.status = a.status;
+  h.chunk_rows = cm;
+  h.tok_rows_routed = h.out_rows_routed = p.R;
+  h.a_rows_routed = p.F;
+  h.gu = (const __nv_bfloat16*)a.gu;
+  h.part = a.dgate_rows ? a.dgate_part : nullptr;
+  h.segments = 1;
+  err = launch_one<kDh, false>(h, grid_of(p.F), s, false);
+  if (err == cudaSuccess && a.dgate_rows) err = launch_dgate_reduce(a.dgate_part, dgate_planes(p), p.R, a.dgate_rows, s);
+  if (err != cudaSuccess) return err;
+
+  if (a.dx_rows) {
+    BwdParams x{};
+    ok = make_weight_tmap(&x.a0_routed, a.W1, p.N, p.F, p.d) && make_weight_tmap(&x.a1_routed, a.W3, p.N, p.F, p.d) &&
+         make_token_tmaps(x.b_routed, a.dg, p.R, p.F) && make_token_tmaps(x.b1, a.du, p.R, p.F) &&
+         make_store_tmap(&x.o_routed, a.dx_rows, p.R, p.d);
+    if (!ok) return cudaErrorInvalidValue;
+    x.unit_base = a.unit_base2;
+    x.grp_row0 = a.grp_row0;
+    x.grp_rows = a.grp_rows;
+    x.sched = a.sched + 1;
+    x.N = p.N;
+    x.k_routed = p.F;
+    x.cols_routed = p.d;
+    x.tile_cols = kTcBN2;
+    x.out_routed = (__nv_bfloat16*)a.dx_rows;
+    x.ld_routed = p.d;
+    x.status = a.status;
+    x.chunk_rows = cm;
+    x.tok_rows_routed = x.out_rows_routed = p.R;
+    x.a_rows_routed = p.d;
+    x.segments = 2;
+    err = launch_one<kDx, false>(x, grid_of(p.d), s, false);
+    if (err != cudaSuccess) return err;
+  }
+  if (!a.dW1) return cudaSuccess;
+  WgradArgs w{};
+  w.mat[0] = {{a.dg, nullptr}, a.x_rows, a.dW1, p.F, p.d, p.F};
+  w.mat[1] = {{a.du, nullptr}, a.x_rows, a.dW3, p.F, p.d, p.F};
+  w.mat[2] = {{a.dy_rows, nullptr}, a.gh, a.dW2, p.d, p.F, p.d};
+  w.nmat = 3;
+  w.groups = p.N;
+  w.segments = 1;
+  w.rows = p.R;
+  w.grp_row0 = a.grp_row0;
+  w.grp_rows = a.grp_rows;
+  w.grad_dtype = a.grad_dtype;
+  w.accumulate = a.accumulate;
+  w.status = a.status;
+  return launch_wgrad_tc(w, s);
+}
+
+// dx = (hi + lo) W_r as the two K segments of the dx GEMM over one group of T
+// rows (its "F" is N, its weights W_r twice), dW_r = (hi + lo)^T x as the two
+// segments of the weight-gradient kernel, the token ranges as its groups.
+cudaError_t launch_route_products_tc(const Problem& p, const RouteBwdArgs& a, cudaStream_t s) {
+  if (a.dx) {
+    cudaError_t err = cudaMemsetAsync(a.sched, 0, sizeof(int), s);
+    if (err != cudaSuccess) return err;
+    BwdParams x{};
+    bool ok = make_weight_tmap(&x.a0_routed, a.W_r, 1, p.N, p.d) && make_store_tmap(&x.o_routed, a.dx, p.T, p.d);
+    for (int i = 0; i < kTokMaps && ok; ++i) {
+      const uint64_t dims[2] = {(uint64_t)p.N, (uint64_t)p.T}, stride[1] = {(uint64_t)a.ld * 2};
+      const uint32_t box[2] = {(uint32_t)kBK, (uint32_t)(kTokBox << i)};
+      ok = make_tmap_nd(&x.b_routed[i], a.hi, 2, 2, dims, stride, box, 128, true) &&
+           make_tmap_nd(&x.b1[i], a.lo, 2, 2, dims, stride, box, 128, true);
+    }
+    if (!ok) return cudaErrorInvalidValue;
+    x.a1_routed = x.a0_routed;
+    x.unit_base = a.unit_base2;
+    x.grp_row0 = a.grp_row0;
+    x.grp_rows = a.grp_rows;
+    x.sched = a.sched;
+    x.N = 1;
+    x.k_routed = p.N;
+    x.cols_routed = p.d;
+    x.tile_cols = kTcBN2;
+    x.out_routed = (__nv_bfloat16*)a.dx;
+    x.ld_routed = p.d;
+    x.status = a.status;
+    x.chunk_rows = Plan<false>::kChunk;
+    x.tok_rows_routed = x.out_rows_routed = p.T;
+    x.a_rows_routed = p.d;
+    x.segments = 2;
+    const int64_t units = (p.T + kTcBM - 1) / kTcBM * ((p.d + kTcBN2 - 1) / kTcBN2);
+    const int sms = device_sm_count();
+    err = launch_one<kDx, false>(x, (int)(units < sms ? units : sms), s, false);
+    if (err != cudaSuccess) return err;
+  }
+  if (!a.dW_r) return cudaSuccess;
+  const bool split = a.splits > 1;
+  WgradArgs w{};
+  w.mat[0] = {{a.hi, a.lo}, a.x, split ? a.planes : a.dW_r, p.N, p.d, a.ld};
+  w.nmat = 1;
+  w.groups = a.splits;
+  w.segments = 2;
+  w.rows = p.T;
+  w.grp_row0 = a.split_row0;
+  w.grp_rows = a.split_rows;
+  w.grad_dtype = split ? (int)MOE_F32 : a.grad_dtype;
+  w.accumulate = !split && a.accumulate;
+  w.status = a.status;
+  const cudaError_t err = launch_wgrad_tc(w, s);
+  if (err != cudaSuccess || !split) return err;
+  return launch_join_planes(a.planes, a.splits, (int64_t)p.N * p.d, a.dW_r, a.grad_dtype, a.accumulate, s);
 }
 
 }  // namespace moe

@@ -5,6 +5,7 @@
 #include <cstddef>
 #include <cstdint>
 #include <cuda.h>
+#include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
 #include "../../include/moe_b200.h"
@@ -83,19 +84,26 @@ bool make_tmap_u8(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols
 bool make_tmap_bf16_swz(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols, uint32_t box_cols,
                         uint32_t box_rows, int swizzle_bytes);
 
+// bf16 (elem_bytes 2) or fp32 (4) tensor of rank 2 or 3, dims[0] contiguous,
+// row_bytes[i] the stride of dims[i + 1] in bytes, with a 64- or 128-byte
+// swizzled box; elements outside load as zero and are not stored. A null base
+// or an empty tensor gives a zeroed map that must not be used.
+bool make_tmap_nd(CUtensorMap* m, const void* base, int elem_bytes, int rank, const uint64_t* dims,
+                  const uint64_t* row_bytes, const uint32_t* box, int swizzle_bytes, bool promote);
+
 // Router: logits (FP32 pipes) then selection. The reduction over d is cut
 // into S contiguous K ranges (S = `splits`, or router_k_splits(p) when
 // splits is 0) whose partial logits land in S planes of [T, N] fp32 in
 // `logits` (logits_bytes must cover them) and are added in a fixed order.
 // A token's logits depend only on its own row, d and S, so every S gives
 // deterministic bits and equal S gives equal bits at any T. `status` (may be
-// null) receives MOE_DEV_* bits.
+// null) receives MOE_DEV_* bits; logits_out [T, N] (may be null) the logits.
 constexpr int kRouterTargetSms = 148;
 int router_k_splits(const Problem& p);
 size_t router_scratch_bytes(const Problem& p);
 cudaError_t launch_router(const Problem& p, const void* x, const void* W_r, const float* b,
                           float* logits, size_t logits_bytes, int32_t* idx, float* gates,
-                          unsigned* status, cudaStream_t s, int splits = 0);
+                          unsigned* status, cudaStream_t s, int splits = 0, float* logits_out = nullptr);
 
 // Histogram / scan / scatter; bm, bn1, bn2 select the GEMM tile grid that
 // the unit tables describe.
@@ -146,6 +154,8 @@ struct GemmArgs {
   const uint8_t* Ws1s = nullptr;
   const uint8_t* Ws3s = nullptr;
   const uint8_t* Ws2s = nullptr;
+  // training forward: the pre-activations [R, 2 F] (g, then u) are kept here
+  void* gu = nullptr;
 };
 
 // Tensor-core (bf16) expert GEMMs: SwiGLU projection then gated down
@@ -158,13 +168,143 @@ cudaError_t launch_expert_gemms_tc(const Problem& p, const GemmArgs& a, cudaStre
 cudaError_t launch_expert_gemms_simt(const Problem& p, const GemmArgs& a, cudaStream_t s,
                                      cudaEvent_t between);
 
+// Backward of the grouped experts (moe_experts_backward), after the unit
+// tables of its row tiles are in place. gu [R, 2 F] as the forward kept it;
+// dg, du, gh [R, F] and dgate_part [dgate_planes(p), R] are scratch: the
+// gradients of g and u, gate * h, and partial sums of the gate gradient.
+struct ExpertsBwdArgs {
+  const void* x_rows;      // [R, d]
+  const float* gate_rows;  // [R] or null (gate 1)
+  const void* W1;          // [N, F, d]
+  const void* W3;
+  const void* W2;          // [N, d, F]
+  const void* gu;
+  const void* dy_rows;     // [R, d]
+  void* dx_rows;           // [R, d] or null
+  float* dgate_rows;       // [R] or null
+  void* dW1;               // [N, F, d], or null (with dW3 and dW2)
+  void* dW3;
+  void* dW2;               // [N, d, F]
+  int grad_dtype;          // of dW1, dW3, dW2
+  bool accumulate;         // add to them (fp32 only)
+  void* dg;
+  void* du;
+  void* gh;
+  float* dgate_part;
+  const int32_t* grp_row0;
+  const int32_t* grp_rows;
+  const int32_t* unit_base1;
+  const int32_t* unit_base2;
+  unsigned* status;
+  int* sched;              // [4]
+};
+// Tensor-core weight gradients: for every group g and matrix i,
+// out[g][m][n] = sum over the group's rows r (and the segments s) of
+// A[s][r][m] B[r][n], bf16 operands, fp32 accumulation.
+struct WgradMatrix {
+  const void* A[2];  // [rows, M], row stride lda elements (a multiple of 8); one per segment
+  const void* B;     // [rows, N]
+  void* out;         // [groups, M, N]
+  int M, N;
+  int64_t lda;
+};
+struct WgradArgs {
+  WgradMatrix mat[3];
+  int nmat, groups, segments;
+  int64_t rows;
+  const int32_t* grp_row0;
+  const int32_t* grp_rows;
+  int grad_dtype;
+  bool accumulate;   // fp32 only
+  unsigned* status;
+};
+cudaError_t launch_wgrad_tc(const WgradArgs& a, cudaStream_t s);
+int dgate_planes(const Problem& p);
+cudaError_t launch_experts_backward_tc(const Problem& p, const ExpertsBwdArgs& a, cudaStream_t s);
+cudaError_t launch_experts_backward_simt(const Problem& p, const ExpertsBwdArgs& a, cudaStream_t s);
+// dgate[r] = sum over the planes of part[plane][r], in order.
+cudaError_t launch_dgate_reduce(const float* part, int planes, int64_t rows, float* dgate, cudaStream_t s);
+
+// The gradient of the logits (see route_bwd.cu) and the tables of the two
+// products that follow.
+struct RouteDzArgs {
+  const float* logits;      // [T, N]
+  const int32_t* idx;       // [T, k]
+  const float* dgates;      // [T, k], or by permuted row with slot_pos
+  const int32_t* slot_pos;  // [T, k] or null
+  int64_t T;
+  int N, k, score_fn, normalize;
+  float route_scale;
+  unsigned* status;
+  float* dz;                // [T, N] fp32, or null: hi and lo instead
+  __nv_bfloat16* hi;
+  __nv_bfloat16* lo;
+  int64_t ld;
+  int32_t* grp_row0;
+  int32_t* grp_rows;
+  int32_t* unit_base;
+  int32_t units;
+  int32_t* split_row0;
+  int32_t* split_rows;
+  int splits;
+};
+cudaError_t launch_route_dz(const RouteDzArgs& a, cudaStream_t s);
+// dW [elems] = sum of n fp32 planes, in order (elems a multiple of 4).
+cudaError_t launch_join_planes(const float* planes, int n, int64_t elems, void* dW, int grad_dtype, bool accumulate,
+                               cudaStream_t s);
+
+// The router's two backward products from dz [T, N] fp32 (fp32 layers).
+struct RouteBwdArgs {
+  const void* x;     // [T, d]
+  const void* W_r;   // [N, d]
+  void* dx;          // [T, d] or null
+  void* dW_r;        // [N, d] or null
+  int grad_dtype;
+  bool accumulate;
+  const int32_t* grp_row0;   // one group of T rows (unit tables as for the experts)
+  const int32_t* grp_rows;
+  const int32_t* unit_base2;
+  unsigned* status;
+  int* sched;
+  // bf16 layers: dz as hi + lo [T, N] with row stride ld, and the row ranges
+  // and fp32 planes [splits, N, d] of the split weight gradient (splits > 1)
+  const __nv_bfloat16* hi;
+  const __nv_bfloat16* lo;
+  int64_t ld;
+  int splits;
+  const int32_t* split_row0;
+  const int32_t* split_rows;
+  float* planes;
+};
+constexpr int kMaxRouteSplits = 16;
+cudaError_t launch_route_products_tc(const Problem& p, const RouteBwdArgs& a, cudaStream_t s);
+cudaError_t launch_route_products_simt(const Problem& p, const RouteBwdArgs& a, const float* dz, cudaStream_t s);
+
+// Entry-point helpers shared by the ABI's translation units (moe_abi.cu).
+moe_status make_group_problem(const moe_cfg* cfg, int64_t rows, Problem* p);
+moe_status cuda_fail(cudaError_t e);
+cudaError_t wait_host_outputs(const void* ws, cudaStream_t s);
+cudaError_t note_device_use(const void* ws, cudaStream_t s);
+// Copies the group counts into `out` if they are non-negative and sum to
+// `rows`; otherwise writes zeros (no group runs) and flags the status.
+cudaError_t launch_check_counts(const int32_t* counts, int E, int64_t rows, int32_t* out, unsigned* status,
+                                cudaStream_t s);
+inline size_t align256(size_t v) { return (v + 255) & ~size_t(255); }
+inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+template <typename T>
+T* at(void* ws, size_t off) {
+  return reinterpret_cast<T*>(static_cast<uint8_t*>(ws) + off);
+}
+
 // y[t] = sum over the token's rows slot_pos[t, 0..k) (ascending expert) of
 // y_rows, plus the shared row y_rows[R + t]
 cudaError_t launch_combine(const Problem& p, const void* y_rows, const int32_t* slot_pos, void* y,
                            cudaStream_t s);
-// The same with the routed rows [R, d] and the shared rows [T, d] (or null) apart.
+// The same with the routed rows [R, d] and the shared rows [T, d] (or null) apart,
+// and a second set of rows [T, d] added after them (or null).
 cudaError_t launch_combine_rows(const Problem& p, const void* routed_rows, const void* shared_rows,
-                                const int32_t* slot_pos, void* y, cudaStream_t s);
+                                const int32_t* slot_pos, void* y, cudaStream_t s,
+                                const void* more_rows = nullptr);
 
 int device_sm_count();
 

@@ -46,15 +46,12 @@ cudaError_t mark_stage(int i, cudaStream_t s) {
   return g_stage_events_on ? cudaEventRecord(g_stage_events[i], s) : cudaSuccess;
 }
 
-size_t align256(size_t v) { return (v + 255) & ~size_t(255); }
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+}  // namespace
 
 moe_status cuda_fail(cudaError_t e) {
   g_last_cuda_error = (int32_t)e;
   return MOE_ERR_CUDA;
 }
-}  // namespace
 
 void record_cuda_error(cudaError_t e) { g_last_cuda_error = (int32_t)e; }
 
@@ -155,11 +152,6 @@ Layout make_layout(const Problem& p) {
 
 namespace {
 
-template <typename T>
-T* at(void* ws, size_t off) {
-  return reinterpret_cast<T*>(static_cast<uint8_t*>(ws) + off);
-}
-
 moe_status check_ws(const Layout& L, void* ws, size_t ws_bytes, size_t need) {
   if (!ws || ws_bytes < need || (reinterpret_cast<uintptr_t>(ws) & 255u)) return MOE_ERR_WORKSPACE;
   (void)L;
@@ -167,9 +159,10 @@ moe_status check_ws(const Layout& L, void* ws, size_t ws_bytes, size_t need) {
 }
 
 moe_status run_router(const Problem& p, const Layout& L, const void* x, const void* W_r,
-                      const float* b, int32_t* idx, float* gates, void* ws, cudaStream_t s) {
+                      const float* b, int32_t* idx, float* gates, void* ws, cudaStream_t s,
+                      float* logits_out = nullptr) {
   cudaError_t e = launch_router(p, x, W_r, b, at<float>(ws, L.logits), router_scratch_bytes(p), idx, gates,
-                                at<unsigned>(ws, L.status), s);
+                                at<unsigned>(ws, L.status), s, 0, logits_out);
   return e == cudaSuccess ? MOE_OK : cuda_fail(e);
 }
 
@@ -345,6 +338,8 @@ cudaError_t host_pipe_locked(const void* ws, HostPipe** out) {
   return cudaSuccess;
 }
 
+}  // namespace
+
 // A device-buffer entry point is about to enqueue work on `s` that uses ws:
 // if asynchronous host calls on this workspace have output copies that may
 // still read it, `s` waits for them first. Copies that have already finished
@@ -390,6 +385,8 @@ cudaError_t note_device_use(const void* ws, cudaStream_t s) {
   return cudaEventRecord(it->second.done, s);
 }
 
+namespace {
+
 moe_status check_weights(const Problem& p, const void* W_r, const float* b, const void* W1,
                          const void* W3, const void* W2, const void* Ws1, const void* Ws3,
                          const void* Ws2) {
@@ -402,6 +399,8 @@ moe_status check_weights(const Problem& p, const void* W_r, const float* b, cons
   }
   return MOE_OK;
 }
+
+}  // namespace
 
 // moe_experts: a problem of E groups over `rows` grouped rows (no routing,
 // no shared MLP); workspace regions and a device check of the counts.
@@ -429,6 +428,8 @@ moe_status make_group_problem(const moe_cfg* cfg, int64_t rows, Problem* p) {
   *p = q;
   return MOE_OK;
 }
+
+namespace {
 
 struct GroupLayout {
   size_t status, sched, counts_in, chunk_base, counts, offsets, grp_row0, grp_rows, unit_base1, unit_base2, h;
@@ -482,6 +483,13 @@ __global__ void check_counts_kernel(const int32_t* __restrict__ counts, int E, i
 }
 
 }  // namespace
+
+cudaError_t launch_check_counts(const int32_t* counts, int E, int64_t rows, int32_t* out, unsigned* status,
+                                cudaStream_t s) {
+  check_counts_kernel<<<1, 256, 0, s>>>(counts, E, rows, out, status);
+  return cudaGetLastError();
+}
+
 // Configuration checks of the FP8 entry points.
 moe_status check_fp8_cfg(const Problem& p) {
   if (p.dtype != MOE_BF16) return MOE_ERR_INVALID_ARG;
@@ -576,6 +584,81 @@ moe_status forward_host_pipe(const Problem& p, const Layout& L, const void* x_ho
   return MOE_OK;
 }
 
+// moe_experts and moe_experts_train (which also keeps g and u).
+static moe_status experts_device(const moe_cfg* cfg, int64_t rows, const int32_t* counts, const void* x_rows,
+                                 const float* gate_rows, const void* W1, const void* W3, const void* W2,
+                                 void* y_rows, void* gu, void* ws, size_t ws_bytes, void* stream) {
+  Problem p;
+  moe_status st = make_group_problem(cfg, rows, &p);
+  if (st != MOE_OK) return st;
+  if (rows == 0) return MOE_OK;
+  if (!counts || !x_rows || !y_rows || !W1 || !W3 || !W2) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(x_rows) || !aligned16(y_rows) || !aligned16(W1) || !aligned16(W3) || !aligned16(W2))
+    return MOE_ERR_INVALID_ARG;
+  if (gate_rows && (reinterpret_cast<uintptr_t>(gate_rows) & 3u)) return MOE_ERR_INVALID_ARG;
+  const GroupLayout L = make_group_layout(p);
+  if (!ws || ws_bytes < L.total || (reinterpret_cast<uintptr_t>(ws) & 255u)) return MOE_ERR_WORKSPACE;
+  cudaStream_t s = (cudaStream_t)stream;
+  unsigned* status = at<unsigned>(ws, L.status);
+  cudaError_t e = wait_host_outputs(ws, s);
+  if (e == cudaSuccess) e = cudaMemsetAsync(status, 0, 4, s);
+  if (e != cudaSuccess) return cuda_fail(e);
+  e = launch_check_counts(counts, p.N, rows, at<int32_t>(ws, L.counts_in), status, s);
+  if (e != cudaSuccess) return cuda_fail(e);
+  DispatchBuffers db{};
+  db.chunk_base = at<int32_t>(ws, L.chunk_base);
+  db.counts = at<int32_t>(ws, L.counts);
+  db.offsets = at<int32_t>(ws, L.offsets);
+  db.grp_row0 = at<int32_t>(ws, L.grp_row0);
+  db.grp_rows = at<int32_t>(ws, L.grp_rows);
+  db.unit_base1 = at<int32_t>(ws, L.unit_base1);
+  db.unit_base2 = at<int32_t>(ws, L.unit_base2);
+  const bool tc = p.dtype == MOE_BF16;
+  e = launch_unit_tables(p, at<int32_t>(ws, L.counts_in), db, tc ? kTcBM : kSimtBM, tc ? kTcBN1 : kSimtBN,
+                         tc ? kTcBN2 : kSimtBN, s);
+  if (e != cudaSuccess) return cuda_fail(e);
+  GemmArgs ga;
+  ga.x = nullptr;
+  ga.x_perm = x_rows;
+  ga.W1 = W1;
+  ga.W3 = W3;
+  ga.W2 = W2;
+  ga.Ws1 = ga.Ws3 = ga.Ws2 = nullptr;
+  ga.h_perm = at<void>(ws, L.h);
+  ga.h_sh = nullptr;
+  ga.y_rows = y_rows;
+  ga.grp_row0 = db.grp_row0;
+  ga.grp_rows = db.grp_rows;
+  ga.unit_base1 = db.unit_base1;
+  ga.unit_base2 = db.unit_base2;
+  ga.gate_perm = gate_rows;
+  ga.status = status;
+  ga.sched = at<int>(ws, L.sched);
+  ga.gu = gu;
+  e = tc ? launch_expert_gemms_tc(p, ga, s, nullptr) : launch_expert_gemms_simt(p, ga, s, nullptr);
+  if (e == cudaSuccess) e = note_device_use(ws, s);
+  return e == cudaSuccess ? MOE_OK : cuda_fail(e);
+}
+
+// moe_route and moe_route_train (which also keeps the logits).
+static moe_status route_device(const moe_cfg* cfg, int64_t T, const void* x, const void* W_r, const float* b,
+                               int32_t* topk_idx, float* gates, float* logits, void* ws, size_t ws_bytes,
+                               void* stream) {
+  Problem p;
+  moe_status st = make_problem(cfg, T, &p);
+  if (st != MOE_OK) return st;
+  if (T == 0) return MOE_OK;
+  if (!x || !W_r || !topk_idx || !gates || !aligned16(x) || !aligned16(W_r)) return MOE_ERR_INVALID_ARG;
+  Layout L = make_layout(p);
+  if ((st = check_ws(L, ws, ws_bytes, L.total)) != MOE_OK) return st;
+  cudaError_t e = wait_host_outputs(ws, (cudaStream_t)stream);
+  if (e == cudaSuccess) e = cudaMemsetAsync(at<void>(ws, L.status), 0, 4, (cudaStream_t)stream);
+  if (e != cudaSuccess) return cuda_fail(e);
+  if ((st = run_router(p, L, x, W_r, b, topk_idx, gates, ws, (cudaStream_t)stream, logits)) != MOE_OK) return st;
+  if ((e = note_device_use(ws, (cudaStream_t)stream)) != cudaSuccess) return cuda_fail(e);
+  return MOE_OK;
+}
+
 }  // namespace moe
 
 using namespace moe;
@@ -602,19 +685,13 @@ moe_status moe_workspace_size_host(const moe_cfg* cfg, int64_t T, size_t* bytes)
 
 moe_status moe_route(const moe_cfg* cfg, int64_t T, const void* x, const void* W_r, const float* b,
                      int32_t* topk_idx, float* gates, void* ws, size_t ws_bytes, void* stream) {
-  Problem p;
-  moe_status st = make_problem(cfg, T, &p);
-  if (st != MOE_OK) return st;
-  if (T == 0) return MOE_OK;
-  if (!x || !W_r || !topk_idx || !gates || !aligned16(x) || !aligned16(W_r)) return MOE_ERR_INVALID_ARG;
-  Layout L = make_layout(p);
-  if ((st = check_ws(L, ws, ws_bytes, L.total)) != MOE_OK) return st;
-  cudaError_t e = wait_host_outputs(ws, (cudaStream_t)stream);
-  if (e == cudaSuccess) e = cudaMemsetAsync(at<void>(ws, L.status), 0, 4, (cudaStream_t)stream);
-  if (e != cudaSuccess) return cuda_fail(e);
-  if ((st = run_router(p, L, x, W_r, b, topk_idx, gates, ws, (cudaStream_t)stream)) != MOE_OK) return st;
-  if ((e = note_device_use(ws, (cudaStream_t)stream)) != cudaSuccess) return cuda_fail(e);
-  return MOE_OK;
+  return route_device(cfg, T, x, W_r, b, topk_idx, gates, nullptr, ws, ws_bytes, stream);
+}
+
+moe_status moe_route_train(const moe_cfg* cfg, int64_t T, const void* x, const void* W_r, const float* b,
+                           int32_t* topk_idx, float* gates, float* logits, void* ws, size_t ws_bytes, void* stream) {
+  if (T > 0 && (!logits || (reinterpret_cast<uintptr_t>(logits) & 3u))) return MOE_ERR_INVALID_ARG;
+  return route_device(cfg, T, x, W_r, b, topk_idx, gates, logits, ws, ws_bytes, stream);
 }
 
 moe_status moe_dispatch(const moe_cfg* cfg, int64_t T, const int32_t* topk_idx, int32_t* counts,
@@ -832,55 +909,14 @@ moe_status moe_experts_workspace_size(const moe_cfg* cfg, int64_t rows, size_t* 
 moe_status moe_experts(const moe_cfg* cfg, int64_t rows, const int32_t* counts, const void* x_rows,
                        const float* gate_rows, const void* W1, const void* W3, const void* W2, void* y_rows,
                        void* ws, size_t ws_bytes, void* stream) {
-  Problem p;
-  moe_status st = make_group_problem(cfg, rows, &p);
-  if (st != MOE_OK) return st;
-  if (rows == 0) return MOE_OK;
-  if (!counts || !x_rows || !y_rows || !W1 || !W3 || !W2) return MOE_ERR_INVALID_ARG;
-  if (!aligned16(x_rows) || !aligned16(y_rows) || !aligned16(W1) || !aligned16(W3) || !aligned16(W2))
-    return MOE_ERR_INVALID_ARG;
-  if (gate_rows && (reinterpret_cast<uintptr_t>(gate_rows) & 3u)) return MOE_ERR_INVALID_ARG;
-  const GroupLayout L = make_group_layout(p);
-  if (!ws || ws_bytes < L.total || (reinterpret_cast<uintptr_t>(ws) & 255u)) return MOE_ERR_WORKSPACE;
-  cudaStream_t s = (cudaStream_t)stream;
-  unsigned* status = at<unsigned>(ws, L.status);
-  cudaError_t e = wait_host_outputs(ws, s);
-  if (e == cudaSuccess) e = cudaMemsetAsync(status, 0, 4, s);
-  if (e != cudaSuccess) return cuda_fail(e);
-  check_counts_kernel<<<1, 256, 0, s>>>(counts, p.N, rows, at<int32_t>(ws, L.counts_in), status);
-  if ((e = cudaGetLastError()) != cudaSuccess) return cuda_fail(e);
-  DispatchBuffers db{};
-  db.chunk_base = at<int32_t>(ws, L.chunk_base);
-  db.counts = at<int32_t>(ws, L.counts);
-  db.offsets = at<int32_t>(ws, L.offsets);
-  db.grp_row0 = at<int32_t>(ws, L.grp_row0);
-  db.grp_rows = at<int32_t>(ws, L.grp_rows);
-  db.unit_base1 = at<int32_t>(ws, L.unit_base1);
-  db.unit_base2 = at<int32_t>(ws, L.unit_base2);
-  const bool tc = p.dtype == MOE_BF16;
-  e = launch_unit_tables(p, at<int32_t>(ws, L.counts_in), db, tc ? kTcBM : kSimtBM, tc ? kTcBN1 : kSimtBN,
-                         tc ? kTcBN2 : kSimtBN, s);
-  if (e != cudaSuccess) return cuda_fail(e);
-  GemmArgs ga;
-  ga.x = nullptr;
-  ga.x_perm = x_rows;
-  ga.W1 = W1;
-  ga.W3 = W3;
-  ga.W2 = W2;
-  ga.Ws1 = ga.Ws3 = ga.Ws2 = nullptr;
-  ga.h_perm = at<void>(ws, L.h);
-  ga.h_sh = nullptr;
-  ga.y_rows = y_rows;
-  ga.grp_row0 = db.grp_row0;
-  ga.grp_rows = db.grp_rows;
-  ga.unit_base1 = db.unit_base1;
-  ga.unit_base2 = db.unit_base2;
-  ga.gate_perm = gate_rows;
-  ga.status = status;
-  ga.sched = at<int>(ws, L.sched);
-  e = tc ? launch_expert_gemms_tc(p, ga, s, nullptr) : launch_expert_gemms_simt(p, ga, s, nullptr);
-  if (e == cudaSuccess) e = note_device_use(ws, s);
-  return e == cudaSuccess ? MOE_OK : cuda_fail(e);
+  return experts_device(cfg, rows, counts, x_rows, gate_rows, W1, W3, W2, y_rows, nullptr, ws, ws_bytes, stream);
+}
+
+moe_status moe_experts_train(const moe_cfg* cfg, int64_t rows, const int32_t* counts, const void* x_rows,
+                             const float* gate_rows, const void* W1, const void* W3, const void* W2, void* y_rows,
+                             void* gu, void* ws, size_t ws_bytes, void* stream) {
+  if (rows > 0 && (!gu || !aligned16(gu))) return MOE_ERR_INVALID_ARG;
+  return experts_device(cfg, rows, counts, x_rows, gate_rows, W1, W3, W2, y_rows, gu, ws, ws_bytes, stream);
 }
 
 moe_status moe_combine(const moe_cfg* cfg, int64_t T, const void* routed_rows, const int32_t* slot_pos,

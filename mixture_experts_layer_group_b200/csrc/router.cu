@@ -241,6 +241,7 @@ struct SelectArgs {
   int32_t* idx;
   float* gates;
   unsigned* status;     // MOE_DEV_* bits (may be null)
+  float* logits_out;    // [T, N]: the summed logits (may be null)
 };
 
 // One warp per token. Lane l holds experts e = 32 j + l, j < V.
@@ -274,6 +275,11 @@ __global__ void __launch_bounds__(256) router_select_kernel(SelectArgs a) {
   for (; sp < a.S; ++sp) {
 #pragma unroll
     for (int j = 0; j < V; ++j) s[j] += 32 * j + lane < N ? zrow[sp * plane + 32 * j + lane] : 0.f;
+  }
+  if (a.logits_out) {
+#pragma unroll
+    for (int j = 0; j < V; ++j)
+      if (32 * j + lane < N) a.logits_out[t * N + 32 * j + lane] = s[j];
   }
 #pragma unroll
   for (int j = 0; j < V; ++j)
@@ -413,7 +419,7 @@ size_t router_scratch_bytes(const Problem& p) {
 
 cudaError_t launch_router(const Problem& p, const void* x, const void* W_r, const float* b,
                           float* logits, size_t logits_bytes, int32_t* idx, float* gates,
-                          unsigned* status, cudaStream_t s, int splits) {
+                          unsigned* status, cudaStream_t s, int splits, float* logits_out) {
   // K splits: `splits` when given, else router_k_splits(p); the scratch must
   // hold one [T, N] plane of partial logits per split
   const size_t plane = (size_t)p.T * (size_t)p.N * sizeof(float);
@@ -449,7 +455,7 @@ cudaError_t launch_router(const Problem& p, const void* x, const void* W_r, cons
   if (err != cudaSuccess) return err;
 
   SelectArgs a{logits, S, b, p.T, p.N, p.k, p.G, p.TG, p.score_fn, p.group_score, p.normalize,
-               p.route_scale, idx, gates, status};
+               p.route_scale, idx, gates, status, logits_out};
   const int warps = 8;
   unsigned blocks = (unsigned)((p.T + warps - 1) / warps);
   int V = (p.N + 31) / 32;

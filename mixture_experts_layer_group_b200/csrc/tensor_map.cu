@@ -49,6 +49,28 @@ bool make_tmap_bf16_swz(CUtensorMap* m, const void* base, uint64_t rows, uint64_
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool make_tmap_nd(CUtensorMap* m, const void* base, int elem_bytes, int rank, const uint64_t* dims,
+                  const uint64_t* row_bytes, const uint32_t* box, int swizzle_bytes, bool promote) {
+  memset(m, 0, sizeof(*m));
+  if (!base) return true;  // never referenced
+  for (int i = 0; i < rank; ++i)
+    if (dims[i] == 0) return true;
+  EncodeTiledFn enc = encode_fn();
+  if (!enc) return false;
+  cuuint64_t d[3], st[2];
+  cuuint32_t b[3], estr[3] = {1, 1, 1};
+  for (int i = 0; i < rank; ++i) {
+    d[i] = dims[i];
+    b[i] = box[i];
+    if (i > 0) st[i - 1] = row_bytes[i - 1];
+  }
+  return enc(m, elem_bytes == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32,
+             (cuuint32_t)rank, const_cast<void*>(base), d, st, b, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             swizzle_bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+             promote ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B : CU_TENSOR_MAP_L2_PROMOTION_NONE,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 bool make_tmap_u8(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols, uint32_t box_cols,
                   uint32_t box_rows, int swizzle_bytes) {
   memset(m, 0, sizeof(*m));

@@ -1,0 +1,302 @@
+// C ABI of the layer's backward steps (declared in include/moe_b200.h):
+// argument checks, workspace carving and launch sequences, all on the
+// caller's stream. The training forward lives with the forward (moe_abi.cu),
+// the gradient norm and clipping in grad_clip.cu.
+#include "internal.h"
+
+namespace moe {
+namespace {
+
+struct BwdLayout {
+  size_t status, sched, counts_in, chunk_base, counts, offsets, grp_row0, grp_rows, unit_base1, unit_base2;
+  size_t dg, du, gh, part;
+  size_t total;
+};
+
+BwdLayout make_bwd_layout(const Problem& p) {
+  BwdLayout L{};
+  size_t off = 0;
+  auto take = [&](size_t bytes) {
+    size_t at = off;
+    off = align256(off + bytes);
+    return at;
+  };
+  const size_t N = (size_t)p.N, rf = (size_t)p.R * p.F * p.elem;
+  L.status = take(256);  // first, as in every workspace of the library
+  L.sched = take(256);
+  L.counts_in = take(N * 4);
+  L.chunk_base = take(N * 4);
+  L.counts = take(N * 4);
+  L.offsets = take((N + 1) * 4);
+  L.grp_row0 = take((N + 1) * 4);
+  L.grp_rows = take((N + 1) * 4);
+  L.unit_base1 = take((N + 2) * 4);
+  L.unit_base2 = take((N + 2) * 4);
+  L.dg = take(rf);
+  L.du = take(rf);
+  L.gh = take(rf);
+  L.part = take((size_t)dgate_planes(p) * p.R * 4);
+  L.total = off;
+  return L;
+}
+
+// The router's products: row tables, the logits' gradient (fp32, or two bf16
+// terms of ld columns) and the planes of a split weight gradient.
+struct RouteLayout {
+  size_t status, sched, grp_row0, grp_rows, unit_base, split_row0, split_rows, dz, lo, planes;
+  size_t total;
+  int splits;
+  int64_t ld;
+};
+
+RouteLayout make_route_layout(const Problem& p) {
+  RouteLayout L{};
+  size_t off = 0;
+  auto take = [&](size_t bytes) {
+    size_t at = off;
+    off = align256(off + bytes);
+    return at;
+  };
+  L.ld = (p.N + 7) / 8 * 8;
+  L.splits = 1;
+  if (p.dtype == MOE_BF16) {
+    // dW_r is N x d summed over all tokens: few tiles with a long sum. The
+    // tokens are split so that about one tile per CTA pair runs at a time,
+    // each over 256 tokens or more.
+    const int64_t tiles = (int64_t)((p.N + 255) / 256) * ((p.d + 255) / 256);
+    int64_t n = kRouterTargetSms / 2 / tiles;
+    if (n > p.T / 256) n = p.T / 256;
+    if (n > kMaxRouteSplits) n = kMaxRouteSplits;
+    if (n > 1) L.splits = (int)n;
+  }
+  L.status = take(256);
+  L.sched = take(256);
+  L.grp_row0 = take(8);
+  L.grp_rows = take(8);
+  L.unit_base = take(12);
+  L.split_row0 = take(kMaxRouteSplits * 4);
+  L.split_rows = take(kMaxRouteSplits * 4);
+  L.dz = take(p.dtype == MOE_BF16 ? (size_t)p.T * L.ld * 2 : (size_t)p.T * p.N * 4);
+  L.lo = take(p.dtype == MOE_BF16 ? (size_t)p.T * L.ld * 2 : 0);
+  L.planes = take(L.splits > 1 ? (size_t)L.splits * p.N * p.d * 4 : 0);
+  L.total = off;
+  return L;
+}
+
+// The weight gradients' type and whether they are added to.
+moe_status check_grad(const Problem& p, int32_t grad_dtype, int32_t accumulate) {
+  if (grad_dtype != MOE_F32 && grad_dtype != MOE_BF16) return MOE_ERR_INVALID_ARG;
+  if (grad_dtype == MOE_BF16 && p.dtype != MOE_BF16) return MOE_ERR_INVALID_ARG;
+  // a bf16 sum over steps loses what each step adds: fp32 only
+  if (accumulate && grad_dtype != MOE_F32) return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+bool bad4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) != 0; }
+
+moe_status check_workspace(const void* ws, size_t have, size_t need) {
+  return !ws || have < need || (reinterpret_cast<uintptr_t>(ws) & 255u) ? MOE_ERR_WORKSPACE : MOE_OK;
+}
+
+}  // namespace
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" {
+
+moe_status moe_experts_backward_workspace_size(const moe_cfg* cfg, int64_t rows, size_t* bytes) {
+  Problem p;
+  moe_status st = make_group_problem(cfg, rows, &p);
+  if (st != MOE_OK) return st;
+  if (!bytes) return MOE_ERR_INVALID_ARG;
+  *bytes = make_bwd_layout(p).total;
+  return MOE_OK;
+}
+
+moe_status moe_experts_backward(const moe_cfg* cfg, int64_t rows, const int32_t* counts, const void* x_rows,
+                                const float* gate_rows, const void* W1, const void* W3, const void* W2,
+                                const void* gu, const void* dy_rows, void* dx_rows, float* dgate_rows, void* dW1,
+                                void* dW3, void* dW2, int32_t grad_dtype, int32_t accumulate, void* ws,
+                                size_t ws_bytes, void* stream) {
+  Problem p;
+  moe_status st = make_group_problem(cfg, rows, &p);
+  if (st != MOE_OK) return st;
+  if ((st = check_grad(p, grad_dtype, accumulate)) != MOE_OK) return st;
+  const bool any_dw = dW1 || dW3 || dW2;
+  if (any_dw && (!dW1 || !dW3 || !dW2 || !aligned16(dW1) || !aligned16(dW3) || !aligned16(dW2)))
+    return MOE_ERR_INVALID_ARG;
+  cudaStream_t s = (cudaStream_t)stream;
+  if (rows == 0) {
+    // no rows: the weight gradients are zero (or unchanged)
+    if (!any_dw || accumulate) return MOE_OK;
+    const size_t n = (size_t)p.N * p.F * p.d * (grad_dtype == MOE_F32 ? 4 : 2);
+    cudaError_t e = cudaMemsetAsync(dW1, 0, n, s);
+    if (e == cudaSuccess) e = cudaMemsetAsync(dW3, 0, n, s);
+    if (e == cudaSuccess) e = cudaMemsetAsync(dW2, 0, n, s);
+    return e == cudaSuccess ? MOE_OK : cuda_fail(e);
+  }
+  if (!counts || !x_rows || !W1 || !W3 || !W2 || !gu || !dy_rows) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(x_rows) || !aligned16(W1) || !aligned16(W3) || !aligned16(W2) || !aligned16(gu) ||
+      !aligned16(dy_rows) || !aligned16(dx_rows) || bad4(counts) || bad4(gate_rows) || bad4(dgate_rows))
+    return MOE_ERR_INVALID_ARG;
+  const BwdLayout L = make_bwd_layout(p);
+  if ((st = check_workspace(ws, ws_bytes, L.total)) != MOE_OK) return st;
+  unsigned* status = at<unsigned>(ws, L.status);
+  cudaError_t e = wait_host_outputs(ws, s);
+  if (e == cudaSuccess) e = cudaMemsetAsync(status, 0, 4, s);
+  if (e == cudaSuccess) e = launch_check_counts(counts, p.N, rows, at<int32_t>(ws, L.counts_in), status, s);
+  if (e != cudaSuccess) return cuda_fail(e);
+  DispatchBuffers db{};
+  db.chunk_base = at<int32_t>(ws, L.chunk_base);
+  db.counts = at<int32_t>(ws, L.counts);
+  db.offsets = at<int32_t>(ws, L.offsets);
+  db.grp_row0 = at<int32_t>(ws, L.grp_row0);
+  db.grp_rows = at<int32_t>(ws, L.grp_rows);
+  db.unit_base1 = at<int32_t>(ws, L.unit_base1);
+  db.unit_base2 = at<int32_t>(ws, L.unit_base2);
+  const bool tc = p.dtype == MOE_BF16;
+  e = launch_unit_tables(p, at<int32_t>(ws, L.counts_in), db, tc ? kTcBM : kSimtBM, tc ? kTcBN2 : kSimtBN,
+                         tc ? kTcBN2 : kSimtBN, s);
+  if (e != cudaSuccess) return cuda_fail(e);
+  ExpertsBwdArgs a{};
+  a.x_rows = x_rows;
+  a.gate_rows = gate_rows;
+  a.W1 = W1;
+  a.W3 = W3;
+  a.W2 = W2;
+  a.gu = gu;
+  a.dy_rows = dy_rows;
+  a.dx_rows = dx_rows;
+  a.dgate_rows = dgate_rows;
+  a.dW1 = dW1;
+  a.dW3 = dW3;
+  a.dW2 = dW2;
+  a.grad_dtype = grad_dtype;
+  a.accumulate = accumulate != 0;
+  a.dg = at<void>(ws, L.dg);
+  a.du = at<void>(ws, L.du);
+  a.gh = at<void>(ws, L.gh);
+  a.dgate_part = at<float>(ws, L.part);
+  a.grp_row0 = db.grp_row0;
+  a.grp_rows = db.grp_rows;
+  a.unit_base1 = db.unit_base1;
+  a.unit_base2 = db.unit_base2;
+  a.status = status;
+  a.sched = at<int>(ws, L.sched);
+  e = tc ? launch_experts_backward_tc(p, a, s) : launch_experts_backward_simt(p, a, s);
+  if (e == cudaSuccess) e = note_device_use(ws, s);
+  return e == cudaSuccess ? MOE_OK : cuda_fail(e);
+}
+
+moe_status moe_combine_backward(const moe_cfg* cfg, int64_t T, const void* dy, const int32_t* slot_pos,
+                                void* dy_rows, void* stream) {
+  Problem p;
+  moe_status st = make_problem(cfg, T, &p);
+  if (st != MOE_OK) return st;
+  if (T == 0) return MOE_OK;
+  if (!dy || !slot_pos || !dy_rows || !aligned16(dy) || !aligned16(dy_rows) || bad4(slot_pos))
+    return MOE_ERR_INVALID_ARG;
+  const cudaError_t e = launch_gather(p, dy, slot_pos, dy_rows, nullptr, (cudaStream_t)stream);
+  return e == cudaSuccess ? MOE_OK : cuda_fail(e);
+}
+
+moe_status moe_dispatch_backward(const moe_cfg* cfg, int64_t T, const void* dx_rows, const int32_t* slot_pos,
+                                 const void* dx_shared, const void* dx_router, void* dx, void* stream) {
+  Problem p;
+  moe_status st = make_problem(cfg, T, &p);
+  if (st != MOE_OK) return st;
+  if (T == 0) return MOE_OK;
+  if (!dx_rows || !slot_pos || !dx || !aligned16(dx_rows) || !aligned16(dx) || !aligned16(dx_shared) ||
+      !aligned16(dx_router) || bad4(slot_pos))
+    return MOE_ERR_INVALID_ARG;
+  const cudaError_t e = launch_combine_rows(p, dx_rows, dx_shared, slot_pos, dx, (cudaStream_t)stream, dx_router);
+  return e == cudaSuccess ? MOE_OK : cuda_fail(e);
+}
+
+moe_status moe_route_backward_workspace_size(const moe_cfg* cfg, int64_t T, size_t* bytes) {
+  Problem p;
+  moe_status st = make_problem(cfg, T, &p);
+  if (st != MOE_OK) return st;
+  if (!bytes) return MOE_ERR_INVALID_ARG;
+  *bytes = make_route_layout(p).total;
+  return MOE_OK;
+}
+
+moe_status moe_route_backward(const moe_cfg* cfg, int64_t T, const void* x, const void* W_r, const float* logits,
+                              const int32_t* topk_idx, const float* dgates, const int32_t* slot_pos, void* dx,
+                              void* dW_r, int32_t grad_dtype, int32_t accumulate, void* ws, size_t ws_bytes,
+                              void* stream) {
+  Problem p;
+  moe_status st = make_problem(cfg, T, &p);
+  if (st != MOE_OK) return st;
+  if ((st = check_grad(p, grad_dtype, accumulate)) != MOE_OK) return st;
+  if (!aligned16(dW_r)) return MOE_ERR_INVALID_ARG;
+  cudaStream_t s = (cudaStream_t)stream;
+  if (T == 0) {
+    if (!dW_r || accumulate) return MOE_OK;
+    const cudaError_t e = cudaMemsetAsync(dW_r, 0, (size_t)p.N * p.d * (grad_dtype == MOE_F32 ? 4 : 2), s);
+    return e == cudaSuccess ? MOE_OK : cuda_fail(e);
+  }
+  if (!x || !W_r || !logits || !topk_idx || !dgates || !aligned16(x) || !aligned16(W_r) || !aligned16(dx) ||
+      bad4(logits) || bad4(topk_idx) || bad4(dgates) || bad4(slot_pos))
+    return MOE_ERR_INVALID_ARG;
+  const RouteLayout L = make_route_layout(p);
+  if ((st = check_workspace(ws, ws_bytes, L.total)) != MOE_OK) return st;
+  unsigned* status = at<unsigned>(ws, L.status);
+  cudaError_t e = wait_host_outputs(ws, s);
+  if (e == cudaSuccess) e = cudaMemsetAsync(status, 0, 4, s);
+  if (e != cudaSuccess) return cuda_fail(e);
+  const bool tc = p.dtype == MOE_BF16;
+  const int bm = tc ? kTcBM : kSimtBM, bn = tc ? kTcBN2 : kSimtBN;
+  const int64_t units = (T + bm - 1) / bm * ((p.d + bn - 1) / bn);
+  if (units > (1ll << 31) - 1) return MOE_ERR_UNSUPPORTED;
+  RouteDzArgs z{};
+  z.logits = logits;
+  z.idx = topk_idx;
+  z.dgates = dgates;
+  z.slot_pos = slot_pos;
+  z.T = T;
+  z.N = p.N;
+  z.k = p.k;
+  z.score_fn = p.score_fn;
+  z.normalize = p.normalize;
+  z.route_scale = p.route_scale;
+  z.status = status;
+  z.dz = tc ? nullptr : at<float>(ws, L.dz);
+  z.hi = at<__nv_bfloat16>(ws, L.dz);
+  z.lo = at<__nv_bfloat16>(ws, L.lo);
+  z.ld = L.ld;
+  z.grp_row0 = at<int32_t>(ws, L.grp_row0);
+  z.grp_rows = at<int32_t>(ws, L.grp_rows);
+  z.unit_base = at<int32_t>(ws, L.unit_base);
+  z.units = (int32_t)units;
+  z.split_row0 = at<int32_t>(ws, L.split_row0);
+  z.split_rows = at<int32_t>(ws, L.split_rows);
+  z.splits = L.splits;
+  if ((e = launch_route_dz(z, s)) != cudaSuccess) return cuda_fail(e);
+  RouteBwdArgs a{};
+  a.x = x;
+  a.W_r = W_r;
+  a.dx = dx;
+  a.dW_r = dW_r;
+  a.grad_dtype = grad_dtype;
+  a.accumulate = accumulate != 0;
+  a.grp_row0 = z.grp_row0;
+  a.grp_rows = z.grp_rows;
+  a.unit_base2 = z.unit_base;
+  a.status = status;
+  a.sched = at<int>(ws, L.sched);
+  a.hi = z.hi;
+  a.lo = z.lo;
+  a.ld = L.ld;
+  a.splits = L.splits;
+  a.split_row0 = z.split_row0;
+  a.split_rows = z.split_rows;
+  a.planes = at<float>(ws, L.planes);
+  e = tc ? launch_route_products_tc(p, a, s) : launch_route_products_simt(p, a, z.dz, s);
+  if (e == cudaSuccess) e = note_device_use(ws, s);
+  return e == cudaSuccess ? MOE_OK : cuda_fail(e);
+}
+
+}  // extern "C"

@@ -1,0 +1,455 @@
+// Weight gradients on the tensor cores: dW[g][m][n] = sum over the rows r of
+// group g of A[r][m] B[r][n], for several matrices in one launch (the
+// experts' dW1 = dg^T x, dW3 = du^T x, dW2 = dy^T (gate h); the router's
+// dW_r = dz^T x). Both operands are row-major with the rows as the reduction,
+// so both are MN-major tiles: a 64 x 64 TMA box is 64 rows (k) of 128 bytes.
+//
+// CTA pairs (clusters of 2, cta_group::2): a unit is one 256 x 256 tile of one
+// group's matrix; CTA r loads 128 columns of A and 128 of B per 64 rows (32
+// KB, six stages) and keeps rows 128 r .. 128 r + 127 of the tile in its
+// tensor memory, in one of two 256-column buffers, so a unit's MMAs overlap
+// the previous unit's stores. Units are taken with a fixed stride.
+//
+// A group's last stage may hold up to 15 rows of the next group inside its
+// last K = 16 step. They would enter the sum, and a NaN there cannot be
+// multiplied away, so a fixer warp in each CTA zeroes them in both operands
+// before the stage is handed to the MMA issuer.
+//
+// Warps: 0 producer, 1 tensor-memory owner and MMA issuer (first CTA), 2..9
+// epilogue (two per lane quadrant), 10 fixer. Waits are bounded as everywhere.
+#include <mutex>
+
+#include "common.cuh"
+#include "internal.h"
+
+namespace moe {
+namespace {
+
+constexpr int kBK = 64;
+constexpr int kTile = 256;
+constexpr int kBox = 64 * kBK * 2;           // 8 KB
+constexpr int kStageBytes = 4 * kBox;        // A: two boxes, B: two boxes
+constexpr int kStages = 6;
+constexpr int kEpiWarps = 8;
+constexpr int kThreads = 32 * (3 + kEpiWarps);
+constexpr int kOutTile = 32 * 128;           // 32 rows x 128 bytes per epilogue warp
+constexpr int kSmem = kStages * kStageBytes + kEpiWarps * kOutTile + 1024 + 512;
+static_assert(kSmem <= 232448, "shared memory budget");
+constexpr int kTmemCols = 512;
+
+struct Matrix {
+  CUtensorMap a[2];  // [R, M] per segment
+  CUtensorMap b;     // [R, N]
+  CUtensorMap out;   // [groups, M, N]
+  int M, N, mt, nt;
+};
+struct Params {
+  Matrix mat[3];
+  int nmat, groups, segments;
+  int units_per_group;
+  int64_t units;
+  const int32_t* grp_row0;
+  const int32_t* grp_rows;
+  int grad_f32, accumulate;
+  unsigned* status;
+};
+
+struct Shared {
+  uint64_t full[kStages];      // CTA 0: the stage's bytes of both CTAs landed (and were fixed)
+  uint64_t empty[kStages];     // both: the MMAs finished reading the stage
+  uint64_t landed[kStages];    // each CTA: its own bytes of a stage that needs fixing landed
+  uint64_t acc_full[2];        // both
+  uint64_t acc_empty[2];       // CTA 0
+  uint64_t drained;            // both
+  uint32_t tmem_base;
+  uint32_t sink;               // target of CTA 1's signalling stores (never read)
+  uint32_t consumed;
+  int abort_flag;
+};
+static_assert(sizeof(Shared) <= 512, "barrier block");
+
+struct Unit {
+  int g, mat, m0, n0, row0, rows;
+};
+MOE_DEV Unit decode(const Params& p, int64_t u) {
+  Unit t;
+  t.g = (int)(u / p.units_per_group);
+  int left = (int)(u % p.units_per_group);
+  t.mat = 0;
+  while (t.mat < p.nmat - 1 && left >= p.mat[t.mat].mt * p.mat[t.mat].nt) {
+    left -= p.mat[t.mat].mt * p.mat[t.mat].nt;
+    ++t.mat;
+  }
+  t.m0 = left / p.mat[t.mat].nt * kTile;
+  t.n0 = left % p.mat[t.mat].nt * kTile;
+  t.row0 = __ldg(p.grp_row0 + t.g);
+  t.rows = __ldg(p.grp_rows + t.g);
+  return t;
+}
+// Rows of the last 64-row block, and whether foreign rows share its last K step.
+MOE_DEV int tail_rows(int rows) { return rows - (rows - 1) / kBK * kBK; }
+
+MOE_DEV void mbar_arrive_n(uint64_t* bar, uint32_t n) {
+  asm volatile("{\n\t.reg .b64 st;\n\tmbarrier.arrive.shared::cta.b64 st, [%0], %1;\n\t}" ::"r"(smem_u32(bar)), "r"(n)
+               : "memory");
+}
+MOE_DEV void mbar_arrive_cluster(uint32_t bar_cluster) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster) : "memory");
+}
+MOE_DEV void tma_store_3d(const void* tmap, uint32_t smem_src, int32_t c0, int32_t c1, int32_t c2) {
+  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
+                   reinterpret_cast<uint64_t>(tmap)),
+               "r"(smem_src), "r"(c0), "r"(c1), "r"(c2)
+               : "memory");
+}
+// Adds the fp32 box to global memory (each element of dW is added to once).
+MOE_DEV void tma_add_3d(const void* tmap, uint32_t smem_src, int32_t c0, int32_t c1, int32_t c2) {
+  asm volatile("cp.reduce.async.bulk.tensor.3d.global.shared::cta.add.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
+                   reinterpret_cast<uint64_t>(tmap)),
+               "r"(smem_src), "r"(c0), "r"(c1), "r"(c2)
+               : "memory");
+}
+
+__global__ void __launch_bounds__(kThreads, 1) wgrad_tc_kernel(const __grid_constant__ Params p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* out_tiles = smem + kStages * kStageBytes;
+  Shared& sh = *reinterpret_cast<Shared*>(out_tiles + kEpiWarps * kOutTile);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();
+  const bool first = rank == 0;
+  const int64_t pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      // a stage as loaded: the producer's three arrivals and both CTAs' bytes;
+      // a fixed stage: the producer's one arrival and the two fixers'
+      mbar_init(&sh.full[s], 3);
+      mbar_init(&sh.empty[s], 1);
+      mbar_init(&sh.landed[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&sh.acc_full[b], 1);
+      mbar_init(&sh.acc_empty[b], kEpiWarps);
+    }
+    mbar_init(&sh.drained, 1);
+    sh.abort_flag = 0;
+    sh.consumed = 0;
+    fence_barrier_init();
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(&sh.tmem_base, kTmemCols);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before();
+  cluster_sync();
+  tc_fence_after();
+  const uint32_t tmem_base = sh.tmem_base;
+  volatile int* abort_flag = &sh.abort_flag;
+  auto in_first = [&](const void* local) { return map_to_rank(smem_u32(local), 0u); };
+  auto fail = [&]() {
+    *abort_flag = 1;
+    set_status(p.status, MOE_DEV_WAIT_TIMEOUT);
+  };
+
+  uint32_t fills = 0, fixes = 0, fix_phase = 0;  // producer: fills issued; slots whose last fill is fixed; uses of landed[]
+  if (warp == 0) {
+    if (lane == 0) {
+      const uint64_t pol = policy_evict_normal();
+      bool ok = true;
+      for (int64_t u = pair; ok && u < p.units; u += pairs) {
+        const Unit t = decode(p, u);
+        if (t.rows == 0) continue;
+        const Matrix& x = p.mat[t.mat];
+        const int nk = (t.rows + kBK - 1) / kBK;
+        const bool ragged = tail_rows(t.rows) % 16 != 0;
+        const int ca = t.m0 + 128 * (int)rank, cb = t.n0 + 128 * (int)rank;
+        for (int sg = 0; sg < p.segments && ok; ++sg)
+          for (int kc = 0; kc < nk; ++kc, ++fills) {
+            const uint32_t s = fills % kStages;
+            if (!mbar_wait_cluster_bounded(&sh.empty[s], ((fills / kStages) & 1u) ^ 1u, abort_flag)) {
+              ok = false;
+              break;
+            }
+            uint8_t* dst = smem + s * kStageBytes;
+            const int r = t.row0 + kc * kBK;
+            const bool fix = ragged && kc == nk - 1;
+            if (fix) {
+              // this CTA's bytes land on its own barrier; the fixers hand the stage on
+              mbar_arrive_expect_tx(&sh.landed[s], kStageBytes);
+              if (first) mbar_arrive(&sh.full[s]);
+              for (int c = 0; c < 2; ++c) {
+                tma_load_2d_hint(dst + c * kBox, &x.a[sg], &sh.landed[s], ca + 64 * c, r, pol);
+                tma_load_2d_hint(dst + (2 + c) * kBox, &x.b, &sh.landed[s], cb + 64 * c, r, pol);
+              }
+              fixes |= 1u << s;
+              fix_phase ^= 1u << s;
+            } else {
+              const uint32_t bar = in_first(&sh.full[s]);
+              if (first) {
+                mbar_arrive_expect_tx(&sh.full[s], 2 * kStageBytes);
+                mbar_arrive_n(&sh.full[s], 2);
+              }
+              for (int c = 0; c < 2; ++c) {
+                tma_load_2d_pair(dst + c * kBox, &x.a[sg], bar, ca + 64 * c, r, pol);
+                tma_load_2d_pair(dst + (2 + c) * kBox, &x.b, bar, cb + 64 * c, r, pol);
+              }
+              fixes &= ~(1u << s);
+            }
+          }
+      }
+      if (!ok) fail();
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    if (lane == 0 && first) {
+      const uint32_t idesc = idesc_bf16_f32(256, kTile) | kIdescAMn | kIdescBMn;
+      uint32_t consumed = 0, accs = 0;
+      bool ok = true;
+      for (int64_t u = pair; ok && u < p.units; u += pairs) {
+        const Unit t = decode(p, u);
+        if (t.rows == 0) continue;
+        const int nk = (t.rows + kBK - 1) / kBK;
+        const int last_steps = (tail_rows(t.rows) + 15) / 16;
+        const uint32_t b = accs & 1u;
+        if (!mbar_wait_cluster_bounded(&sh.acc_empty[b], ((accs >> 1) & 1u) ^ 1u, abort_flag)) {
+          ok = false;
+          break;
+        }
+        ++accs;
+        tc_fence_after();
+        const uint32_t d = tmem_base + b * kTile;
+        bool more = false;  // accumulate onto the unit's earlier steps
+        for (int kc = 0; kc < nk * p.segments; ++kc) {
+          const uint32_t s = consumed % kStages;
+          if (!mbar_wait_cluster_bounded(&sh.full[s], (consumed / kStages) & 1u, abort_flag)) {
+            ok = false;
+            break;
+          }
+          ++consumed;
+          tc_fence_after();
+          const uint32_t at = smem_u32(smem + s * kStageBytes);
+          const int steps = kc % nk == nk - 1 ? last_steps : kBK / 16;
+          for (int kk = 0; kk < steps; ++kk) {
+            umma_bf16_pair(d, smem_desc_sw128_mn(at + kk * 2048, kBox),
+                           smem_desc_sw128_mn(at + 2 * kBox + kk * 2048, kBox), idesc, more);
+            more = true;
+          }
+          umma_commit_pair_both(smem_u32(&sh.empty[s]));
+        }
+        if (ok) umma_commit_pair_both(smem_u32(&sh.acc_full[b]));
+      }
+      if (!ok) fail();
+      umma_commit_pair_both(smem_u32(&sh.drained));
+      sh.consumed = consumed;
+    }
+    if (lane == 0) {
+      int no_abort = 0;
+      if (!mbar_wait_cluster_bounded(&sh.drained, 0, &no_abort)) set_status(p.status, MOE_DEV_WAIT_TIMEOUT);
+    }
+    __syncwarp();
+  } else if (warp < 2 + kEpiWarps) {
+    const int q = warp & 3, ew = warp - 2, sub = ew >> 2;
+    const uint32_t tile = smem_u32(out_tiles + ew * kOutTile);
+    uint32_t accs = 0;
+    for (int64_t u = pair; u < p.units; u += pairs) {
+      const Unit t = decode(p, u);
+      if (t.rows == 0 && p.accumulate) continue;
+      const Matrix& x = p.mat[t.mat];
+      const uint32_t b = accs & 1u;
+      if (t.rows > 0) {
+        int ok = 1;
+        if (lane == 0) ok = mbar_wait_cluster_bounded(&sh.acc_full[b], (accs >> 1) & 1u, abort_flag);
+        ok = __shfl_sync(0xffffffffu, ok, 0);
+        if (!ok) {
+          if (lane == 0) fail();
+          break;
+        }
+        ++accs;
+        tc_fence_after();
+      }
+      const int m = t.m0 + 128 * (int)rank + 32 * q;
+      const uint32_t t_q = tmem_base + ((uint32_t)(q * 32) << 16) + b * kTile;
+      const int width = p.grad_f32 ? 32 : 64;  // columns of a 128-byte tile row
+#pragma unroll 1
+      for (int c = sub * width; c < kTile; c += 2 * width) {
+        const int n = t.n0 + c;
+        if (m >= x.M || n >= x.N) break;
+        uint32_t v[32];
+        if (t.rows == 0) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[i] = 0u;
+        } else if (p.grad_f32) {
+          tmem_ld32(t_q + c, v);
+          tmem_wait_ld();
+        } else {
+          uint32_t w[32];
+          tmem_ld32(t_q + c, v);
+          tmem_ld32(t_q + c + 32, w);
+          tmem_wait_ld();
+#pragma unroll
+          for (int i = 0; i < 16; ++i) v[i] = pack_bf16x2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
+#pragma unroll
+          for (int i = 0; i < 16; ++i) v[16 + i] = pack_bf16x2(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
+        }
+        if (lane == 0) bulk_wait_group_read<0>();  // the previous store has read the tile
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          st_shared_v4(tile + lane * 128 + ((i ^ (lane & 7)) << 4),
+                       make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]));
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          if (p.accumulate) tma_add_3d(&x.out, tile, n, m, t.g);
+          else tma_store_3d(&x.out, tile, n, m, t.g);
+          bulk_commit_group();
+        }
+      }
+      if (t.rows > 0) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          if (!first) st_async_u32(in_first(&sh.sink), 0u, in_first(&sh.acc_empty[b]));
+          else if (ew == 0) mbar_arrive_expect_tx(&sh.acc_empty[b], 4 * kEpiWarps);  // and CTA 1's warps' stores
+          else mbar_arrive(&sh.acc_empty[b]);
+        }
+      }
+    }
+    if (lane == 0) bulk_wait_group_all();
+  } else {
+    // ------------------------------------------------------------- fixer --
+    uint32_t j = 0, phase = 0;
+    bool ok = true;
+    for (int64_t u = pair; ok && u < p.units; u += pairs) {
+      const Unit t = decode(p, u);
+      if (t.rows == 0) continue;
+      const int nk = (t.rows + kBK - 1) / kBK;
+      const int v = tail_rows(t.rows);
+      if (v % 16 == 0) {
+        j += nk * p.segments;
+        continue;
+      }
+      for (int sg = 0; sg < p.segments; ++sg) {
+        j += nk;
+        const uint32_t s = (j - 1) % kStages;
+        int got = 1;
+        if (lane == 0) got = mbar_wait_bounded(&sh.landed[s], (phase >> s) & 1u, abort_flag);
+        got = __shfl_sync(0xffffffffu, got, 0);
+        if (!got) {
+          if (lane == 0) fail();
+          ok = false;
+          break;
+        }
+        phase ^= 1u << s;
+        // rows v .. (the next multiple of 16) - 1 of the four boxes, 128 bytes each
+        const uint32_t at = smem_u32(smem + s * kStageBytes);
+        const int words = 8 * ((16 - v % 16));
+        for (int i = lane; i < 4 * words; i += 32)
+          st_shared_v4(at + (i / words) * kBox + v * 128 + (i % words) * 16, make_uint4(0, 0, 0, 0));
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(in_first(&sh.full[s]));
+      }
+    }
+  }
+
+  __syncthreads();
+  if (warp == 0 && lane == 0) {
+    // wait for any stage fill that was issued but may not have landed
+    const uint32_t done = first ? sh.consumed : (fills > kStages ? fills - kStages : 0u);
+    for (uint32_t j = done; j < fills; ++j) {
+      const uint32_t s = j % kStages;
+      int no_abort = 0;
+      const bool fixed = (fixes >> s) & 1u;
+      if (!fixed && !first) continue;  // the first CTA's barrier: waited for there
+      if (!(fixed ? mbar_wait_bounded(&sh.landed[s], ((fix_phase >> s) & 1u) ^ 1u, &no_abort)
+                  : mbar_wait_cluster_bounded(&sh.full[s], (j / kStages) & 1u, &no_abort))) {
+        set_status(p.status, MOE_DEV_WAIT_TIMEOUT);
+        break;
+      }
+    }
+  }
+  tc_fence_before();
+  cluster_sync();  // neither CTA leaves while the other may still touch its shared memory
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem_base, kTmemCols);
+  }
+}
+
+bool make_rows_map(CUtensorMap* m, const void* base, int64_t rows, int cols, int64_t ld) {
+  const uint64_t dims[2] = {(uint64_t)cols, (uint64_t)rows}, stride[1] = {(uint64_t)ld * 2};
+  const uint32_t box[2] = {64, kBK};
+  return make_tmap_nd(m, base, 2, 2, dims, stride, box, 128, true);
+}
+
+}  // namespace
+
+cudaError_t launch_wgrad_tc(const WgradArgs& a, cudaStream_t s) {
+  Params p{};
+  p.nmat = a.nmat;
+  p.groups = a.groups;
+  p.segments = a.segments;
+  const int elem = a.grad_dtype == MOE_F32 ? 4 : 2;
+  for (int i = 0; i < a.nmat; ++i) {
+    const WgradMatrix& w = a.mat[i];
+    Matrix& x = p.mat[i];
+    x.M = w.M;
+    x.N = w.N;
+    x.mt = (w.M + kTile - 1) / kTile;
+    x.nt = (w.N + kTile - 1) / kTile;
+    p.units_per_group += x.mt * x.nt;
+    const uint64_t dims[3] = {(uint64_t)w.N, (uint64_t)w.M, (uint64_t)a.groups};
+    const uint64_t stride[2] = {(uint64_t)w.N * elem, (uint64_t)w.N * w.M * elem};
+    const uint32_t box[3] = {128u / elem, 32, 1};
+    if (!make_rows_map(&x.a[0], w.A[0], a.rows, w.M, w.lda) || !make_rows_map(&x.a[1], w.A[1], a.rows, w.M, w.lda) ||
+        !make_rows_map(&x.b, w.B, a.rows, w.N, w.N) ||
+        !make_tmap_nd(&x.out, w.out, elem, 3, dims, stride, box, 128, false))
+      return cudaErrorInvalidValue;
+  }
+  p.units = (int64_t)a.groups * p.units_per_group;
+  p.grp_row0 = a.grp_row0;
+  p.grp_rows = a.grp_rows;
+  p.grad_f32 = a.grad_dtype == MOE_F32;
+  p.accumulate = a.accumulate;
+  p.status = a.status;
+  if (p.units == 0) return cudaSuccess;
+
+  static std::mutex mu;
+  static int max_clusters_of[kMaxDevices] = {};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.dynamicSmemBytes = kSmem;
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  int clusters = 0;
+  {
+    std::lock_guard<std::mutex> lock(mu);
+    if (max_clusters_of[dev] == 0) {
+      e = cudaFuncSetAttribute(wgrad_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+      if (e != cudaSuccess) return e;
+      cfg.gridDim = dim3(2 * (device_sm_count() / 2), 1, 1);
+      int n = 0;
+      e = cudaOccupancyMaxActiveClusters(&n, wgrad_tc_kernel, &cfg);
+      if (e != cudaSuccess) return e;
+      max_clusters_of[dev] = n > 0 ? n : 1;
+    }
+    clusters = max_clusters_of[dev];
+  }
+  if (p.units < clusters) clusters = (int)p.units;
+  cfg.gridDim = dim3(2 * clusters, 1, 1);
+  return cudaLaunchKernelEx(&cfg, wgrad_tc_kernel, p);
+}
+
+}  // namespace moe

@@ -1,0 +1,131 @@
+"""One training step of the DeepSeekMoE layer on one GPU.
+
+TrainLayer orders the C ABI's training calls around buffers it keeps: the
+forward that saves what the backward reads, the backward into weight-gradient
+buffers, clipping by the global norm and the loss-free balancing of the
+selection bias. Every compute step runs in the library's CUDA kernels; this
+module only sizes the buffers and orders the calls. It holds no autograd
+graph: forward() and backward() are called in turn, and a step can be captured
+into a CUDA graph.
+"""
+from __future__ import annotations
+
+import torch
+
+from . import (MOE_BF16, MOE_F32, GradList, MoeCfg, bias_update, combine, combine_backward, dispatch_backward,
+               dispatch_rows, experts_backward, experts_backward_workspace_size, experts_train,
+               experts_workspace_size, grad_clip, grad_norm, grad_norm_workspace_size, route_backward,
+               route_backward_workspace_size, route_train, workspace_size)
+
+_DTYPE = {MOE_BF16: torch.bfloat16, MOE_F32: torch.float32}
+
+
+def _group_cfg(cfg: MoeCfg, groups: int, d_ff: int) -> MoeCfg:
+    """The grouped-expert problem of `groups` experts of width d_ff."""
+    return MoeCfg(d=cfg.d, d_ff=d_ff, n_routed=groups, n_shared=0, top_k=1, n_groups=1, topk_groups=1, route_scale=1.0,
+                  dtype=cfg.dtype)
+
+
+class TrainLayer:
+    """The layer with its gradients.
+
+    weights: as for MoELayer (bf16 or fp32 tensors in the layouts of the C
+    ABI; FP8 weights are not trained). grads: the weights' gradients by name,
+    of grad_dtype ("f32" or "bf16"; None: the layer's type), written by each
+    backward(), or added to by backward(accumulate=True) (fp32). max_tokens
+    bounds a call's tokens. All calls of one TrainLayer belong on one stream."""
+
+    def __init__(self, cfg: MoeCfg, weights: dict, max_tokens: int, grad_dtype=None, device="cuda"):
+        self.cfg, self.w, self.max_tokens = cfg, weights, max_tokens
+        self.grad_dtype = grad_dtype or {MOE_BF16: "bf16", MOE_F32: "f32"}[cfg.dtype]
+        self.device = device
+        self.dtype = _DTYPE[cfg.dtype]
+        self.routed = _group_cfg(cfg, cfg.n_routed, cfg.d_ff)
+        self.shared = _group_cfg(cfg, 1, cfg.n_shared * cfg.d_ff) if cfg.n_shared else None
+        T, R = max_tokens, max_tokens * cfg.top_k
+        sizes = [workspace_size(cfg, T), experts_workspace_size(self.routed, R),
+                 experts_backward_workspace_size(self.routed, R), route_backward_workspace_size(cfg, T)]
+        if self.shared is not None:
+            sizes += [experts_workspace_size(self.shared, T), experts_backward_workspace_size(self.shared, T)]
+        # the calls of a step follow one another, so one workspace serves them all
+        self.ws = torch.empty(max(sizes), dtype=torch.uint8, device=device)
+        gdt = {"bf16": torch.bfloat16, "f32": torch.float32}[self.grad_dtype]
+        names = ["W_r", "W1", "W3", "W2"] + (["Ws1", "Ws3", "Ws2"] if self.shared is not None else [])
+        self.grads = {n: torch.zeros(weights[n].shape, dtype=gdt, device=device) for n in names}
+        self.grad_list = GradList(self.grads.values())
+        self.clip_ws = torch.empty(grad_norm_workspace_size(self.grad_list), dtype=torch.uint8, device=device)
+        self.sumsq = torch.zeros(1, dtype=torch.float64, device=device)
+        self.norm = torch.zeros(1, dtype=torch.float32, device=device)
+        self.saved = None
+
+    def _new(self, shape, dtype=None):
+        return torch.empty(shape, dtype=dtype or self.dtype, device=self.device)
+
+    def forward(self, x, stream=None):
+        """y of the tokens x [T, d]; keeps what backward() needs."""
+        cfg, w, T, k = self.cfg, self.w, x.shape[0], self.cfg.top_k
+        if T > self.max_tokens:
+            raise ValueError(f"{T} tokens exceed max_tokens {self.max_tokens}")
+        R, i32, f32 = T * k, torch.int32, torch.float32
+        s = dict(x=x, idx=self._new((T, k), i32), gates=self._new((T, k), f32), logits=self._new((T, cfg.n_routed), f32),
+                 counts=self._new(cfg.n_routed, i32), slot_pos=self._new((T, k), i32), x_rows=self._new((R, cfg.d)),
+                 gate_rows=self._new(R, f32), gu=self._new((R, 2 * cfg.d_ff)))
+        y = torch.empty_like(x)
+        y_rows = self._new((R, cfg.d))
+        offsets = self._new(cfg.n_routed + 1, i32)
+        route_train(cfg, T, x, w["W_r"], w.get("b"), s["idx"], s["gates"], s["logits"], self.ws, stream=stream)
+        dispatch_rows(cfg, T, s["idx"], s["gates"], x, s["counts"], offsets, s["slot_pos"], s["x_rows"],
+                      s["gate_rows"], self.ws, stream=stream)
+        experts_train(self.routed, R, s["counts"], s["x_rows"], s["gate_rows"], w["W1"], w["W3"], w["W2"], y_rows,
+                      s["gu"], self.ws, stream=stream)
+        y_shared = None
+        if self.shared is not None:
+            s["shared_counts"] = torch.full((1,), T, dtype=i32, device=self.device)
+            s["shared_gu"] = self._new((T, 2 * self.shared.d_ff))
+            y_shared = self._new((T, cfg.d))
+            experts_train(self.shared, T, s["shared_counts"], x, None, w["Ws1"], w["Ws3"], w["Ws2"], y_shared,
+                          s["shared_gu"], self.ws, stream=stream)
+        combine(cfg, T, y_rows, s["slot_pos"], y_shared, y, stream=stream)
+        self.saved = s
+        return y
+
+    def backward(self, dy, accumulate=False, stream=None):
+        """dx of the last forward's tokens from dy [T, d]; the weights' gradients go to `grads`."""
+        if self.saved is None:
+            raise RuntimeError("backward() without a forward()")
+        cfg, w, g, s = self.cfg, self.w, self.grads, self.saved
+        T, k = s["x"].shape[0], cfg.top_k
+        if dy.shape != s["x"].shape:
+            raise ValueError(f"dy has shape {tuple(dy.shape)}, the forward's tokens {tuple(s['x'].shape)}")
+        R = T * k
+        opt = dict(grad_dtype=self.grad_dtype, accumulate=accumulate, stream=stream)
+        dy_rows, dx_rows = self._new((R, cfg.d)), self._new((R, cfg.d))
+        dgate_rows = self._new(R, torch.float32)
+        dx, dx_router, dx_shared = torch.empty_like(dy), torch.empty_like(dy), None
+        combine_backward(cfg, T, dy, s["slot_pos"], dy_rows, stream=stream)
+        experts_backward(self.routed, R, s["counts"], s["x_rows"], s["gate_rows"], w["W1"], w["W3"], w["W2"], s["gu"],
+                         dy_rows, dx_rows, dgate_rows, g["W1"], g["W3"], g["W2"], self.ws, **opt)
+        if self.shared is not None:
+            dx_shared = torch.empty_like(dy)
+            experts_backward(self.shared, T, s["shared_counts"], s["x"], None, w["Ws1"], w["Ws3"], w["Ws2"],
+                             s["shared_gu"], dy, dx_shared, None, g["Ws1"], g["Ws3"], g["Ws2"], self.ws, **opt)
+        route_backward(cfg, T, s["x"], w["W_r"], s["logits"], s["idx"], dgate_rows, s["slot_pos"], dx_router, g["W_r"],
+                       self.ws, **opt)
+        dispatch_backward(cfg, T, dx_rows, s["slot_pos"], dx_shared, dx_router, dx, stream=stream)
+        return dx
+
+    def clip(self, max_norm, group=None, stream=None):
+        """Scales the gradients in place to a global norm of at most max_norm;
+        returns the norm before (an fp32 tensor of one element). group: a
+        torch.distributed group over whose ranks the gradients are spread."""
+        grad_norm(self.grad_list, self.sumsq, self.clip_ws, stream=stream)
+        if group is not None:
+            import torch.distributed as dist
+            dist.all_reduce(self.sumsq, group=group)
+        grad_clip(self.grad_list, self.sumsq, max_norm, self.norm, stream=stream)
+        return self.norm
+
+    def balance(self, gamma, stream=None):
+        """The loss-free balancing step of the selection bias from the last forward's expert loads."""
+        s = self.saved
+        bias_update(self.cfg, s["x"].shape[0], s["counts"], gamma, self.w["b"], stream=stream)
