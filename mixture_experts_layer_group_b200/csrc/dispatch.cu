@@ -244,6 +244,50 @@ __global__ void __launch_bounds__(1024) dispatch_small_kernel(ChunkArgs ca, Scan
   chunk_pass<true>(a, gw);
 }
 
+// Grouped rows given by their counts (the expert entry points), in one CTA of
+// 512 threads: the counts are checked (non-negative, summing to T; otherwise
+// no group runs and the status says so), the tables of the row tiles follow,
+// and the unit counters of the GEMMs start at zero.
+__global__ void __launch_bounds__(512) group_tables_kernel(const int32_t* __restrict__ counts_in, ScanArgs a,
+                                                           unsigned* status, int* sched) {
+  const int tid = threadIdx.x;
+  if (tid < kSchedCounters) sched[tid] = 0;
+  const int c = tid < a.N ? counts_in[tid] : 0;
+  __shared__ unsigned long long sum;
+  __shared__ int negative;
+  if (tid == 0) {
+    sum = 0;
+    negative = 0;
+  }
+  __syncthreads();
+  if (c < 0) negative = 1;
+  unsigned long long part = c < 0 ? 0 : c;
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) part += __shfl_xor_sync(0xffffffffu, part, off);
+  if ((tid & 31) == 0) atomicAdd(&sum, part);  // whole numbers: the order does not matter
+  __syncthreads();
+  const bool ok = !negative && sum == (unsigned long long)a.T;
+  if (tid == 0) *status = ok ? 0u : (unsigned)MOE_DEV_BAD_EXPERT;
+  const int rows = ok ? c : 0, mt = (rows + a.bm - 1) / a.bm;
+  const int u1 = mt * ((a.F + a.bn1 - 1) / a.bn1), u2 = mt * ((a.d + a.bn2 - 1) / a.bn2);
+  int total, tot1, tot2;
+  const int off = block_exclusive_scan(rows, &total);
+  const int b1 = block_exclusive_scan(u1, &tot1);
+  const int b2 = block_exclusive_scan(u2, &tot2);
+  if (tid < a.N) {
+    a.grp_row0[tid] = off;
+    a.grp_rows[tid] = rows;
+    a.unit_base1[tid] = b1;
+    a.unit_base2[tid] = b2;
+  }
+  if (tid == 0) {
+    a.grp_row0[a.N] = 0;  // no shared MLP
+    a.grp_rows[a.N] = 0;
+    a.unit_base1[a.N] = a.unit_base1[a.N + 1] = tot1;
+    a.unit_base2[a.N] = a.unit_base2[a.N + 1] = tot2;
+  }
+}
+
 // x_perm[slot_pos[t, s]] = x[t] for every placed pair: a warp reads its
 // part of a token's row once and writes it to each of the token's k permuted
 // rows, so x is read from HBM once (a pair left at -1 by an invalid index is
@@ -336,12 +380,12 @@ cudaError_t launch_ep_reorder(const int32_t* counts, int W, int E, int64_t row_b
   return cudaGetLastError();
 }
 
-cudaError_t launch_unit_tables(const Problem& p, const int32_t* counts, const DispatchBuffers& db, int bm, int bn1,
-                               int bn2, cudaStream_t s) {
-  // the scan over a single "chunk" whose counts are the groups' row counts
-  ScanArgs sa{const_cast<int32_t*>(counts), 1, p.T, p.N, p.ns, p.F, p.nsF, p.d, bm, bn1, bn2,
-              db.counts, db.offsets, db.grp_row0, db.grp_rows, db.unit_base1, db.unit_base2};
-  scan_kernel<<<1, 1024, 0, s>>>(sa, db.chunk_base);
+cudaError_t launch_group_tables(const Problem& p, const int32_t* counts, const DispatchBuffers& db, int bm, int bn1,
+                                int bn2, int* sched, cudaStream_t s) {
+  ScanArgs sa{nullptr, 0, p.T, p.N, 0, p.F, 0, p.d, bm, bn1, bn2, nullptr, nullptr, db.grp_row0, db.grp_rows,
+              db.unit_base1, db.unit_base2};
+  static_assert(kMaxRouted <= 512, "one thread per group");
+  group_tables_kernel<<<1, 512, 0, s>>>(counts, sa, db.status, sched);
   return cudaGetLastError();
 }
 

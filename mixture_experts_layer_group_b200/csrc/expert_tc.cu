@@ -231,7 +231,6 @@ struct BwdParams : TcParams {
   int64_t ld_g;
   const __nv_bfloat16* gu;   // [R, 2 F] (kDh)
   float* part;               // [ceil(F / 32), R] partial gate gradients, or null (kDh)
-  int segments;              // K segments of k_routed each (kDx: 2; 1 elsewhere)
 };
 template <int MODE>
 struct ParamsOf {
@@ -404,12 +403,9 @@ MOE_DEV int load_volatile(const int* p) { return *reinterpret_cast<const volatil
 
 constexpr int kMnBox = 64 * kBK * 2;  // 8 KB: 64 weight columns x 64 k
 
-// K blocks of a unit: one segment of `seg` blocks, or the backward's several.
-template <int MODE, class P>
-MOE_DEV int k_blocks(const P& p, int seg) {
-  if constexpr (MODE == kDx) return seg * p.segments;
-  else return seg;
-}
+// K blocks of a unit: one segment of `seg` blocks, or two (dg W1, then du W3).
+template <int MODE>
+MOE_DEV int k_blocks(int seg) { return MODE == kDx ? 2 * seg : seg; }
 
 // Writes one 64-byte token-row segment (32 bf16 from the transpose tile),
 // or the first ncols of it at a ragged right edge.
@@ -583,7 +579,7 @@ __global__ void __launch_bounds__(Plan<FP8>::kThreads, 1)
         const bool shared = un.g == p.N;
         const int K = shared ? p.k_shared : p.k_routed;
         const int seg = (K + kBK - 1) / kBK;  // K blocks of a segment
-        const int nk = k_blocks<MODE>(p, seg);
+        const int nk = k_blocks<MODE>(seg);
         const int half_n = mma_n<FP8>(un.ntok) / 2;  // token rows per CTA
         // one token box per stage, the smallest of 32 / 64 / 128 rows that
         // covers this CTA's rows (the TMA engine's cost is per box, so a
@@ -671,7 +667,7 @@ __global__ void __launch_bounds__(Plan<FP8>::kThreads, 1)
         if (u < 0) break;
         const Unit un = decode_unit(p, u);
         const int K = un.g == p.N ? p.k_shared : p.k_routed;
-        const int nk = k_blocks<MODE>(p, (K + kBK - 1) / kBK);
+        const int nk = k_blocks<MODE>((K + kBK - 1) / kBK);
         const int n = mma_n<FP8>(un.ntok);
         const uint32_t idesc = idesc_bf16_f32(256, (uint32_t)n) | (is_bwd(MODE) ? kIdescAMn : 0u);
         uint32_t mask, base, stride;
@@ -1237,8 +1233,10 @@ cudaError_t launch_one(const typename ParamsOf<MODE>::type& prm, int max_units, 
 cudaError_t launch_expert_gemms_tc(const Problem& p, const GemmArgs& a, cudaStream_t s,
                                    cudaEvent_t between) {
   const int sms = device_sm_count();
-  cudaError_t err0 = cudaMemsetAsync(a.sched, 0, 2 * sizeof(int), s);
-  if (err0 != cudaSuccess) return err0;
+  if (!a.sched_clear) {
+    const cudaError_t err0 = cudaMemsetAsync(a.sched, 0, 2 * sizeof(int), s);
+    if (err0 != cudaSuccess) return err0;
+  }
   const bool fp8 = a.fp8;
   const int cm = fp8 ? Plan<true>::kChunk : Plan<false>::kChunk;  // token rows of a unit at most
   const int64_t chunks_bound = (p.R + cm - 1) / cm + p.N + (p.ns > 0 ? (p.T + cm - 1) / cm : 0);
@@ -1354,8 +1352,6 @@ int dgate_planes(const Problem& p) { return p.dtype == MOE_BF16 ? (p.F + 31) / 3
 
 cudaError_t launch_experts_backward_tc(const Problem& p, const ExpertsBwdArgs& a, cudaStream_t s) {
   const int sms = device_sm_count();
-  cudaError_t err = cudaMemsetAsync(a.sched, 0, 4 * sizeof(int), s);
-  if (err != cudaSuccess) return err;
   constexpr int cm = Plan<false>::kChunk;
   const int64_t chunks_bound = (p.R + cm - 1) / cm + p.N;
   auto grid_of = [&](int cols) {
@@ -1388,8 +1384,7 @@ cudaError_t launch_experts_backward_tc(const Problem& p, const ExpertsBwdArgs& a
   h.a_rows_routed = p.F;
   h.gu = (const __nv_bfloat16*)a.gu;
   h.part = a.dgate_rows ? a.dgate_part : nullptr;
-  h.segments = 1;
-  err = launch_one<kDh, false>(h, grid_of(p.F), s, false);
+  cudaError_t err = launch_one<kDh, false>(h, grid_of(p.F), s, false);
   if (err == cudaSuccess && a.dgate_rows) err = launch_dgate_reduce(a.dgate_part, dgate_planes(p), p.R, a.dgate_rows, s);
   if (err != cudaSuccess) return err;
 
@@ -1413,18 +1408,16 @@ cudaError_t launch_experts_backward_tc(const Problem& p, const ExpertsBwdArgs& a
     x.chunk_rows = cm;
     x.tok_rows_routed = x.out_rows_routed = p.R;
     x.a_rows_routed = p.d;
-    x.segments = 2;
     err = launch_one<kDx, false>(x, grid_of(p.d), s, false);
     if (err != cudaSuccess) return err;
   }
   if (!a.dW1) return cudaSuccess;
   WgradArgs w{};
-  w.mat[0] = {{a.dg, nullptr}, a.x_rows, a.dW1, p.F, p.d, p.F};
-  w.mat[1] = {{a.du, nullptr}, a.x_rows, a.dW3, p.F, p.d, p.F};
-  w.mat[2] = {{a.dy_rows, nullptr}, a.gh, a.dW2, p.d, p.F, p.d};
+  w.mat[0] = {a.dg, a.x_rows, a.dW1, p.F, p.d, p.F};
+  w.mat[1] = {a.du, a.x_rows, a.dW3, p.F, p.d, p.F};
+  w.mat[2] = {a.dy_rows, a.gh, a.dW2, p.d, p.F, p.d};
   w.nmat = 3;
   w.groups = p.N;
-  w.segments = 1;
   w.rows = p.R;
   w.grp_row0 = a.grp_row0;
   w.grp_rows = a.grp_rows;
@@ -1432,61 +1425,6 @@ cudaError_t launch_experts_backward_tc(const Problem& p, const ExpertsBwdArgs& a
   w.accumulate = a.accumulate;
   w.status = a.status;
   return launch_wgrad_tc(w, s);
-}
-
-// dx = (hi + lo) W_r as the two K segments of the dx GEMM over one group of T
-// rows (its "F" is N, its weights W_r twice), dW_r = (hi + lo)^T x as the two
-// segments of the weight-gradient kernel, the token ranges as its groups.
-cudaError_t launch_route_products_tc(const Problem& p, const RouteBwdArgs& a, cudaStream_t s) {
-  if (a.dx) {
-    cudaError_t err = cudaMemsetAsync(a.sched, 0, sizeof(int), s);
-    if (err != cudaSuccess) return err;
-    BwdParams x{};
-    bool ok = make_weight_tmap(&x.a0_routed, a.W_r, 1, p.N, p.d) && make_store_tmap(&x.o_routed, a.dx, p.T, p.d);
-    for (int i = 0; i < kTokMaps && ok; ++i) {
-      const uint64_t dims[2] = {(uint64_t)p.N, (uint64_t)p.T}, stride[1] = {(uint64_t)a.ld * 2};
-      const uint32_t box[2] = {(uint32_t)kBK, (uint32_t)(kTokBox << i)};
-      ok = make_tmap_nd(&x.b_routed[i], a.hi, 2, 2, dims, stride, box, 128, true) &&
-           make_tmap_nd(&x.b1[i], a.lo, 2, 2, dims, stride, box, 128, true);
-    }
-    if (!ok) return cudaErrorInvalidValue;
-    x.a1_routed = x.a0_routed;
-    x.unit_base = a.unit_base2;
-    x.grp_row0 = a.grp_row0;
-    x.grp_rows = a.grp_rows;
-    x.sched = a.sched;
-    x.N = 1;
-    x.k_routed = p.N;
-    x.cols_routed = p.d;
-    x.tile_cols = kTcBN2;
-    x.out_routed = (__nv_bfloat16*)a.dx;
-    x.ld_routed = p.d;
-    x.status = a.status;
-    x.chunk_rows = Plan<false>::kChunk;
-    x.tok_rows_routed = x.out_rows_routed = p.T;
-    x.a_rows_routed = p.d;
-    x.segments = 2;
-    const int64_t units = (p.T + kTcBM - 1) / kTcBM * ((p.d + kTcBN2 - 1) / kTcBN2);
-    const int sms = device_sm_count();
-    err = launch_one<kDx, false>(x, (int)(units < sms ? units : sms), s, false);
-    if (err != cudaSuccess) return err;
-  }
-  if (!a.dW_r) return cudaSuccess;
-  const bool split = a.splits > 1;
-  WgradArgs w{};
-  w.mat[0] = {{a.hi, a.lo}, a.x, split ? a.planes : a.dW_r, p.N, p.d, a.ld};
-  w.nmat = 1;
-  w.groups = a.splits;
-  w.segments = 2;
-  w.rows = p.T;
-  w.grp_row0 = a.split_row0;
-  w.grp_rows = a.split_rows;
-  w.grad_dtype = split ? (int)MOE_F32 : a.grad_dtype;
-  w.accumulate = !split && a.accumulate;
-  w.status = a.status;
-  const cudaError_t err = launch_wgrad_tc(w, s);
-  if (err != cudaSuccess || !split) return err;
-  return launch_join_planes(a.planes, a.splits, (int64_t)p.N * p.d, a.dW_r, a.grad_dtype, a.accumulate, s);
 }
 
 }  // namespace moe

@@ -110,11 +110,14 @@ cudaError_t launch_router(const Problem& p, const void* x, const void* W_r, cons
 cudaError_t launch_dispatch(const Problem& p, const DispatchBuffers& db, int bm, int bn1, int bn2,
                             cudaStream_t s);
 
-// Unit tables of the grouped GEMMs straight from per-group row counts
-// [p.N] (groups in order, rows contiguous): counts, offsets, grp_row0,
-// grp_rows and unit bases in db; db.chunk_base needs p.N ints of scratch.
-cudaError_t launch_unit_tables(const Problem& p, const int32_t* counts, const DispatchBuffers& db, int bm, int bn1,
-                               int bn2, cudaStream_t s);
+// Tables of the grouped GEMMs straight from per-group row counts [p.N]
+// (groups in order, rows contiguous): grp_row0, grp_rows and unit bases in db.
+// Counts that are negative or do not sum to p.T set MOE_DEV_BAD_EXPERT and
+// give empty groups; db.status and the kSchedCounters counters of `sched` are
+// cleared first.
+constexpr int kSchedCounters = 4;
+cudaError_t launch_group_tables(const Problem& p, const int32_t* counts, const DispatchBuffers& db, int bm, int bn1,
+                                int bn2, int* sched, cudaStream_t s);
 
 // Expert-parallel row reorder between source-major and expert-major order
 // of the blocks counts[W, E] (see ep_reorder_kernel).
@@ -145,6 +148,7 @@ struct GemmArgs {
   const float* gate_perm;
   unsigned* status;
   int* sched;           // [2] unit counters of the two tensor-core launches
+  bool sched_clear = false;  // they are zero already
   // FP8 expert weights: W1 .. Ws2 above hold the e4m3 codes (uint8, same
   // shapes) and these their UE8M0 scales, one byte per 128 x 128 block
   bool fp8 = false;
@@ -196,21 +200,22 @@ struct ExpertsBwdArgs {
   const int32_t* unit_base1;
   const int32_t* unit_base2;
   unsigned* status;
-  int* sched;              // [4]
+  int* sched;              // [kSchedCounters], zero
 };
-// Tensor-core weight gradients: for every group g and matrix i,
-// out[g][m][n] = sum over the group's rows r (and the segments s) of
-// A[s][r][m] B[r][n], bf16 operands, fp32 accumulation.
+// Tensor-core sums over rows (the weight gradients, and the router's dx): for
+// every group g and matrix i, out[g][m][n] = sum over the group's rows r of
+// A[r][m] B[r][n], bf16 operands, fp32 accumulation.
 struct WgradMatrix {
-  const void* A[2];  // [rows, M], row stride lda elements (a multiple of 8); one per segment
-  const void* B;     // [rows, N]
-  void* out;         // [groups, M, N]
-  int M, N;
+  const void* A;  // [rows, M], row stride lda elements (a multiple of 8)
+  const void* B;  // [rows, N]
+  void* out;      // [groups, M, N]
+  int64_t M;
+  int N;
   int64_t lda;
 };
 struct WgradArgs {
   WgradMatrix mat[3];
-  int nmat, groups, segments;
+  int nmat, groups;
   int64_t rows;
   const int32_t* grp_row0;
   const int32_t* grp_rows;
@@ -225,8 +230,18 @@ cudaError_t launch_experts_backward_simt(const Problem& p, const ExpertsBwdArgs&
 // dgate[r] = sum over the planes of part[plane][r], in order.
 cudaError_t launch_dgate_reduce(const float* part, int planes, int64_t rows, float* dgate, cudaStream_t s);
 
-// The gradient of the logits (see route_bwd.cu) and the tables of the two
-// products that follow.
+// The gradient of the logits (see route_bwd.cu), and the row tables of the
+// two products that follow: ints written to `tables` from the parameters.
+constexpr int kMaxRouteSplits = 16;
+enum RouteTable : int {
+  kRtRow0 = 0,                               // [2] one group of T rows (fp32 products) ...
+  kRtRows = 2,                               // [2]
+  kRtUnits = 4,                              // [3] ... and its unit table
+  kRtExperts = 7,                            // [1] N
+  kRtSplit0 = 8,                             // [kMaxRouteSplits] token ranges of the split dW_r
+  kRtSplitRows = kRtSplit0 + kMaxRouteSplits,
+  kRouteTables = kRtSplitRows + kMaxRouteSplits
+};
 struct RouteDzArgs {
   const float* logits;      // [T, N]
   const int32_t* idx;       // [T, k]
@@ -236,24 +251,19 @@ struct RouteDzArgs {
   int N, k, score_fn, normalize;
   float route_scale;
   unsigned* status;
-  float* dz;                // [T, N] fp32, or null: hi and lo instead
-  __nv_bfloat16* hi;
-  __nv_bfloat16* lo;
-  int64_t ld;
-  int32_t* grp_row0;
-  int32_t* grp_rows;
-  int32_t* unit_base;
-  int32_t units;
-  int32_t* split_row0;
-  int32_t* split_rows;
-  int splits;
+  float* dz;                // [T, ld] fp32 (zero past N), or null:
+  __nv_bfloat16* dz16;      // [T, ld]
+  __nv_bfloat16* dz16_t;    // [N, ld_t], or null when not needed
+  int64_t ld, ld_t;         // multiples of 8
+  int32_t* tables;
+  int32_t table_values[kRouteTables];
 };
 cudaError_t launch_route_dz(const RouteDzArgs& a, cudaStream_t s);
 // dW [elems] = sum of n fp32 planes, in order (elems a multiple of 4).
 cudaError_t launch_join_planes(const float* planes, int n, int64_t elems, void* dW, int grad_dtype, bool accumulate,
                                cudaStream_t s);
 
-// The router's two backward products from dz [T, N] fp32 (fp32 layers).
+// The router's two backward products from dz.
 struct RouteBwdArgs {
   const void* x;     // [T, d]
   const void* W_r;   // [N, d]
@@ -261,34 +271,23 @@ struct RouteBwdArgs {
   void* dW_r;        // [N, d] or null
   int grad_dtype;
   bool accumulate;
-  const int32_t* grp_row0;   // one group of T rows (unit tables as for the experts)
-  const int32_t* grp_rows;
-  const int32_t* unit_base2;
   unsigned* status;
-  int* sched;
-  // bf16 layers: dz as hi + lo [T, N] with row stride ld, and the row ranges
-  // and fp32 planes [splits, N, d] of the split weight gradient (splits > 1)
-  const __nv_bfloat16* hi;
-  const __nv_bfloat16* lo;
-  int64_t ld;
-  int splits;
-  const int32_t* split_row0;
-  const int32_t* split_rows;
-  float* planes;
+  const float* dz;   // as in RouteDzArgs
+  const __nv_bfloat16* dz16;
+  const __nv_bfloat16* dz16_t;
+  int64_t ld, ld_t;
+  const int32_t* tables;
+  int splits;        // token ranges of dW_r, summed from the planes when above 1
+  float* planes;     // [splits, N, d] fp32
 };
-constexpr int kMaxRouteSplits = 16;
 cudaError_t launch_route_products_tc(const Problem& p, const RouteBwdArgs& a, cudaStream_t s);
-cudaError_t launch_route_products_simt(const Problem& p, const RouteBwdArgs& a, const float* dz, cudaStream_t s);
+cudaError_t launch_route_products_simt(const Problem& p, const RouteBwdArgs& a, cudaStream_t s);
 
 // Entry-point helpers shared by the ABI's translation units (moe_abi.cu).
 moe_status make_group_problem(const moe_cfg* cfg, int64_t rows, Problem* p);
 moe_status cuda_fail(cudaError_t e);
 cudaError_t wait_host_outputs(const void* ws, cudaStream_t s);
 cudaError_t note_device_use(const void* ws, cudaStream_t s);
-// Copies the group counts into `out` if they are non-negative and sum to
-// `rows`; otherwise writes zeros (no group runs) and flags the status.
-cudaError_t launch_check_counts(const int32_t* counts, int E, int64_t rows, int32_t* out, unsigned* status,
-                                cudaStream_t s);
 inline size_t align256(size_t v) { return (v + 255) & ~size_t(255); }
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 template <typename T>

@@ -432,7 +432,7 @@ moe_status make_group_problem(const moe_cfg* cfg, int64_t rows, Problem* p) {
 namespace {
 
 struct GroupLayout {
-  size_t status, sched, counts_in, chunk_base, counts, offsets, grp_row0, grp_rows, unit_base1, unit_base2, h;
+  size_t status, sched, grp_row0, grp_rows, unit_base1, unit_base2, h;
   size_t total;
 };
 
@@ -447,10 +447,6 @@ GroupLayout make_group_layout(const Problem& p) {
   const size_t N = (size_t)p.N;
   L.status = take(256);
   L.sched = take(256);
-  L.counts_in = take(N * 4);
-  L.chunk_base = take(N * 4);
-  L.counts = take(N * 4);
-  L.offsets = take((N + 1) * 4);
   L.grp_row0 = take((N + 1) * 4);
   L.grp_rows = take((N + 1) * 4);
   L.unit_base1 = take((N + 2) * 4);
@@ -460,35 +456,7 @@ GroupLayout make_group_layout(const Problem& p) {
   return L;
 }
 
-// Copies the group counts into the workspace if they are non-negative and
-// sum to `rows`; otherwise writes zeros (no group runs) and flags the status.
-__global__ void check_counts_kernel(const int32_t* __restrict__ counts, int E, int64_t rows, int32_t* out,
-                                    unsigned* status) {
-  __shared__ unsigned long long total;
-  __shared__ int bad;
-  if (threadIdx.x == 0) {
-    total = 0;
-    bad = 0;
-  }
-  __syncthreads();
-  for (int e = threadIdx.x; e < E; e += blockDim.x) {
-    const int32_t c = counts[e];
-    if (c < 0) atomicExch(&bad, 1);
-    atomicAdd(&total, (unsigned long long)(c < 0 ? 0 : c));
-  }
-  __syncthreads();
-  const bool ok = !bad && total == (unsigned long long)rows;
-  for (int e = threadIdx.x; e < E; e += blockDim.x) out[e] = ok ? counts[e] : 0;
-  if (threadIdx.x == 0 && !ok) set_status(status, MOE_DEV_BAD_EXPERT);
-}
-
 }  // namespace
-
-cudaError_t launch_check_counts(const int32_t* counts, int E, int64_t rows, int32_t* out, unsigned* status,
-                                cudaStream_t s) {
-  check_counts_kernel<<<1, 256, 0, s>>>(counts, E, rows, out, status);
-  return cudaGetLastError();
-}
 
 // Configuration checks of the FP8 entry points.
 moe_status check_fp8_cfg(const Problem& p) {
@@ -601,21 +569,16 @@ static moe_status experts_device(const moe_cfg* cfg, int64_t rows, const int32_t
   cudaStream_t s = (cudaStream_t)stream;
   unsigned* status = at<unsigned>(ws, L.status);
   cudaError_t e = wait_host_outputs(ws, s);
-  if (e == cudaSuccess) e = cudaMemsetAsync(status, 0, 4, s);
-  if (e != cudaSuccess) return cuda_fail(e);
-  e = launch_check_counts(counts, p.N, rows, at<int32_t>(ws, L.counts_in), status, s);
   if (e != cudaSuccess) return cuda_fail(e);
   DispatchBuffers db{};
-  db.chunk_base = at<int32_t>(ws, L.chunk_base);
-  db.counts = at<int32_t>(ws, L.counts);
-  db.offsets = at<int32_t>(ws, L.offsets);
+  db.status = status;
   db.grp_row0 = at<int32_t>(ws, L.grp_row0);
   db.grp_rows = at<int32_t>(ws, L.grp_rows);
   db.unit_base1 = at<int32_t>(ws, L.unit_base1);
   db.unit_base2 = at<int32_t>(ws, L.unit_base2);
   const bool tc = p.dtype == MOE_BF16;
-  e = launch_unit_tables(p, at<int32_t>(ws, L.counts_in), db, tc ? kTcBM : kSimtBM, tc ? kTcBN1 : kSimtBN,
-                         tc ? kTcBN2 : kSimtBN, s);
+  e = launch_group_tables(p, counts, db, tc ? kTcBM : kSimtBM, tc ? kTcBN1 : kSimtBN, tc ? kTcBN2 : kSimtBN,
+                          at<int>(ws, L.sched), s);
   if (e != cudaSuccess) return cuda_fail(e);
   GemmArgs ga;
   ga.x = nullptr;
@@ -634,6 +597,7 @@ static moe_status experts_device(const moe_cfg* cfg, int64_t rows, const int32_t
   ga.gate_perm = gate_rows;
   ga.status = status;
   ga.sched = at<int>(ws, L.sched);
+  ga.sched_clear = true;
   ga.gu = gu;
   e = tc ? launch_expert_gemms_tc(p, ga, s, nullptr) : launch_expert_gemms_simt(p, ga, s, nullptr);
   if (e == cudaSuccess) e = note_device_use(ws, s);

@@ -7,12 +7,13 @@
 //   sigmoid             dz_j = ds_j s_j (1 - s_j)
 //   softmax             dz_j = s_j (ds_j - sum_S ds_i s_i)  (all experts; the
 //                       sum is zero for normalised gates)
-// The two products dx = dz W_r and dW_r = dz^T x run on the expert kernels.
-// bf16 layers: dz is passed as two bf16 terms hi + lo (16 bits of mantissa),
-// whose products are summed in fp32, so dz costs no visible rounding next to
-// the bf16 W_r, x and results; fp32 layers use fp32 throughout.
-#include <cfloat>
-
+// The two products dx = dz W_r and dW_r = dz^T x then run as sums over rows:
+// of dz^T and W_r (the experts), and of dz and x (the tokens). bf16 layers
+// round dz to bf16 for them, as the experts' dg and du are (one rounding per
+// term of sums kept in fp32); dz is written both ways. fp32 layers keep fp32.
+//
+// The kernel reads the logits once and writes dz twice (2 T N of each): a few
+// microseconds at any size here, next to the products.
 #include "common.cuh"
 #include "internal.h"
 
@@ -30,123 +31,115 @@ MOE_DEV float wmax(float v) {
   return v;
 }
 
-// Lane l holds experts 32 j + l, j < V; slot i of the token sits in lane i.
+constexpr int kDzTokens = 16;  // tokens of a CTA: 32-byte runs of the transposed dz
+constexpr int kDzWarps = 8;
+
+// One warp per token, two in turn. Lane l holds experts 32 j + l, j < V; slot
+// i of the token sits in lane i.
 template <int V>
-__global__ void __launch_bounds__(256) route_dz_kernel(RouteDzArgs a) {
-  if (blockIdx.x == 0 && threadIdx.x == 0) {
-    // tables of the products: one group of T rows, and the row ranges of the
-    // split weight gradient
-    a.grp_row0[0] = 0;
-    a.grp_rows[0] = (int32_t)a.T;
-    a.grp_row0[1] = 0;
-    a.grp_rows[1] = 0;
-    a.unit_base[0] = 0;
-    a.unit_base[1] = a.unit_base[2] = a.units;
-    for (int i = 0; i < a.splits; ++i) {
-      const int64_t lo = a.T * i / a.splits / 64 * 64, hi = i + 1 == a.splits ? a.T : a.T * (i + 1) / a.splits / 64 * 64;
-      a.split_row0[i] = (int32_t)lo;
-      a.split_rows[i] = (int32_t)(hi - lo);
-    }
-  }
+__global__ void __launch_bounds__(32 * kDzWarps) route_dz_kernel(const __grid_constant__ RouteDzArgs a) {
+  __shared__ __nv_bfloat16 tile[32 * V][kDzTokens + 2];  // [expert][token] (+2: rows start in different banks)
+  if (blockIdx.x == 0 && threadIdx.x < kRouteTables) a.tables[threadIdx.x] = a.table_values[threadIdx.x];
   const int lane = threadIdx.x & 31;
-  const int64_t t = (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
-  if (t >= a.T) return;
   const int N = a.N, k = a.k;
-  float s[V], om[V], ds[V];  // scores, 1 - sigmoid, gradient of the scores
-#pragma unroll
-  for (int j = 0; j < V; ++j) {
-    s[j] = 32 * j + lane < N ? a.logits[t * N + 32 * j + lane] : -INFINITY;
-    om[j] = 1.f;
-    ds[j] = 0.f;
-  }
-  if (a.score_fn == MOE_SOFTMAX) {
-    float m = -INFINITY;
-#pragma unroll
-    for (int j = 0; j < V; ++j) m = fmaxf(m, s[j]);
-    m = wmax(m);
-    float sum = 0.f;
+  const int64_t t0 = (int64_t)blockIdx.x * kDzTokens;
+  for (int w = threadIdx.x >> 5; w < kDzTokens; w += kDzWarps) {
+    const int64_t t = t0 + w;
+    if (t >= a.T) break;
+    float s[V], om[V], ds[V];  // scores, 1 - sigmoid, gradient of the scores
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-      s[j] = 32 * j + lane < N ? expf(s[j] - m) : 0.f;
-      sum += s[j];
+      s[j] = 32 * j + lane < N ? __ldg(a.logits + t * N + 32 * j + lane) : -INFINITY;
+      om[j] = 1.f;
+      ds[j] = 0.f;
     }
-    sum = wsum(sum);
-#pragma unroll
-    for (int j = 0; j < V; ++j) s[j] = s[j] / sum;
-  } else {
-#pragma unroll
-    for (int j = 0; j < V; ++j) {
-      const float z = s[j];
-      s[j] = 32 * j + lane < N ? 1.f / (1.f + expf(-z)) : 0.f;
-      om[j] = 1.f / (1.f + expf(z));
-    }
-  }
-  // this lane's slot: its expert (-1: none), whether it is the expert's first
-  // slot, and its rank among the token's distinct experts
-  int e = -1;
-  if (lane < k) {
-    e = a.idx[t * k + lane];
-    if (e < 0 || e >= N) {
+    // this lane's slot: its expert (-1: none) and logit, and whether it is the expert's first slot
+    int e = lane < k ? __ldg(a.idx + t * k + lane) : -1;
+    if (lane < k && (e < 0 || e >= N)) {
       set_status(a.status, MOE_DEV_BAD_EXPERT);
       e = -1;
     }
-  }
-  bool firsts = e >= 0;
-  for (int i = 0; i < k; ++i) {
-    const int ei = __shfl_sync(0xffffffffu, e, i);
-    if (i < lane && ei == e) firsts = false;
-  }
-  float dG = 0.f;
-  if (a.slot_pos) {
-    // the gradient of the slot's gate is that of the row the dispatch gave it:
-    // slot_pos lists the token's rows by ascending expert
-    int rank = 0;
-    for (int i = 0; i < k; ++i) {
-      const int ei = __shfl_sync(0xffffffffu, firsts ? e : -1, i);
-      rank += ei >= 0 && ei < e;
+    float my_s = e >= 0 ? __ldg(a.logits + t * N + e) : -INFINITY;
+    const unsigned same = __match_any_sync(0xffffffffu, e);
+    const bool firsts = e >= 0 && lane == __ffs(same) - 1;
+    float dG = 0.f;
+    if (a.slot_pos) {
+      // the gradient of the slot's gate is that of the row the dispatch gave it:
+      // slot_pos lists the token's rows by ascending expert
+      int rank = 0;
+      for (int i = 0; i < k; ++i) {
+        const int ei = __shfl_sync(0xffffffffu, firsts ? e : -1, i);
+        rank += ei >= 0 && ei < e;
+      }
+      if (firsts) {
+        const int32_t row = __ldg(a.slot_pos + t * k + rank);
+        if (row >= 0 && row < a.T * k) dG = __ldg(a.dgates + row);
+      }
+    } else if (e >= 0) {
+      dG = __ldg(a.dgates + t * k + lane);
     }
-    if (firsts) {
-      const int32_t row = a.slot_pos[t * k + rank];
-      if (row >= 0 && row < a.T * k) dG = a.dgates[row];
-    }
-  } else if (e >= 0) {
-    dG = a.dgates[t * k + lane];
-  }
-  float Z = 0.f, dot = 0.f, my_s = 0.f;
-  for (int i = 0; i < k; ++i) {
-    const int ei = __shfl_sync(0xffffffffu, e, i);
-    if (ei < 0) continue;
-    float v = 0.f;
+    if (a.score_fn == MOE_SOFTMAX) {
+      float m = -INFINITY;
 #pragma unroll
-    for (int j = 0; j < V; ++j)
-      if (j == ei >> 5) v = s[j];
-    v = __shfl_sync(0xffffffffu, v, ei & 31);
-    Z += v;
-    dot = fmaf(__shfl_sync(0xffffffffu, dG, i), v, dot);
-    if (lane == i) my_s = v;
-  }
-  const float my_ds = a.normalize ? a.route_scale / Z * (dG - dot / Z) : a.route_scale * dG;
-  for (int i = 0; i < k; ++i) {
-    const int ei = __shfl_sync(0xffffffffu, e, i);
-    const float v = __shfl_sync(0xffffffffu, my_ds, i);
-    if (ei < 0 || lane != (ei & 31)) continue;
+      for (int j = 0; j < V; ++j) m = fmaxf(m, s[j]);
+      m = wmax(m);
+      float sum = 0.f;
 #pragma unroll
-    for (int j = 0; j < V; ++j)
-      if (j == ei >> 5) ds[j] += v;
-  }
-  const float mean = a.score_fn == MOE_SOFTMAX && !a.normalize ? wsum(e >= 0 ? my_ds * my_s : 0.f) : 0.f;
+      for (int j = 0; j < V; ++j) {
+        s[j] = 32 * j + lane < N ? expf(s[j] - m) : 0.f;
+        sum += s[j];
+      }
+      const float inv = 1.f / wsum(sum);
 #pragma unroll
-  for (int j = 0; j < V; ++j) {
-    const int col = 32 * j + lane;
-    if (col >= N) continue;
-    const float dz = a.score_fn == MOE_SOFTMAX ? s[j] * (ds[j] - mean) : ds[j] * s[j] * om[j];
-    if (a.dz) {
-      a.dz[t * N + col] = dz;
+      for (int j = 0; j < V; ++j) s[j] *= inv;
+      my_s = e >= 0 ? expf(my_s - m) * inv : 0.f;
     } else {
-      const __nv_bfloat16 hi = __float2bfloat16_rn(dz);
-      a.hi[t * a.ld + col] = hi;
-      a.lo[t * a.ld + col] = __float2bfloat16_rn(dz - __bfloat162float(hi));
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        const float z = s[j];
+        s[j] = 32 * j + lane < N ? 1.f / (1.f + expf(-z)) : 0.f;
+        om[j] = 1.f / (1.f + expf(z));  // 1 - s without its cancellation
+      }
+      my_s = e >= 0 ? 1.f / (1.f + expf(-my_s)) : 0.f;
     }
+    float my_ds = a.route_scale * dG;
+    float mean = 0.f;  // sum of ds_i s_i over the slots (zero for normalised gates)
+    if (a.normalize) {
+      const float Z = wsum(my_s), dot = wsum(dG * my_s);
+      my_ds = a.route_scale / Z * (dG - dot / Z);
+    } else if (a.score_fn == MOE_SOFTMAX) {
+      mean = wsum(my_ds * my_s);
+    }
+    for (int i = 0; i < k; ++i) {
+      const int ei = __shfl_sync(0xffffffffu, e, i);
+      const float v = __shfl_sync(0xffffffffu, my_ds, i);
+      if (ei < 0 || lane != (ei & 31)) continue;
+#pragma unroll
+      for (int j = 0; j < V; ++j)
+        if (j == ei >> 5) ds[j] += v;
+    }
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      const int col = 32 * j + lane;
+      const float dz = a.score_fn == MOE_SOFTMAX ? s[j] * (ds[j] - mean) : ds[j] * s[j] * om[j];
+      if (a.dz) {
+        // (columns N .. ld - 1 are zero)
+        if (col < a.ld) a.dz[t * a.ld + col] = col < N ? dz : 0.f;
+      } else if (col < N) {
+        const __nv_bfloat16 v = __float2bfloat16_rn(dz);
+        a.dz16[t * a.ld + col] = v;
+        tile[col][w] = v;
+      }
+    }
+  }
+  if (a.dz || !a.dz16_t) return;
+  __syncthreads();
+  for (int i = threadIdx.x; i < N * (kDzTokens / 2); i += blockDim.x) {
+    const int n = i / (kDzTokens / 2), c = i % (kDzTokens / 2) * 2;
+    // a pair that starts inside T may end one past it, in the row's padding
+    if (t0 + c < a.T)
+      *reinterpret_cast<uint32_t*>(a.dz16_t + (int64_t)n * a.ld_t + t0 + c) =
+          *reinterpret_cast<const uint32_t*>(&tile[n][c]);
   }
 }
 
@@ -181,14 +174,13 @@ __global__ void __launch_bounds__(256) join_planes_kernel(const float4* __restri
 }  // namespace
 
 cudaError_t launch_route_dz(const RouteDzArgs& a, cudaStream_t s) {
-  const int warps = 8;
-  const unsigned blocks = (unsigned)((a.T + warps - 1) / warps);
-  const int V = (a.N + 31) / 32;
-  if (V <= 1) route_dz_kernel<1><<<blocks, 32 * warps, 0, s>>>(a);
-  else if (V <= 2) route_dz_kernel<2><<<blocks, 32 * warps, 0, s>>>(a);
-  else if (V <= 4) route_dz_kernel<4><<<blocks, 32 * warps, 0, s>>>(a);
-  else if (V <= 8) route_dz_kernel<8><<<blocks, 32 * warps, 0, s>>>(a);
-  else route_dz_kernel<16><<<blocks, 32 * warps, 0, s>>>(a);
+  const unsigned blocks = (unsigned)((a.T + kDzTokens - 1) / kDzTokens);
+  const int V = (a.N + 31) / 32, threads = 32 * kDzWarps;
+  if (V <= 1) route_dz_kernel<1><<<blocks, threads, 0, s>>>(a);
+  else if (V <= 2) route_dz_kernel<2><<<blocks, threads, 0, s>>>(a);
+  else if (V <= 4) route_dz_kernel<4><<<blocks, threads, 0, s>>>(a);
+  else if (V <= 8) route_dz_kernel<8><<<blocks, threads, 0, s>>>(a);
+  else route_dz_kernel<16><<<blocks, threads, 0, s>>>(a);
   return cudaGetLastError();
 }
 

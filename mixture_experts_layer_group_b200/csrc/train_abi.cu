@@ -8,7 +8,7 @@ namespace moe {
 namespace {
 
 struct BwdLayout {
-  size_t status, sched, counts_in, chunk_base, counts, offsets, grp_row0, grp_rows, unit_base1, unit_base2;
+  size_t status, sched, grp_row0, grp_rows, unit_base1, unit_base2;
   size_t dg, du, gh, part;
   size_t total;
 };
@@ -24,10 +24,6 @@ BwdLayout make_bwd_layout(const Problem& p) {
   const size_t N = (size_t)p.N, rf = (size_t)p.R * p.F * p.elem;
   L.status = take(256);  // first, as in every workspace of the library
   L.sched = take(256);
-  L.counts_in = take(N * 4);
-  L.chunk_base = take(N * 4);
-  L.counts = take(N * 4);
-  L.offsets = take((N + 1) * 4);
   L.grp_row0 = take((N + 1) * 4);
   L.grp_rows = take((N + 1) * 4);
   L.unit_base1 = take((N + 2) * 4);
@@ -40,13 +36,13 @@ BwdLayout make_bwd_layout(const Problem& p) {
   return L;
 }
 
-// The router's products: row tables, the logits' gradient (fp32, or two bf16
-// terms of ld columns) and the planes of a split weight gradient.
+// The router's products: row tables, the logits' gradient (fp32, or bf16 by
+// token and by expert) and the planes of a split weight gradient.
 struct RouteLayout {
-  size_t status, sched, grp_row0, grp_rows, unit_base, split_row0, split_rows, dz, lo, planes;
+  size_t status, tables, dz, dz_t, planes;
   size_t total;
   int splits;
-  int64_t ld;
+  int64_t ld, ld_t;
 };
 
 RouteLayout make_route_layout(const Problem& p) {
@@ -57,9 +53,11 @@ RouteLayout make_route_layout(const Problem& p) {
     off = align256(off + bytes);
     return at;
   };
+  const bool tc = p.dtype == MOE_BF16;
   L.ld = (p.N + 7) / 8 * 8;
+  L.ld_t = (p.T + 7) / 8 * 8;
   L.splits = 1;
-  if (p.dtype == MOE_BF16) {
+  if (tc) {
     // dW_r is N x d summed over all tokens: few tiles with a long sum. The
     // tokens are split so that about one tile per CTA pair runs at a time,
     // each over 256 tokens or more.
@@ -70,14 +68,9 @@ RouteLayout make_route_layout(const Problem& p) {
     if (n > 1) L.splits = (int)n;
   }
   L.status = take(256);
-  L.sched = take(256);
-  L.grp_row0 = take(8);
-  L.grp_rows = take(8);
-  L.unit_base = take(12);
-  L.split_row0 = take(kMaxRouteSplits * 4);
-  L.split_rows = take(kMaxRouteSplits * 4);
-  L.dz = take(p.dtype == MOE_BF16 ? (size_t)p.T * L.ld * 2 : (size_t)p.T * p.N * 4);
-  L.lo = take(p.dtype == MOE_BF16 ? (size_t)p.T * L.ld * 2 : 0);
+  L.tables = take(kRouteTables * 4);
+  L.dz = take((size_t)p.T * L.ld * p.elem);
+  L.dz_t = take(tc ? (size_t)p.N * L.ld_t * 2 : 0);
   L.planes = take(L.splits > 1 ? (size_t)L.splits * p.N * p.d * 4 : 0);
   L.total = off;
   return L;
@@ -144,20 +137,16 @@ moe_status moe_experts_backward(const moe_cfg* cfg, int64_t rows, const int32_t*
   if ((st = check_workspace(ws, ws_bytes, L.total)) != MOE_OK) return st;
   unsigned* status = at<unsigned>(ws, L.status);
   cudaError_t e = wait_host_outputs(ws, s);
-  if (e == cudaSuccess) e = cudaMemsetAsync(status, 0, 4, s);
-  if (e == cudaSuccess) e = launch_check_counts(counts, p.N, rows, at<int32_t>(ws, L.counts_in), status, s);
   if (e != cudaSuccess) return cuda_fail(e);
   DispatchBuffers db{};
-  db.chunk_base = at<int32_t>(ws, L.chunk_base);
-  db.counts = at<int32_t>(ws, L.counts);
-  db.offsets = at<int32_t>(ws, L.offsets);
+  db.status = status;
   db.grp_row0 = at<int32_t>(ws, L.grp_row0);
   db.grp_rows = at<int32_t>(ws, L.grp_rows);
   db.unit_base1 = at<int32_t>(ws, L.unit_base1);
   db.unit_base2 = at<int32_t>(ws, L.unit_base2);
   const bool tc = p.dtype == MOE_BF16;
-  e = launch_unit_tables(p, at<int32_t>(ws, L.counts_in), db, tc ? kTcBM : kSimtBM, tc ? kTcBN2 : kSimtBN,
-                         tc ? kTcBN2 : kSimtBN, s);
+  e = launch_group_tables(p, counts, db, tc ? kTcBM : kSimtBM, tc ? kTcBN2 : kSimtBN, tc ? kTcBN2 : kSimtBN,
+                          at<int>(ws, L.sched), s);
   if (e != cudaSuccess) return cuda_fail(e);
   ExpertsBwdArgs a{};
   a.x_rows = x_rows;
@@ -248,8 +237,7 @@ moe_status moe_route_backward(const moe_cfg* cfg, int64_t T, const void* x, cons
   if (e == cudaSuccess) e = cudaMemsetAsync(status, 0, 4, s);
   if (e != cudaSuccess) return cuda_fail(e);
   const bool tc = p.dtype == MOE_BF16;
-  const int bm = tc ? kTcBM : kSimtBM, bn = tc ? kTcBN2 : kSimtBN;
-  const int64_t units = (T + bm - 1) / bm * ((p.d + bn - 1) / bn);
+  const int64_t units = (T + kSimtBM - 1) / kSimtBM * ((p.d + kSimtBN - 1) / kSimtBN);  // fp32 row tiles
   if (units > (1ll << 31) - 1) return MOE_ERR_UNSUPPORTED;
   RouteDzArgs z{};
   z.logits = logits;
@@ -264,16 +252,20 @@ moe_status moe_route_backward(const moe_cfg* cfg, int64_t T, const void* x, cons
   z.route_scale = p.route_scale;
   z.status = status;
   z.dz = tc ? nullptr : at<float>(ws, L.dz);
-  z.hi = at<__nv_bfloat16>(ws, L.dz);
-  z.lo = at<__nv_bfloat16>(ws, L.lo);
+  z.dz16 = at<__nv_bfloat16>(ws, L.dz);
+  z.dz16_t = tc && dx ? at<__nv_bfloat16>(ws, L.dz_t) : nullptr;
   z.ld = L.ld;
-  z.grp_row0 = at<int32_t>(ws, L.grp_row0);
-  z.grp_rows = at<int32_t>(ws, L.grp_rows);
-  z.unit_base = at<int32_t>(ws, L.unit_base);
-  z.units = (int32_t)units;
-  z.split_row0 = at<int32_t>(ws, L.split_row0);
-  z.split_rows = at<int32_t>(ws, L.split_rows);
-  z.splits = L.splits;
+  z.ld_t = L.ld_t;
+  z.tables = at<int32_t>(ws, L.tables);
+  int32_t* v = z.table_values;
+  v[kRtRows] = (int32_t)T;
+  v[kRtUnits + 1] = v[kRtUnits + 2] = (int32_t)units;
+  v[kRtExperts] = p.N;
+  for (int i = 0; i < L.splits; ++i) {
+    const int64_t lo = T * i / L.splits / 64 * 64, hi = i + 1 == L.splits ? T : T * (i + 1) / L.splits / 64 * 64;
+    v[kRtSplit0 + i] = (int32_t)lo;
+    v[kRtSplitRows + i] = (int32_t)(hi - lo);
+  }
   if ((e = launch_route_dz(z, s)) != cudaSuccess) return cuda_fail(e);
   RouteBwdArgs a{};
   a.x = x;
@@ -282,19 +274,16 @@ moe_status moe_route_backward(const moe_cfg* cfg, int64_t T, const void* x, cons
   a.dW_r = dW_r;
   a.grad_dtype = grad_dtype;
   a.accumulate = accumulate != 0;
-  a.grp_row0 = z.grp_row0;
-  a.grp_rows = z.grp_rows;
-  a.unit_base2 = z.unit_base;
   a.status = status;
-  a.sched = at<int>(ws, L.sched);
-  a.hi = z.hi;
-  a.lo = z.lo;
+  a.dz = z.dz;
+  a.dz16 = z.dz16;
+  a.dz16_t = z.dz16_t;
   a.ld = L.ld;
+  a.ld_t = L.ld_t;
+  a.tables = z.tables;
   a.splits = L.splits;
-  a.split_row0 = z.split_row0;
-  a.split_rows = z.split_rows;
   a.planes = at<float>(ws, L.planes);
-  e = tc ? launch_route_products_tc(p, a, s) : launch_route_products_simt(p, a, z.dz, s);
+  e = tc ? launch_route_products_tc(p, a, s) : launch_route_products_simt(p, a, s);
   if (e == cudaSuccess) e = note_device_use(ws, s);
   return e == cudaSuccess ? MOE_OK : cuda_fail(e);
 }

@@ -16,53 +16,89 @@
 namespace moe {
 namespace {
 
-constexpr int kBM = kSimtBM, kBN = kSimtBN, kBK = 16;
+constexpr int kBM = kSimtBM, kBN = kSimtBN, kBK = 32;
 constexpr int kThreads = 256;  // 16 x 16 threads, 4 x 4 outputs each
-constexpr int kPad = 4;
+constexpr int kVecs = kBM * kBK / 4 / kThreads;  // 16-byte loads per thread, operand and K step
+static_assert(kBM == kBN && kVecs * kThreads * 4 == kBM * kBK, "both operands load alike");
 
-// A strided operand: element (r, k) at p[r * rs + k * ks], one stride 1.
+// A strided operand: element (r, k) at p[r * rs + k * ks] for r < rows and
+// k < ks_len, zero elsewhere. One of the strides is 1, the other and the
+// bound along the unit stride are multiples of 4, so four consecutive
+// elements load as one aligned vector.
 struct Operand {
   const float* p;
-  int64_t rs, ks;
+  int64_t rs, ks, rows, len;
 };
 
+// Two buffers of a 32 x 64 block of each operand, [k][r]. The 16-byte column
+// groups of row k are permuted by k / 4, so that the four rows a k-contiguous
+// vector is spread over, and the reads along a row, hit all banks.
 struct Tile {
-  float a[kBK][kBM + kPad];
-  float b[kBK][kBN + kPad];
+  float a[2][kBK][kBM];
+  float b[2][kBK][kBN];
 };
+MOE_DEV int swz(int k, int r) { return r ^ (((k >> 2) & 7) << 2); }
 
-// A 64 x 16 block of an operand into sm[k][r]; rows at or past `rows` and k
-// at or past `K` read as zero. Threads run along the contiguous index.
-MOE_DEV void load_block(float (&sm)[kBK][kBM + kPad], const Operand& o, int64_t r0, int64_t rows, int64_t k0,
-                        int64_t K) {
-  const bool along_k = o.ks == 1;
+MOE_DEV void fetch(const Operand& o, int64_t r0, int64_t k0, float4 (&v)[kVecs]) {
 #pragma unroll
-  for (int i = 0; i < kBM * kBK / kThreads; ++i) {
+  for (int i = 0; i < kVecs; ++i) {
     const int t = threadIdx.x + i * kThreads;
-    const int r = along_k ? t / kBK : t % kBM, k = along_k ? t % kBK : t / kBM;
-    const bool in = r0 + r < rows && k0 + k < K;
-    sm[k][r] = in ? o.p[(r0 + r) * o.rs + (k0 + k) * o.ks] : 0.f;
+    const int64_t r = r0 + (o.ks == 1 ? t / (kBK / 4) : t % (kBM / 4) * 4);
+    const int64_t k = k0 + (o.ks == 1 ? t % (kBK / 4) * 4 : t / (kBM / 4));
+    v[i] = r < o.rows && k < o.len ? __ldg(reinterpret_cast<const float4*>(o.p + r * o.rs + k * o.ks))
+                                   : make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+}
+MOE_DEV void put(float (&sm)[kBK][kBM], bool along_k, const float4 (&v)[kVecs]) {
+#pragma unroll
+  for (int i = 0; i < kVecs; ++i) {
+    const int t = threadIdx.x + i * kThreads;
+    if (along_k) {
+      const int r = t / (kBK / 4), k = t % (kBK / 4) * 4;
+      sm[k][swz(k, r)] = v[i].x;
+      sm[k + 1][swz(k, r)] = v[i].y;
+      sm[k + 2][swz(k, r)] = v[i].z;
+      sm[k + 3][swz(k, r)] = v[i].w;
+    } else {
+      const int r = t % (kBM / 4) * 4, k = t / (kBM / 4);
+      *reinterpret_cast<float4*>(&sm[k][swz(k, r)]) = v[i];
+    }
   }
 }
 
-// acc[i][j] += sum_k A(m0 + 4 ty + i, k) B(n0 + 4 tx + j, k).
-MOE_DEV void gemm_tile(Tile& sm, const Operand& A, int64_t m0, int64_t M, const Operand& B, int64_t n0, int64_t N,
-                       int64_t K, float (&acc)[4][4]) {
+// acc[i][j] += sum_{k < K} A(m0 + 4 ty + i, k) B(n0 + 4 tx + j, k). The next
+// block's loads are in flight while a block is multiplied.
+MOE_DEV void gemm_tile(Tile& sm, const Operand& A, int64_t m0, const Operand& B, int64_t n0, int64_t K,
+                       float (&acc)[4][4]) {
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  for (int64_t k0 = 0; k0 < K; k0 += kBK) {
+  if (K <= 0) return;
+  float4 va[kVecs], vb[kVecs];
+  fetch(A, m0, 0, va);
+  fetch(B, n0, 0, vb);
+  __syncthreads();  // the buffers' last readers are done
+  put(sm.a[0], A.ks == 1, va);
+  put(sm.b[0], B.ks == 1, vb);
+  int buf = 0;
+  for (int64_t k0 = 0; k0 < K; k0 += kBK, buf ^= 1) {
     __syncthreads();
-    load_block(sm.a, A, m0, M, k0, K);
-    load_block(sm.b, B, n0, N, k0, K);
-    __syncthreads();
+    const bool more = k0 + kBK < K;
+    if (more) {
+      fetch(A, m0, k0 + kBK, va);
+      fetch(B, n0, k0 + kBK, vb);
+    }
 #pragma unroll
     for (int kk = 0; kk < kBK; ++kk) {
-      const float4 a4 = *reinterpret_cast<const float4*>(&sm.a[kk][4 * ty]);
-      const float4 b4 = *reinterpret_cast<const float4*>(&sm.b[kk][4 * tx]);
+      const float4 a4 = *reinterpret_cast<const float4*>(&sm.a[buf][kk][swz(kk, 4 * ty)]);
+      const float4 b4 = *reinterpret_cast<const float4*>(&sm.b[buf][kk][swz(kk, 4 * tx)]);
       const float a[4] = {a4.x, a4.y, a4.z, a4.w}, b[4] = {b4.x, b4.y, b4.z, b4.w};
 #pragma unroll
       for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(a[i], b[j], acc[i][j]);
+    }
+    if (more) {
+      put(sm.a[buf ^ 1], A.ks == 1, va);
+      put(sm.b[buf ^ 1], B.ks == 1, vb);
     }
   }
 }
@@ -113,8 +149,8 @@ __global__ void __launch_bounds__(kThreads) dh_simt_kernel(DhParams p) {
     const int rows = p.gr.grp_rows[g];
     const int64_t row0 = p.gr.grp_row0[g];
     float acc[4][4] = {};
-    gemm_tile(sm, Operand{p.dy + row0 * p.d, p.d, 1}, (int64_t)m * kBM, rows,
-              Operand{p.W2 + (int64_t)g * p.d * p.F, 1, p.F}, (int64_t)f * kBN, p.F, p.d, acc);
+    gemm_tile(sm, Operand{p.dy + row0 * p.d, p.d, 1, rows, p.d}, (int64_t)m * kBM,
+              Operand{p.W2 + (int64_t)g * p.d * p.F, 1, p.F, p.F, p.d}, (int64_t)f * kBN, p.d, acc);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int r = m * kBM + 4 * ty + i;
@@ -142,12 +178,13 @@ __global__ void __launch_bounds__(kThreads) dh_simt_kernel(DhParams p) {
 
 struct DxParams {
   Groups gr;
-  const float* d0;  // [R, F]: dg | dz
+  const float* d0;  // [R, F]: dg | dz (row stride ld)
   const float* d1;  // [R, F]: du | null
   const float* W0;  // [N, F, d]: W1 | W_r
   const float* W1;  // [N, F, d]: W3 | null
   float* dx;        // [R, d]
   int d, F;
+  int64_t ld;       // a multiple of 4; columns F .. ld - 1 are zero
 };
 
 __global__ void __launch_bounds__(kThreads) dx_simt_kernel(DxParams p) {
@@ -160,11 +197,11 @@ __global__ void __launch_bounds__(kThreads) dx_simt_kernel(DxParams p) {
     const int rows = p.gr.grp_rows[g];
     const int64_t row0 = p.gr.grp_row0[g], w0 = (int64_t)g * p.F * p.d;
     float acc[4][4] = {};
-    gemm_tile(sm, Operand{p.d0 + row0 * p.F, p.F, 1}, (int64_t)m * kBM, rows, Operand{p.W0 + w0, 1, p.d},
-              (int64_t)f * kBN, p.d, p.F, acc);
+    gemm_tile(sm, Operand{p.d0 + row0 * p.ld, p.ld, 1, rows, p.ld}, (int64_t)m * kBM,
+              Operand{p.W0 + w0, 1, p.d, p.d, p.F}, (int64_t)f * kBN, p.F, acc);
     if (p.d1)
-      gemm_tile(sm, Operand{p.d1 + row0 * p.F, p.F, 1}, (int64_t)m * kBM, rows, Operand{p.W1 + w0, 1, p.d},
-                (int64_t)f * kBN, p.d, p.F, acc);
+      gemm_tile(sm, Operand{p.d1 + row0 * p.ld, p.ld, 1, rows, p.ld}, (int64_t)m * kBM,
+                Operand{p.W1 + w0, 1, p.d, p.d, p.F}, (int64_t)f * kBN, p.F, acc);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int r = m * kBM + 4 * ty + i;
@@ -180,10 +217,11 @@ __global__ void __launch_bounds__(kThreads) dx_simt_kernel(DxParams p) {
 
 // dW[g][m][n] = sum over the rows r of group g of A[r][m] B[r][n].
 struct DwMatrix {
-  const float* A;  // [R, M]
+  const float* A;  // [R, M], row stride lda (a multiple of 4; columns M .. lda - 1 are zero)
   const float* B;  // [R, N]
   float* out;      // [groups, M, N]
   int M, N;
+  int64_t lda;
 };
 struct DwParams {
   DwMatrix mat[3];
@@ -212,8 +250,9 @@ __global__ void __launch_bounds__(kThreads) dw_simt_kernel(DwParams p, int64_t u
     const int64_t m0 = local / nt * kBM, n0 = local % nt * kBN;
     const int64_t row0 = p.grp_row0[g];
     float acc[4][4] = {};
-    gemm_tile(sm, Operand{x.A + row0 * x.M, 1, x.M}, m0, x.M, Operand{x.B + row0 * x.N, 1, x.N}, n0, x.N,
-              p.grp_rows[g], acc);
+    const int rows = p.grp_rows[g];
+    gemm_tile(sm, Operand{x.A + row0 * x.lda, 1, x.lda, x.lda, rows}, m0,
+              Operand{x.B + row0 * x.N, 1, x.N, x.N, rows}, n0, rows, acc);
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -267,15 +306,15 @@ cudaError_t launch_experts_backward_simt(const Problem& p, const ExpertsBwdArgs&
   if (e == cudaSuccess && a.dgate_rows) e = launch_dgate_reduce(a.dgate_part, dgate_planes(p), p.R, a.dgate_rows, s);
   if (e == cudaSuccess && a.dx_rows) {
     DxParams x{g2, (const float*)a.dg, (const float*)a.du, (const float*)a.W1, (const float*)a.W3, (float*)a.dx_rows,
-               p.d, p.F};
+               p.d, p.F, p.F};
     dx_simt_kernel<<<grid, kThreads, 0, s>>>(x);
     e = cudaGetLastError();
   }
   if (e == cudaSuccess && a.dW1) {
     DwParams w{};
-    w.mat[0] = {(const float*)a.dg, (const float*)a.x_rows, (float*)a.dW1, p.F, p.d};
-    w.mat[1] = {(const float*)a.du, (const float*)a.x_rows, (float*)a.dW3, p.F, p.d};
-    w.mat[2] = {(const float*)a.dy_rows, (const float*)a.gh, (float*)a.dW2, p.d, p.F};
+    w.mat[0] = {(const float*)a.dg, (const float*)a.x_rows, (float*)a.dW1, p.F, p.d, p.F};
+    w.mat[1] = {(const float*)a.du, (const float*)a.x_rows, (float*)a.dW3, p.F, p.d, p.F};
+    w.mat[2] = {(const float*)a.dy_rows, (const float*)a.gh, (float*)a.dW2, p.d, p.F, p.d};
     w.nmat = 3;
     w.groups = p.N;
     w.grp_row0 = a.grp_row0;
@@ -286,21 +325,23 @@ cudaError_t launch_experts_backward_simt(const Problem& p, const ExpertsBwdArgs&
   return e;
 }
 
-cudaError_t launch_route_products_simt(const Problem& p, const RouteBwdArgs& a, const float* dz, cudaStream_t s) {
+cudaError_t launch_route_products_simt(const Problem& p, const RouteBwdArgs& a, cudaStream_t s) {
+  const int32_t* row0 = a.tables + kRtRow0;
+  const int32_t* rows = a.tables + kRtRows;
   cudaError_t e = cudaSuccess;
   if (a.dx) {
-    DxParams x{Groups{a.unit_base2, a.grp_row0, a.grp_rows, 1}, dz, nullptr, (const float*)a.W_r, nullptr,
-               (float*)a.dx, p.d, p.N};
+    DxParams x{Groups{a.tables + kRtUnits, row0, rows, 1}, a.dz, nullptr, (const float*)a.W_r, nullptr,
+               (float*)a.dx, p.d, p.N, a.ld};
     dx_simt_kernel<<<device_sm_count() * 6, kThreads, 0, s>>>(x);
     e = cudaGetLastError();
   }
   if (e == cudaSuccess && a.dW_r) {
     DwParams w{};
-    w.mat[0] = {dz, (const float*)a.x, (float*)a.dW_r, p.N, p.d};
+    w.mat[0] = {a.dz, (const float*)a.x, (float*)a.dW_r, p.N, p.d, a.ld};
     w.nmat = 1;
     w.groups = 1;
-    w.grp_row0 = a.grp_row0;
-    w.grp_rows = a.grp_rows;
+    w.grp_row0 = row0;
+    w.grp_rows = rows;
     w.accumulate = a.accumulate;
     e = launch_dw(w, s);
   }

@@ -1,7 +1,7 @@
 // Weight gradients on the tensor cores: dW[g][m][n] = sum over the rows r of
 // group g of A[r][m] B[r][n], for several matrices in one launch (the
 // experts' dW1 = dg^T x, dW3 = du^T x, dW2 = dy^T (gate h); the router's
-// dW_r = dz^T x). Both operands are row-major with the rows as the reduction,
+// dW_r = dz^T x, and its dx = (dz^T)^T W_r over the experts as rows). Both operands are row-major with the rows as the reduction,
 // so both are MN-major tiles: a 64 x 64 TMA box is 64 rows (k) of 128 bytes.
 //
 // CTA pairs (clusters of 2, cta_group::2): a unit is one 256 x 256 tile of one
@@ -38,19 +38,19 @@ static_assert(kSmem <= 232448, "shared memory budget");
 constexpr int kTmemCols = 512;
 
 struct Matrix {
-  CUtensorMap a[2];  // [R, M] per segment
-  CUtensorMap b;     // [R, N]
-  CUtensorMap out;   // [groups, M, N]
+  CUtensorMap a;    // [R, M]
+  CUtensorMap b;    // [R, N]
+  CUtensorMap out;  // [groups, M, N]
   int M, N, mt, nt;
 };
 struct Params {
   Matrix mat[3];
-  int nmat, groups, segments;
+  int nmat, groups;
   int units_per_group;
   int64_t units;
   const int32_t* grp_row0;
   const int32_t* grp_rows;
-  int grad_f32, accumulate;
+  int accumulate;
   unsigned* status;
 };
 
@@ -110,6 +110,7 @@ MOE_DEV void tma_add_3d(const void* tmap, uint32_t smem_src, int32_t c0, int32_t
                : "memory");
 }
 
+template <bool F32>
 __global__ void __launch_bounds__(kThreads, 1) wgrad_tc_kernel(const __grid_constant__ Params p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -164,8 +165,7 @@ __global__ void __launch_bounds__(kThreads, 1) wgrad_tc_kernel(const __grid_cons
         const int nk = (t.rows + kBK - 1) / kBK;
         const bool ragged = tail_rows(t.rows) % 16 != 0;
         const int ca = t.m0 + 128 * (int)rank, cb = t.n0 + 128 * (int)rank;
-        for (int sg = 0; sg < p.segments && ok; ++sg)
-          for (int kc = 0; kc < nk; ++kc, ++fills) {
+        for (int kc = 0; kc < nk; ++kc, ++fills) {
             const uint32_t s = fills % kStages;
             if (!mbar_wait_cluster_bounded(&sh.empty[s], ((fills / kStages) & 1u) ^ 1u, abort_flag)) {
               ok = false;
@@ -179,7 +179,7 @@ __global__ void __launch_bounds__(kThreads, 1) wgrad_tc_kernel(const __grid_cons
               mbar_arrive_expect_tx(&sh.landed[s], kStageBytes);
               if (first) mbar_arrive(&sh.full[s]);
               for (int c = 0; c < 2; ++c) {
-                tma_load_2d_hint(dst + c * kBox, &x.a[sg], &sh.landed[s], ca + 64 * c, r, pol);
+                tma_load_2d_hint(dst + c * kBox, &x.a, &sh.landed[s], ca + 64 * c, r, pol);
                 tma_load_2d_hint(dst + (2 + c) * kBox, &x.b, &sh.landed[s], cb + 64 * c, r, pol);
               }
               fixes |= 1u << s;
@@ -191,7 +191,7 @@ __global__ void __launch_bounds__(kThreads, 1) wgrad_tc_kernel(const __grid_cons
                 mbar_arrive_n(&sh.full[s], 2);
               }
               for (int c = 0; c < 2; ++c) {
-                tma_load_2d_pair(dst + c * kBox, &x.a[sg], bar, ca + 64 * c, r, pol);
+                tma_load_2d_pair(dst + c * kBox, &x.a, bar, ca + 64 * c, r, pol);
                 tma_load_2d_pair(dst + (2 + c) * kBox, &x.b, bar, cb + 64 * c, r, pol);
               }
               fixes &= ~(1u << s);
@@ -220,7 +220,7 @@ __global__ void __launch_bounds__(kThreads, 1) wgrad_tc_kernel(const __grid_cons
         tc_fence_after();
         const uint32_t d = tmem_base + b * kTile;
         bool more = false;  // accumulate onto the unit's earlier steps
-        for (int kc = 0; kc < nk * p.segments; ++kc) {
+        for (int kc = 0; kc < nk; ++kc) {
           const uint32_t s = consumed % kStages;
           if (!mbar_wait_cluster_bounded(&sh.full[s], (consumed / kStages) & 1u, abort_flag)) {
             ok = false;
@@ -229,7 +229,7 @@ __global__ void __launch_bounds__(kThreads, 1) wgrad_tc_kernel(const __grid_cons
           ++consumed;
           tc_fence_after();
           const uint32_t at = smem_u32(smem + s * kStageBytes);
-          const int steps = kc % nk == nk - 1 ? last_steps : kBK / 16;
+          const int steps = kc == nk - 1 ? last_steps : kBK / 16;
           for (int kk = 0; kk < steps; ++kk) {
             umma_bf16_pair(d, smem_desc_sw128_mn(at + kk * 2048, kBox),
                            smem_desc_sw128_mn(at + 2 * kBox + kk * 2048, kBox), idesc, more);
@@ -270,40 +270,31 @@ __global__ void __launch_bounds__(kThreads, 1) wgrad_tc_kernel(const __grid_cons
       }
       const int m = t.m0 + 128 * (int)rank + 32 * q;
       const uint32_t t_q = tmem_base + ((uint32_t)(q * 32) << 16) + b * kTile;
-      const int width = p.grad_f32 ? 32 : 64;  // columns of a 128-byte tile row
-#pragma unroll 1
-      for (int c = sub * width; c < kTile; c += 2 * width) {
-        const int n = t.n0 + c;
-        if (m >= x.M || n >= x.N) break;
-        uint32_t v[32];
+      // this warp's half of the columns in 128-byte tile rows: converted to
+      // registers first, so the accumulator is free for the next unit's MMAs
+      // before the stores
+      constexpr int kCols = F32 ? 32 : 64, kBlocks = kTile / kCols / 2;
+      uint32_t v[kBlocks][32];
+#pragma unroll
+      for (int i = 0; i < kBlocks; ++i) {
+        const int c = (2 * i + sub) * kCols;
         if (t.rows == 0) {
 #pragma unroll
-          for (int i = 0; i < 32; ++i) v[i] = 0u;
-        } else if (p.grad_f32) {
-          tmem_ld32(t_q + c, v);
+          for (int j = 0; j < 32; ++j) v[i][j] = 0u;
+        } else if (F32) {
+          tmem_ld32(t_q + c, v[i]);
           tmem_wait_ld();
         } else {
           uint32_t w[32];
-          tmem_ld32(t_q + c, v);
+          tmem_ld32(t_q + c, v[i]);
           tmem_ld32(t_q + c + 32, w);
           tmem_wait_ld();
 #pragma unroll
-          for (int i = 0; i < 16; ++i) v[i] = pack_bf16x2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
+          for (int j = 0; j < 16; ++j)
+            v[i][j] = pack_bf16x2(__uint_as_float(v[i][2 * j]), __uint_as_float(v[i][2 * j + 1]));
 #pragma unroll
-          for (int i = 0; i < 16; ++i) v[16 + i] = pack_bf16x2(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
-        }
-        if (lane == 0) bulk_wait_group_read<0>();  // the previous store has read the tile
-        __syncwarp();
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          st_shared_v4(tile + lane * 128 + ((i ^ (lane & 7)) << 4),
-                       make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]));
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-          if (p.accumulate) tma_add_3d(&x.out, tile, n, m, t.g);
-          else tma_store_3d(&x.out, tile, n, m, t.g);
-          bulk_commit_group();
+          for (int j = 0; j < 16; ++j)
+            v[i][16 + j] = pack_bf16x2(__uint_as_float(w[2 * j]), __uint_as_float(w[2 * j + 1]));
         }
       }
       if (t.rows > 0) {
@@ -313,6 +304,24 @@ __global__ void __launch_bounds__(kThreads, 1) wgrad_tc_kernel(const __grid_cons
           if (!first) st_async_u32(in_first(&sh.sink), 0u, in_first(&sh.acc_empty[b]));
           else if (ew == 0) mbar_arrive_expect_tx(&sh.acc_empty[b], 4 * kEpiWarps);  // and CTA 1's warps' stores
           else mbar_arrive(&sh.acc_empty[b]);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < kBlocks; ++i) {
+        const int n = t.n0 + (2 * i + sub) * kCols;
+        if (m >= x.M || n >= x.N) break;
+        if (lane == 0) bulk_wait_group_read<0>();  // the previous store has read the tile
+        __syncwarp();
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          st_shared_v4(tile + lane * 128 + ((j ^ (lane & 7)) << 4),
+                       make_uint4(v[i][4 * j], v[i][4 * j + 1], v[i][4 * j + 2], v[i][4 * j + 3]));
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          if (p.accumulate) tma_add_3d(&x.out, tile, n, m, t.g);
+          else tma_store_3d(&x.out, tile, n, m, t.g);
+          bulk_commit_group();
         }
       }
     }
@@ -326,12 +335,9 @@ __global__ void __launch_bounds__(kThreads, 1) wgrad_tc_kernel(const __grid_cons
       if (t.rows == 0) continue;
       const int nk = (t.rows + kBK - 1) / kBK;
       const int v = tail_rows(t.rows);
-      if (v % 16 == 0) {
-        j += nk * p.segments;
-        continue;
-      }
-      for (int sg = 0; sg < p.segments; ++sg) {
-        j += nk;
+      j += nk;
+      if (v % 16 == 0) continue;
+      {
         const uint32_t s = (j - 1) % kStages;
         int got = 1;
         if (lane == 0) got = mbar_wait_bounded(&sh.landed[s], (phase >> s) & 1u, abort_flag);
@@ -378,7 +384,7 @@ __global__ void __launch_bounds__(kThreads, 1) wgrad_tc_kernel(const __grid_cons
   }
 }
 
-bool make_rows_map(CUtensorMap* m, const void* base, int64_t rows, int cols, int64_t ld) {
+bool make_rows_map(CUtensorMap* m, const void* base, int64_t rows, int64_t cols, int64_t ld) {
   const uint64_t dims[2] = {(uint64_t)cols, (uint64_t)rows}, stride[1] = {(uint64_t)ld * 2};
   const uint32_t box[2] = {64, kBK};
   return make_tmap_nd(m, base, 2, 2, dims, stride, box, 128, true);
@@ -390,34 +396,33 @@ cudaError_t launch_wgrad_tc(const WgradArgs& a, cudaStream_t s) {
   Params p{};
   p.nmat = a.nmat;
   p.groups = a.groups;
-  p.segments = a.segments;
   const int elem = a.grad_dtype == MOE_F32 ? 4 : 2;
   for (int i = 0; i < a.nmat; ++i) {
     const WgradMatrix& w = a.mat[i];
     Matrix& x = p.mat[i];
-    x.M = w.M;
+    x.M = (int)w.M;
     x.N = w.N;
-    x.mt = (w.M + kTile - 1) / kTile;
+    x.mt = (int)((w.M + kTile - 1) / kTile);
     x.nt = (w.N + kTile - 1) / kTile;
     p.units_per_group += x.mt * x.nt;
     const uint64_t dims[3] = {(uint64_t)w.N, (uint64_t)w.M, (uint64_t)a.groups};
     const uint64_t stride[2] = {(uint64_t)w.N * elem, (uint64_t)w.N * w.M * elem};
     const uint32_t box[3] = {128u / elem, 32, 1};
-    if (!make_rows_map(&x.a[0], w.A[0], a.rows, w.M, w.lda) || !make_rows_map(&x.a[1], w.A[1], a.rows, w.M, w.lda) ||
-        !make_rows_map(&x.b, w.B, a.rows, w.N, w.N) ||
+    if (!make_rows_map(&x.a, w.A, a.rows, w.M, w.lda) || !make_rows_map(&x.b, w.B, a.rows, w.N, w.N) ||
         !make_tmap_nd(&x.out, w.out, elem, 3, dims, stride, box, 128, false))
       return cudaErrorInvalidValue;
   }
   p.units = (int64_t)a.groups * p.units_per_group;
   p.grp_row0 = a.grp_row0;
   p.grp_rows = a.grp_rows;
-  p.grad_f32 = a.grad_dtype == MOE_F32;
   p.accumulate = a.accumulate;
   p.status = a.status;
   if (p.units == 0) return cudaSuccess;
 
+  const bool f32 = a.grad_dtype == MOE_F32;
+  const auto kernel = f32 ? wgrad_tc_kernel<true> : wgrad_tc_kernel<false>;
   static std::mutex mu;
-  static int max_clusters_of[kMaxDevices] = {};
+  static int max_clusters_of[2][kMaxDevices] = {};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
@@ -436,20 +441,52 @@ cudaError_t launch_wgrad_tc(const WgradArgs& a, cudaStream_t s) {
   int clusters = 0;
   {
     std::lock_guard<std::mutex> lock(mu);
-    if (max_clusters_of[dev] == 0) {
-      e = cudaFuncSetAttribute(wgrad_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    int& known = max_clusters_of[f32][dev];
+    if (known == 0) {
+      e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
       if (e != cudaSuccess) return e;
       cfg.gridDim = dim3(2 * (device_sm_count() / 2), 1, 1);
       int n = 0;
-      e = cudaOccupancyMaxActiveClusters(&n, wgrad_tc_kernel, &cfg);
+      e = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg);
       if (e != cudaSuccess) return e;
-      max_clusters_of[dev] = n > 0 ? n : 1;
+      known = n > 0 ? n : 1;
     }
-    clusters = max_clusters_of[dev];
+    clusters = known;
   }
   if (p.units < clusters) clusters = (int)p.units;
   cfg.gridDim = dim3(2 * clusters, 1, 1);
-  return cudaLaunchKernelEx(&cfg, wgrad_tc_kernel, p);
+  return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+
+cudaError_t launch_route_products_tc(const Problem& p, const RouteBwdArgs& a, cudaStream_t s) {
+  if (a.dx) {
+    WgradArgs x{};
+    x.mat[0] = {a.dz16_t, a.W_r, a.dx, p.T, p.d, a.ld_t};
+    x.nmat = 1;
+    x.groups = 1;
+    x.rows = p.N;
+    x.grp_row0 = a.tables + kRtRow0;
+    x.grp_rows = a.tables + kRtExperts;
+    x.grad_dtype = MOE_BF16;
+    x.status = a.status;
+    const cudaError_t e = launch_wgrad_tc(x, s);
+    if (e != cudaSuccess) return e;
+  }
+  if (!a.dW_r) return cudaSuccess;
+  const bool split = a.splits > 1;
+  WgradArgs w{};
+  w.mat[0] = {a.dz16, a.x, split ? a.planes : a.dW_r, p.N, p.d, a.ld};
+  w.nmat = 1;
+  w.groups = a.splits;
+  w.rows = p.T;
+  w.grp_row0 = a.tables + kRtSplit0;
+  w.grp_rows = a.tables + kRtSplitRows;
+  w.grad_dtype = split ? (int)MOE_F32 : a.grad_dtype;
+  w.accumulate = !split && a.accumulate;
+  w.status = a.status;
+  const cudaError_t e = launch_wgrad_tc(w, s);
+  if (e != cudaSuccess || !split) return e;
+  return launch_join_planes(a.planes, a.splits, (int64_t)p.N * p.d, a.dW_r, a.grad_dtype, a.accumulate, s);
 }
 
 }  // namespace moe

@@ -421,8 +421,8 @@ def route_check(c, dx, dW, exact, dG=None):
     their terms and not by dz_j: each factor is good to a few units of 2^-24,
     a sum over the N scores (the softmax) or k slots to N + k, together
     (N + k + 16) 2^-23 A_j. The products then add (terms + 16) 2^-23 of the
-    sum of the absolute terms, and in bf16 layers dz as two bf16 terms 2^-16
-    of itself at most."""
+    sum of the absolute terms. In bf16 layers dz is rounded to bf16 as an
+    operand of the products: 2^-8 of itself (and the norm's bound applies)."""
     dz, rx, rW = exact
     z, idx, g = c["logits"].double(), c["idx"].long(), (c["dG"] if dG is None else dG).double().abs()
     s = torch.sigmoid(z) if c["score"] == "sigmoid" else torch.softmax(z, 1)
@@ -432,7 +432,7 @@ def route_check(c, dx, dW, exact, dG=None):
     A = torch.zeros_like(s).scatter_(1, idx, ds) * s
     if c["score"] == "softmax":
         A = A + s * (ds * sel).sum(1, keepdim=True)
-    err = (c["N"] + c["k"] + 16) * 2.0 ** -23 * A + (2.0 ** -16 if c["dtype"] == "bf16" else 0.0) * dz.abs()
+    err = (c["N"] + c["k"] + 16) * 2.0 ** -23 * A + (2.0 ** -8 if c["dtype"] == "bf16" else 0.0) * dz.abs()
     W, x = c["W_r"].double().abs(), c["x"].double().abs()
     ex = err @ W + (c["N"] + 16) * 2.0 ** -23 * (dz.abs() @ W)
     eW = err.T @ x + (c["T"] + 16) * 2.0 ** -23 * (dz.abs().T @ x)
@@ -440,6 +440,8 @@ def route_check(c, dx, dW, exact, dG=None):
         bound = e + (2.0 ** -8 * (r.abs() + e) if y.dtype == torch.bfloat16 else 0.0)
         off = (y.double() - r).abs()
         assert bool((off <= bound + 1e-30).all()), float((off / (bound + 1e-30)).max())
+        assert c["dtype"] == "f32" or float(torch.linalg.vector_norm(off)) <= (
+            BF16_TWO * float(torch.linalg.vector_norm(r)) + float(torch.linalg.vector_norm(e)) * 2.0 ** -8)
 
 
 ROUTES = [(1, 4, 2, 64), (7, 63, 7, 136), (300, 64, 16, 512), (1000, 100, 6, 264), (517, 256, 8, 1280),
