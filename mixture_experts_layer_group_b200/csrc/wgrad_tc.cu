@@ -46,8 +46,7 @@ struct Matrix {
 struct Params {
   Matrix mat[3];
   int nmat, groups;
-  int units_per_group;
-  int64_t units;
+  int units_per_group, units;
   const int32_t* grp_row0;
   const int32_t* grp_rows;
   int accumulate;
@@ -71,31 +70,40 @@ static_assert(sizeof(Shared) <= 512, "barrier block");
 struct Unit {
   int g, mat, m0, n0, row0, rows;
 };
-MOE_DEV Unit decode(const Params& p, int64_t u) {
-  Unit t;
-  t.g = (int)(u / p.units_per_group);
-  int left = (int)(u % p.units_per_group);
-  t.mat = 0;
+MOE_DEV Unit decode(const Params& p, int u) {
+  Unit t{};
+  if (u >= p.units) return t;
+  t.g = u / p.units_per_group;
+  int left = u - t.g * p.units_per_group;
+  t.row0 = __ldg(p.grp_row0 + t.g);
+  t.rows = __ldg(p.grp_rows + t.g);
   while (t.mat < p.nmat - 1 && left >= p.mat[t.mat].mt * p.mat[t.mat].nt) {
     left -= p.mat[t.mat].mt * p.mat[t.mat].nt;
     ++t.mat;
   }
-  t.m0 = left / p.mat[t.mat].nt * kTile;
-  t.n0 = left % p.mat[t.mat].nt * kTile;
-  t.row0 = __ldg(p.grp_row0 + t.g);
-  t.rows = __ldg(p.grp_rows + t.g);
+  const int nt = p.mat[t.mat].nt;
+  t.m0 = left / nt * kTile;
+  t.n0 = (left - left / nt * nt) * kTile;
   return t;
 }
+// A pair's units, u = pair, pair + pairs, ...: the next one is decoded while
+// the current one is worked on (its two table reads and divisions cost about
+// 900 cycles otherwise, in every role).
+struct Walk {
+  int u, step;
+  Unit next;
+  MOE_DEV Walk(const Params& p, int pair, int pairs) : u(pair), step(pairs), next(decode(p, pair)) {}
+  MOE_DEV bool take(const Params& p, Unit& t) {
+    if (u >= p.units) return false;
+    t = next;
+    u += step;
+    next = decode(p, u);
+    return true;
+  }
+};
 // Rows of the last 64-row block, and whether foreign rows share its last K step.
 MOE_DEV int tail_rows(int rows) { return rows - (rows - 1) / kBK * kBK; }
 
-MOE_DEV void mbar_arrive_n(uint64_t* bar, uint32_t n) {
-  asm volatile("{\n\t.reg .b64 st;\n\tmbarrier.arrive.shared::cta.b64 st, [%0], %1;\n\t}" ::"r"(smem_u32(bar)), "r"(n)
-               : "memory");
-}
-MOE_DEV void mbar_arrive_cluster(uint32_t bar_cluster) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster) : "memory");
-}
 MOE_DEV void tma_store_3d(const void* tmap, uint32_t smem_src, int32_t c0, int32_t c1, int32_t c2) {
   asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
                    reinterpret_cast<uint64_t>(tmap)),
@@ -119,13 +127,14 @@ __global__ void __launch_bounds__(kThreads, 1) wgrad_tc_kernel(const __grid_cons
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
   const bool first = rank == 0;
-  const int64_t pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+  Walk walk(p, (int)(blockIdx.x >> 1), (int)(gridDim.x >> 1));
+  Unit t;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
-      // a stage as loaded: the producer's three arrivals and both CTAs' bytes;
-      // a fixed stage: the producer's one arrival and the two fixers'
-      mbar_init(&sh.full[s], 3);
+      // the first CTA's producer and the bytes of both CTAs, or (a fixed
+      // stage) four bytes from each CTA's fixer
+      mbar_init(&sh.full[s], 1);
       mbar_init(&sh.empty[s], 1);
       mbar_init(&sh.landed[s], 1);
     }
@@ -158,8 +167,7 @@ __global__ void __launch_bounds__(kThreads, 1) wgrad_tc_kernel(const __grid_cons
     if (lane == 0) {
       const uint64_t pol = policy_evict_normal();
       bool ok = true;
-      for (int64_t u = pair; ok && u < p.units; u += pairs) {
-        const Unit t = decode(p, u);
+      while (ok && walk.take(p, t)) {
         if (t.rows == 0) continue;
         const Matrix& x = p.mat[t.mat];
         const int nk = (t.rows + kBK - 1) / kBK;
@@ -177,7 +185,7 @@ __global__ void __launch_bounds__(kThreads, 1) wgrad_tc_kernel(const __grid_cons
             if (fix) {
               // this CTA's bytes land on its own barrier; the fixers hand the stage on
               mbar_arrive_expect_tx(&sh.landed[s], kStageBytes);
-              if (first) mbar_arrive(&sh.full[s]);
+              if (first) mbar_arrive_expect_tx(&sh.full[s], 8);
               for (int c = 0; c < 2; ++c) {
                 tma_load_2d_hint(dst + c * kBox, &x.a, &sh.landed[s], ca + 64 * c, r, pol);
                 tma_load_2d_hint(dst + (2 + c) * kBox, &x.b, &sh.landed[s], cb + 64 * c, r, pol);
@@ -186,10 +194,7 @@ __global__ void __launch_bounds__(kThreads, 1) wgrad_tc_kernel(const __grid_cons
               fix_phase ^= 1u << s;
             } else {
               const uint32_t bar = in_first(&sh.full[s]);
-              if (first) {
-                mbar_arrive_expect_tx(&sh.full[s], 2 * kStageBytes);
-                mbar_arrive_n(&sh.full[s], 2);
-              }
+              if (first) mbar_arrive_expect_tx(&sh.full[s], 2 * kStageBytes);
               for (int c = 0; c < 2; ++c) {
                 tma_load_2d_pair(dst + c * kBox, &x.a, bar, ca + 64 * c, r, pol);
                 tma_load_2d_pair(dst + (2 + c) * kBox, &x.b, bar, cb + 64 * c, r, pol);
@@ -206,8 +211,7 @@ __global__ void __launch_bounds__(kThreads, 1) wgrad_tc_kernel(const __grid_cons
       const uint32_t idesc = idesc_bf16_f32(256, kTile) | kIdescAMn | kIdescBMn;
       uint32_t consumed = 0, accs = 0;
       bool ok = true;
-      for (int64_t u = pair; ok && u < p.units; u += pairs) {
-        const Unit t = decode(p, u);
+      while (ok && walk.take(p, t)) {
         if (t.rows == 0) continue;
         const int nk = (t.rows + kBK - 1) / kBK;
         const int last_steps = (tail_rows(t.rows) + 15) / 16;
@@ -252,8 +256,7 @@ __global__ void __launch_bounds__(kThreads, 1) wgrad_tc_kernel(const __grid_cons
     const int q = warp & 3, ew = warp - 2, sub = ew >> 2;
     const uint32_t tile = smem_u32(out_tiles + ew * kOutTile);
     uint32_t accs = 0;
-    for (int64_t u = pair; u < p.units; u += pairs) {
-      const Unit t = decode(p, u);
+    while (walk.take(p, t)) {
       if (t.rows == 0 && p.accumulate) continue;
       const Matrix& x = p.mat[t.mat];
       const uint32_t b = accs & 1u;
@@ -330,8 +333,7 @@ __global__ void __launch_bounds__(kThreads, 1) wgrad_tc_kernel(const __grid_cons
     // ------------------------------------------------------------- fixer --
     uint32_t j = 0, phase = 0;
     bool ok = true;
-    for (int64_t u = pair; ok && u < p.units; u += pairs) {
-      const Unit t = decode(p, u);
+    while (ok && walk.take(p, t)) {
       if (t.rows == 0) continue;
       const int nk = (t.rows + kBK - 1) / kBK;
       const int v = tail_rows(t.rows);
@@ -355,7 +357,8 @@ __global__ void __launch_bounds__(kThreads, 1) wgrad_tc_kernel(const __grid_cons
           st_shared_v4(at + (i / words) * kBox + v * 128 + (i % words) * 16, make_uint4(0, 0, 0, 0));
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(in_first(&sh.full[s]));
+        // (an asynchronous store: a remote arrive would hold this warp for about 1000 cycles)
+        if (lane == 0) st_async_u32(in_first(&sh.sink), 0u, in_first(&sh.full[s]));
       }
     }
   }
@@ -412,7 +415,9 @@ cudaError_t launch_wgrad_tc(const WgradArgs& a, cudaStream_t s) {
         !make_tmap_nd(&x.out, w.out, elem, 3, dims, stride, box, 128, false))
       return cudaErrorInvalidValue;
   }
-  p.units = (int64_t)a.groups * p.units_per_group;
+  const int64_t units = (int64_t)a.groups * p.units_per_group;
+  if (units > (1ll << 31) - 1 - 4096) return cudaErrorInvalidValue;
+  p.units = (int)units;
   p.grp_row0 = a.grp_row0;
   p.grp_rows = a.grp_rows;
   p.accumulate = a.accumulate;
@@ -453,7 +458,7 @@ cudaError_t launch_wgrad_tc(const WgradArgs& a, cudaStream_t s) {
     }
     clusters = known;
   }
-  if (p.units < clusters) clusters = (int)p.units;
+  if (p.units < clusters) clusters = p.units;
   cfg.gridDim = dim3(2 * clusters, 1, 1);
   return cudaLaunchKernelEx(&cfg, kernel, p);
 }
