@@ -40,6 +40,21 @@ MOE_DEV uint64_t global_timer_ns() {
 
 MOE_DEV uint32_t lane_id() { return threadIdx.x & 31u; }
 
+// The warp's index within its block, in a form that the compiler keeps in
+// uniform registers (as it then does with what follows from it).
+MOE_DEV int uniform_warp_id() { return __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0); }
+
+// True in exactly one lane of a converged warp. The operands of a tensor-core
+// instruction are uniform registers: issued by a lane picked this way inside
+// warp-uniform code, their values are computed there; inside a branch on the
+// lane index every operand is first moved over from a thread's register,
+// which made issuing a pair MMA about as long as its 128 cycles of work.
+MOE_DEV bool elect_one() {
+  uint32_t one;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(one));
+  return one != 0;
+}
+
 // ---------------------------------------------------------------- mbarrier --
 
 MOE_DEV void mbar_init(uint64_t* bar, uint32_t count) {

@@ -124,7 +124,7 @@ __global__ void __launch_bounds__(kThreads, 1) wgrad_tc_kernel(const __grid_cons
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* out_tiles = smem + kStages * kStageBytes;
   Shared& sh = *reinterpret_cast<Shared*>(out_tiles + kEpiWarps * kOutTile);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = uniform_warp_id(), lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
   const bool first = rank == 0;
   Walk walk(p, (int)(blockIdx.x >> 1), (int)(gridDim.x >> 1));
@@ -207,45 +207,46 @@ __global__ void __launch_bounds__(kThreads, 1) wgrad_tc_kernel(const __grid_cons
     }
     __syncwarp();
   } else if (warp == 1) {
-    if (lane == 0 && first) {
+    if (first) {
+      // the whole warp runs the loop, one elected lane issues
       const uint32_t idesc = idesc_bf16_f32(256, kTile) | kIdescAMn | kIdescBMn;
       uint32_t consumed = 0, accs = 0;
       bool ok = true;
       while (ok && walk.take(p, t)) {
-        if (t.rows == 0) continue;
-        const int nk = (t.rows + kBK - 1) / kBK;
-        const int last_steps = (tail_rows(t.rows) + 15) / 16;
+        const int rows = __shfl_sync(0xffffffffu, t.rows, 0);
+        if (rows == 0) continue;
+        const int nk = (rows + kBK - 1) / kBK;
+        const int last_steps = (tail_rows(rows) + 15) / 16;
         const uint32_t b = accs & 1u;
-        if (!mbar_wait_cluster_bounded(&sh.acc_empty[b], ((accs >> 1) & 1u) ^ 1u, abort_flag)) {
-          ok = false;
-          break;
-        }
+        ok = __all_sync(0xffffffffu, mbar_wait_cluster_bounded(&sh.acc_empty[b], ((accs >> 1) & 1u) ^ 1u, abort_flag));
+        if (!ok) break;
         ++accs;
         tc_fence_after();
         const uint32_t d = tmem_base + b * kTile;
-        bool more = false;  // accumulate onto the unit's earlier steps
         for (int kc = 0; kc < nk; ++kc) {
           const uint32_t s = consumed % kStages;
-          if (!mbar_wait_cluster_bounded(&sh.full[s], (consumed / kStages) & 1u, abort_flag)) {
-            ok = false;
-            break;
-          }
+          ok = __all_sync(0xffffffffu, mbar_wait_cluster_bounded(&sh.full[s], (consumed / kStages) & 1u, abort_flag));
+          if (!ok) break;
           ++consumed;
           tc_fence_after();
-          const uint32_t at = smem_u32(smem + s * kStageBytes);
+          const uint64_t da = smem_desc_sw128_mn(smem_u32(smem) + s * kStageBytes, kBox);
+          const uint64_t db = da + (2 * kBox >> 4);
           const int steps = kc == nk - 1 ? last_steps : kBK / 16;
-          for (int kk = 0; kk < steps; ++kk) {
-            umma_bf16_pair(d, smem_desc_sw128_mn(at + kk * 2048, kBox),
-                           smem_desc_sw128_mn(at + 2 * kBox + kk * 2048, kBox), idesc, more);
-            more = true;
+          if (elect_one()) {
+#pragma unroll
+            for (int kk = 0; kk < kBK / 16; ++kk)
+              if (kk < steps) umma_bf16_pair(d, da + kk * (2048 >> 4), db + kk * (2048 >> 4), idesc, (kc | kk) != 0);
+            umma_commit_pair_both(smem_u32(&sh.empty[s]));
           }
-          umma_commit_pair_both(smem_u32(&sh.empty[s]));
+          __syncwarp();
         }
-        if (ok) umma_commit_pair_both(smem_u32(&sh.acc_full[b]));
+        if (ok && elect_one()) umma_commit_pair_both(smem_u32(&sh.acc_full[b]));
+        __syncwarp();
       }
-      if (!ok) fail();
-      umma_commit_pair_both(smem_u32(&sh.drained));
-      sh.consumed = consumed;
+      if (!ok && lane == 0) fail();
+      if (elect_one()) umma_commit_pair_both(smem_u32(&sh.drained));
+      if (lane == 0) sh.consumed = consumed;
+      __syncwarp();
     }
     if (lane == 0) {
       int no_abort = 0;
