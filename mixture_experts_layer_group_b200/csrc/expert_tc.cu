@@ -322,6 +322,8 @@ struct Shared {
   uint64_t drained;            // both: all pair MMAs completed
   uint32_t slot_off[kSlots];   // byte offset of each stage in the ring
   int ring[kRing];
+  int ring_nk[kRing];          // CTA 0, for the MMA issuer: the unit's K blocks and tokens (0: none left)
+  int ring_ntok[kRing];
   int epi_unit[2];             // the epilogue leader's unit for the epilogue warps
   int epi_info[2][5];          // its decoded (g, f, tok0, ntok) and first output row
   uint32_t tmem_base;
@@ -434,7 +436,7 @@ __global__ void __launch_bounds__(Plan<FP8>::kThreads, 1)
   Shared& sh = *reinterpret_cast<Shared*>(reinterpret_cast<uint8_t*>(tiles) + kTBytes);
   SharedFp8& shf = *reinterpret_cast<SharedFp8*>(reinterpret_cast<uint8_t*>(&sh) + 512);
 
-  const int warp = threadIdx.x >> 5;
+  const int warp = uniform_warp_id();
   const int lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();  // 0: issues the pair MMAs and takes the units
   const bool first = rank == 0;
@@ -555,10 +557,9 @@ __global__ void __launch_bounds__(Plan<FP8>::kThreads, 1)
           }
           u = atomicAdd(p.sched, 1);
           if (u >= total_units) u = -1;
-          sh.ring[q] = u;
-          mbar_arrive(&sh.ring_full[q]);
           // the id itself is the 4 transaction bytes of the peer's ring_full
           st_async_u32(peer(&sh.ring[q]), (uint32_t)u, peer(&sh.ring_full[q]));
+          sh.ring[q] = u;
         } else {
           // this CTA's ring_full phase: one arrival (here) and the 4 bytes of CTA 0's store
           mbar_arrive_expect_tx(&sh.ring_full[q], 4);
@@ -569,17 +570,26 @@ __global__ void __launch_bounds__(Plan<FP8>::kThreads, 1)
           u = load_volatile(&sh.ring[q]);
           st_async_u32(in_first(&sh.sink), 0u, in_first(&sh.ring_empty[q]));
         }
+        Unit un{};
+        int K = 0;
+        if (u >= 0) {
+          un = decode_unit(p, u);
+          K = un.g == p.N ? p.k_shared : p.k_routed;
+        }
+        const int seg = (K + kBK - 1) / kBK;  // K blocks of a segment
+        const int nk = k_blocks<MODE>(seg);
+        if (first) {
+          sh.ring_nk[q] = nk;
+          sh.ring_ntok[q] = un.ntok;
+          mbar_arrive(&sh.ring_full[q]);
+        }
         if (u < 0) {
           // no units left for this CTA: the down GEMM may start on SMs as
           // they free up
           if (is_swiglu(MODE)) griddep_launch_dependents();
           break;
         }
-        const Unit un = decode_unit(p, u);
         const bool shared = un.g == p.N;
-        const int K = shared ? p.k_shared : p.k_routed;
-        const int seg = (K + kBK - 1) / kBK;  // K blocks of a segment
-        const int nk = k_blocks<MODE>(seg);
         const int half_n = mma_n<FP8>(un.ntok) / 2;  // token rows per CTA
         // one token box per stage, the smallest of 32 / 64 / 128 rows that
         // covers this CTA's rows (the TMA engine's cost is per box, so a
@@ -651,24 +661,31 @@ __global__ void __launch_bounds__(Plan<FP8>::kThreads, 1)
     __syncwarp();
   } else if (warp == 1) {
     // ------------------------------------------------- MMA issuer (CTA 0) --
-    if (lane == 0 && first) {
+    if (first) {
+      // The whole warp runs the loop and one elected lane issues: the
+      // instruction operands then stay in uniform registers (see elect_one()).
+      // Issued from a branch on the lane index instead, four pair MMAs with
+      // their wait and commit cost about 610 cycles of issue at any N; so,
+      // 290, and at N = 256 all of it hides behind the MMAs' 512.
       uint32_t consumed = 0;
       uint32_t uses[2] = {0u, 0u};
       AccPlan<PL::kAccCols> plan;
       bool ok = true;
+      auto wait = [&](uint64_t* bar, uint32_t parity) {
+        return (bool)__all_sync(0xffffffffu, mbar_wait_cluster_bounded(bar, parity, abort_flag));
+      };
       for (int i = 0; ok; ++i) {
         const int q = i % kRing;
-        if (!mbar_wait_cluster_bounded(&sh.ring_full[q], (i / kRing) & 1, abort_flag)) {
+        if (!wait(&sh.ring_full[q], (i / kRing) & 1)) {
           ok = false;
           break;
         }
-        const int u = load_volatile(&sh.ring[q]);
-        mbar_arrive_expect_tx(&sh.ring_empty[q], 4 * kRingReaders);  // and CTA 1's readers' stores
-        if (u < 0) break;
-        const Unit un = decode_unit(p, u);
-        const int K = un.g == p.N ? p.k_shared : p.k_routed;
-        const int nk = k_blocks<MODE>((K + kBK - 1) / kBK);
-        const int n = mma_n<FP8>(un.ntok);
+        // K blocks and tokens of the unit (0 tokens: no unit left)
+        const int nk = __shfl_sync(0xffffffffu, load_volatile(&sh.ring_nk[q]), 0);
+        const int ntok = __shfl_sync(0xffffffffu, load_volatile(&sh.ring_ntok[q]), 0);
+        if (elect_one()) mbar_arrive_expect_tx(&sh.ring_empty[q], 4 * kRingReaders);  // and CTA 1's readers' stores
+        if (ntok == 0) break;
+        const int n = mma_n<FP8>(ntok);
         const uint32_t idesc = idesc_bf16_f32(256, (uint32_t)n) | (is_bwd(MODE) ? kIdescAMn : 0u);
         uint32_t mask, base, stride;
         plan.place(n, mask, base, stride);
@@ -676,7 +693,7 @@ __global__ void __launch_bounds__(Plan<FP8>::kThreads, 1)
         plan.advance(n);
         for (int b = 0; b < 2 && ok; ++b)
           if ((mask >> b) & 1u) {
-            ok = mbar_wait_cluster_bounded(&sh.acc_empty[b], (uses[b] & 1u) ^ 1u, abort_flag);
+            ok = wait(&sh.acc_empty[b], (uses[b] & 1u) ^ 1u);
             ++uses[b];
           }
         if (!ok) break;
@@ -687,58 +704,57 @@ __global__ void __launch_bounds__(Plan<FP8>::kThreads, 1)
           // FP8: the converted slot of this fill (both CTAs' converters have
           // observed its bytes land before they released it)
           const uint32_t c = FP8 ? consumed % kASlots : 0u;
-          const bool landed = FP8 ? mbar_wait_cluster_bounded(&shf.conv_full[c], (consumed / kASlots) & 1u, abort_flag)
-                                  : mbar_wait_cluster_bounded(&sh.full[s], ph, abort_flag);
+          const bool landed = FP8 ? wait(&shf.conv_full[c], (consumed / kASlots) & 1u) : wait(&sh.full[s], ph);
           if (!landed) {
             ok = false;
             break;
           }
           ++consumed;
           tc_fence_after();
-          const uint32_t stage_addr = smem_u32(smem + *reinterpret_cast<volatile uint32_t*>(&sh.slot_off[s]));
-          const uint32_t b_addr = stage_addr + PL::kABytes;  // the token box follows the weights
-          if (FP8) {
-            // A: the converted slot in tensor memory, 8 columns per 16 K
-            const uint32_t a_t = tmem_base + PL::kAccCols + c * kASlotCols;
+          const uint32_t off =
+              __shfl_sync(0xffffffffu, *reinterpret_cast<volatile uint32_t*>(&sh.slot_off[s]), 0);
+          const uint32_t stage_addr = smem_u32(smem) + off;
+          const uint64_t bdesc = smem_desc_sw128(stage_addr + PL::kABytes);  // the token box follows the weights
+          if (elect_one()) {
+            if (FP8) {
+              // A: the converted slot in tensor memory, 8 columns per 16 K
+              const uint32_t a_t = tmem_base + PL::kAccCols + c * kASlotCols;
 #pragma unroll
-            for (int kk = 0; kk < kBK / 16; ++kk) {
-              const uint64_t bdesc = smem_desc_sw128(b_addr + kk * 32);
-              umma_bf16_pair_ts(d0, a_t + kk * 8, bdesc, idesc, (kc | kk) != 0);
-              umma_bf16_pair_ts(d1, a_t + kBK / 2 + kk * 8, bdesc, idesc, (kc | kk) != 0);
-            }
-          } else if (is_bwd(MODE)) {
+              for (int kk = 0; kk < kBK / 16; ++kk) {
+                umma_bf16_pair_ts(d0, a_t + kk * 8, bdesc + kk * 2, idesc, (kc | kk) != 0);
+                umma_bf16_pair_ts(d1, a_t + kBK / 2 + kk * 8, bdesc + kk * 2, idesc, (kc | kk) != 0);
+              }
+            } else {
+              // 16 K are 32 bytes of a K-major row, 16 rows of 128 bytes of an MN-major tile
+              const uint64_t adesc = is_bwd(MODE) ? smem_desc_sw128_mn(stage_addr, kMnBox) : smem_desc_sw128(stage_addr);
+              constexpr int kStep = is_bwd(MODE) ? 2048 >> 4 : 2, kHalf = kHalfBytes >> 4;
 #pragma unroll
-            for (int kk = 0; kk < kBK / 16; ++kk) {
-              const uint64_t bdesc = smem_desc_sw128(b_addr + kk * 32);
-              umma_bf16_pair(d0, smem_desc_sw128_mn(stage_addr + kk * 2048, kMnBox), bdesc, idesc, (kc | kk) != 0);
-              umma_bf16_pair(d1, smem_desc_sw128_mn(stage_addr + kHalfBytes + kk * 2048, kMnBox), bdesc, idesc,
-                             (kc | kk) != 0);
+              for (int kk = 0; kk < kBK / 16; ++kk) {
+                umma_bf16_pair(d0, adesc + kk * kStep, bdesc + kk * 2, idesc, (kc | kk) != 0);
+                umma_bf16_pair(d1, adesc + kHalf + kk * kStep, bdesc + kk * 2, idesc, (kc | kk) != 0);
+              }
             }
-          } else {
-#pragma unroll
-            for (int kk = 0; kk < kBK / 16; ++kk) {
-              const uint64_t bdesc = smem_desc_sw128(b_addr + kk * 32);
-              umma_bf16_pair(d0, smem_desc_sw128(stage_addr + kk * 32), bdesc, idesc, (kc | kk) != 0);
-              umma_bf16_pair(d1, smem_desc_sw128(stage_addr + kHalfBytes + kk * 32), bdesc, idesc, (kc | kk) != 0);
-            }
+            umma_commit_pair_both(smem_u32(&sh.empty[s]));
+            if (FP8) umma_commit_pair_both(smem_u32(&shf.conv_empty[c]));
           }
-          umma_commit_pair_both(smem_u32(&sh.empty[s]));
-          if (FP8) umma_commit_pair_both(smem_u32(&shf.conv_empty[c]));
+          __syncwarp();
         }
-        if (ok) {
+        if (ok && elect_one()) {
           for (int b = 0; b < 2; ++b)
             if ((mask >> b) & 1u) {
               umma_commit_pair_both(smem_u32(&sh.acc_full[b]));
             }
         }
+        __syncwarp();
       }
-      if (!ok) {
+      if (!ok && lane == 0) {
         *abort_flag = 1;
         set_status(p.status, MOE_DEV_WAIT_TIMEOUT);
       }
       // all pair MMAs have completed once `drained` fires (in both CTAs)
-      umma_commit_pair_both(smem_u32(&sh.drained));
-      sh.consumed = consumed;
+      if (elect_one()) umma_commit_pair_both(smem_u32(&sh.drained));
+      if (lane == 0) sh.consumed = consumed;
+      __syncwarp();
     }
     if (lane == 0) {
       int no_abort = 0;  // wait for the MMAs even when unwinding
