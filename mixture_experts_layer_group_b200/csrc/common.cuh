@@ -487,9 +487,48 @@ MOE_DEV uint32_t pack_bf16x2(float lo, float hi) {
 
 MOE_DEV float silu_f32(float g) { return g / (1.0f + __expf(-g)); }
 
-// sigma(g) = 1 / (1 + e^-g) by the hardware exponential and division; 0 where
-// e^-g overflows.
-MOE_DEV float sigmoid_fast(float g) { return __fdividef(1.0f, 1.0f + __expf(-g)); }
+// Two fp32 values in one 64-bit register pair, and their packed arithmetic
+// (each lane rounded as the scalar operation rounds it).
+MOE_DEV uint64_t f32x2(float lo, float hi) {
+  uint64_t v;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(lo), "f"(hi));
+  return v;
+}
+MOE_DEV void split_f32x2(uint64_t v, float& lo, float& hi) { asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v)); }
+MOE_DEV uint64_t mul_f32x2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+MOE_DEV uint64_t add_f32x2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+MOE_DEV uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+MOE_DEV uint64_t bf16x2_to_f32x2(uint32_t v) { return f32x2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u)); }
+MOE_DEV uint32_t f32x2_to_bf16x2(uint64_t v) {
+  float lo, hi;
+  split_f32x2(v, lo, hi);
+  return pack_bf16x2(lo, hi);
+}
+
+// sigma(g) = 1 / (1 + 2^(-g log2 e)) of a pair, by the hardware's exponential
+// and reciprocal; 0 where the power overflows.
+MOE_DEV uint64_t sigmoid_f32x2(uint64_t g) {
+  float x, y;
+  split_f32x2(mul_f32x2(g, f32x2(-1.4426950408889634f, -1.4426950408889634f)), x, y);
+  asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(x));
+  asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(y));
+  split_f32x2(add_f32x2(f32x2(x, y), f32x2(1.0f, 1.0f)), x, y);
+  asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(x));
+  asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(y));
+  return f32x2(x, y);
+}
 MOE_DEV float2 unpack_bf16x2(uint32_t v) { return __bfloat1622float2(*reinterpret_cast<__nv_bfloat162*>(&v)); }
 
 // silu(g) = g sigma(g) with sigma(g) = (1 + tanh(g / 2)) / 2 from the

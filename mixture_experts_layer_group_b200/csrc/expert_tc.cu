@@ -424,6 +424,167 @@ MOE_DEV void store_row32(__nv_bfloat16* dst, int ncols, const uint4 (&v)[4]) {
   }
 }
 
+// Address of a lane's row for the transposing matrix moves between a 32 x 32
+// block in the accumulator's m16n8 layout and its [token][feature] tile (64-byte
+// swizzled): matrix m of (hf, rp) is column group r = 2 rp + m / 2 and feature
+// octet e = m % 2 of the lane half hf.
+MOE_DEV uint32_t tile_row_addr(uint32_t tile, int hf, int rp) {
+  const int lane = threadIdx.x & 31, m = lane >> 3, k = lane & 7;
+  const int t = 8 * (2 * rp + (m >> 1)) + k;  // token row this lane addresses
+  const int c = 2 * hf + (m & 1);             // feature chunk
+  return tile + t * 64 + ((c ^ ((t >> 1) & 3)) << 4);
+}
+
+// g and u of one block (32 tokens x 32 features) of gu, 16 bytes per load.
+struct GuBlock {
+  uint4 v[2][4];
+  MOE_DEV void load(const __nv_bfloat16* gu, int cols, int64_t row, int left, int c0) {
+    const int lane = threadIdx.x & 31, c = c0 + 8 * (lane & 3);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int t = 8 * i + (lane >> 2);
+      const bool in = t < left && c < cols;  // 8 columns are all in or all out
+      const __nv_bfloat16* src = gu + (row + t) * 2 * cols + c;
+      v[0][i] = in ? __ldg(reinterpret_cast<const uint4*>(src)) : make_uint4(0, 0, 0, 0);
+      v[1][i] = in ? __ldg(reinterpret_cast<const uint4*>(src + cols)) : make_uint4(0, 0, 0, 0);
+    }
+  }
+  MOE_DEV void put(uint32_t tiles) const {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int t = 8 * i + (lane >> 2);
+      const uint32_t at = tiles + t * 64 + (((lane & 3) ^ ((t >> 1) & 3)) << 4);
+      st_shared_v4(at, v[0][i]);
+      st_shared_v4(at + kTileBytes, v[1][i]);
+    }
+  }
+};
+
+// Epilogue of a kDh unit for one warp: blocks of 32 tokens x the warp's 32
+// features of each half, q from tensor memory, g and u from gu. Per element,
+// with s = sigma(g), act = g s, h = act u, dh = gate q:
+//   dgate += q h   du = dh act   dg = dh u (s + s (g - act))   gh = gate h
+// in packed fp32 pairs (two tokens). Per block a thread spends 64 special
+// function operations, which bound it: about 1000 cycles for the two warps
+// of a scheduler. The next block's g and u load meanwhile; the tiles of the
+// three results are written in place of g and u (one TMA store each), and the
+// sum over the block's features of q h is folded over the lanes after them.
+MOE_DEV void dh_epilogue(const BwdParams& p, const Unit& un, int64_t row_base, uint32_t t_q, uint32_t stride,
+                         uint8_t* tiles, int c_first, int sub, int subs) {
+  const int lane = threadIdx.x & 31, cols = p.cols_routed;
+  const uint32_t tile = smem_u32(tiles);
+  const int tok_blocks = (un.ntok + 31) / 32;
+  const int per_half = (tok_blocks - sub + subs - 1) / subs;  // this warp's blocks of a half (0: none)
+  // (features at or past the matrix's width belong to a tile that reaches past it)
+  const int blocks = c_first >= cols ? 0 : c_first + 128 >= cols ? per_half : 2 * per_half;
+  if (blocks <= 0) return;
+  auto c_of = [&](int b) { return c_first + (b >= per_half ? 128 : 0); };
+  auto j_of = [&](int b) { return 32 * (sub + subs * (b >= per_half ? b - per_half : b)); };
+  GuBlock gu;
+  gu.load(p.gu, cols, row_base + j_of(0), un.ntok - j_of(0), c_of(0));
+#pragma unroll 1
+  for (int b = 0; b < blocks; ++b) {
+    const int c0 = c_of(b), j0 = j_of(b);
+    const uint32_t t_b = t_q + (b >= per_half ? stride : 0) + j0;
+    uint32_t a[2][16];
+    tmem_ld16x256b_x4(t_b, a[0]);
+    tmem_ld16x256b_x4(t_b + (16u << 16), a[1]);
+    const int tok = j0 + lane;
+    float my_gate = 1.0f;
+    if (p.gate_perm && tok < un.ntok && MOE_IN_BOUNDS(row_base + tok < p.tok_rows_routed, p.status))
+      my_gate = __ldg(p.gate_perm + row_base + tok);
+    if (lane == 0) bulk_wait_group_read<0>();  // the previous block's stores have read the tiles
+    __syncwarp();
+    gu.put(tile);
+    __syncwarp();
+    if (b + 1 < blocks) gu.load(p.gu, cols, row_base + j_of(b + 1), un.ntok - j_of(b + 1), c_of(b + 1));
+    uint64_t dgate[4];
+    tmem_wait_ld();
+#pragma unroll
+    for (int hf = 0; hf < 2; ++hf) {
+      uint32_t pg[4][2], pu[4][2], ph[4][2];
+#pragma unroll
+      for (int rp = 0; rp < 2; ++rp) {
+        const uint32_t at = tile_row_addr(tile, hf, rp);
+        ldmatrix_x4_trans(at, pg[2 * rp][0], pg[2 * rp][1], pg[2 * rp + 1][0], pg[2 * rp + 1][1]);
+        ldmatrix_x4_trans(at + kTileBytes, pu[2 * rp][0], pu[2 * rp][1], pu[2 * rp + 1][0], pu[2 * rp + 1][1]);
+      }
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int tq = 8 * r + 2 * (lane & 3);
+        const uint64_t gate = f32x2(__shfl_sync(0xffffffffu, my_gate, tq), __shfl_sync(0xffffffffu, my_gate, tq + 1));
+        if (hf == 0) dgate[r] = 0;  // (0.0f, 0.0f)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int x = 4 * r + 2 * e;
+          const uint64_t q = f32x2(__uint_as_float(a[hf][x]), __uint_as_float(a[hf][x + 1]));
+          const uint64_t g = bf16x2_to_f32x2(pg[r][e]), u = bf16x2_to_f32x2(pu[r][e]);
+          const uint64_t s = sigmoid_f32x2(g), act = mul_f32x2(g, s), h = mul_f32x2(act, u), dh = mul_f32x2(gate, q);
+          dgate[r] = fma_f32x2(q, h, dgate[r]);
+          const uint64_t rest = fma_f32x2(act, f32x2(-1.0f, -1.0f), g);  // g - act
+          pg[r][e] = f32x2_to_bf16x2(mul_f32x2(mul_f32x2(dh, u), fma_f32x2(s, rest, s)));
+          pu[r][e] = f32x2_to_bf16x2(mul_f32x2(dh, act));
+          ph[r][e] = f32x2_to_bf16x2(mul_f32x2(gate, h));
+        }
+      }
+      __syncwarp();  // every lane has read this half's chunks
+#pragma unroll
+      for (int rp = 0; rp < 2; ++rp) {
+        const uint32_t at = tile_row_addr(tile, hf, rp);
+        stmatrix_x4_trans(at, pg[2 * rp][0], pg[2 * rp][1], pg[2 * rp + 1][0], pg[2 * rp + 1][1]);
+        stmatrix_x4_trans(at + kTileBytes, pu[2 * rp][0], pu[2 * rp][1], pu[2 * rp + 1][0], pu[2 * rp + 1][1]);
+        stmatrix_x4_trans(at + 2 * kTileBytes, ph[2 * rp][0], ph[2 * rp][1], ph[2 * rp + 1][0], ph[2 * rp + 1][1]);
+      }
+    }
+    if (j0 + 32 <= un.ntok && c0 + 32 <= cols) {
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        (void)MOE_IN_BOUNDS(row_base + j0 + 32 <= p.out_rows_routed, p.status);
+        const int row = (int)(row_base + j0);
+        tma_store_2d(&p.o_g, tiles, c0, row);
+        tma_store_2d(&p.o_u, tiles + kTileBytes, c0, row);
+        tma_store_2d(&p.o_routed, tiles + 2 * kTileBytes, c0, row);
+        bulk_commit_group();
+      }
+    } else {
+      __syncwarp();
+      const int64_t row = row_base + tok;
+      if (tok < un.ntok && c0 < cols && MOE_IN_BOUNDS(row < p.out_rows_routed, p.status)) {
+#pragma unroll
+        for (int i = 0; i < 3; ++i) {
+          uint4 rowv[4];
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            rowv[c] = ld_shared_v4(tile + i * kTileBytes + lane * 64 + ((c ^ ((lane >> 1) & 3)) << 4));
+          store_row32((i == 0 ? p.out_g : i == 1 ? p.out_u : p.out_routed) + row * cols + c0, cols - c0, rowv);
+        }
+      }
+    }
+    if (p.part) {
+      // fold the 8 partial sums of the 8 lanes that share lane % 4 (each holds
+      // other features of the same tokens): after the exchanges lane 4 j + i
+      // holds the block's sum for token 8 (j / 2) + 2 i + j % 2
+      float v[8];
+#pragma unroll
+      for (int r = 0; r < 4; ++r) split_f32x2(dgate[r], v[2 * r], v[2 * r + 1]);
+#pragma unroll
+      for (int w = 4; w >= 1; w >>= 1) {
+        const bool upper = lane & (4 * w);
+#pragma unroll
+        for (int i = 0; i < w; ++i) {
+          const float keep = upper ? v[i + w] : v[i], give = upper ? v[i] : v[i + w];
+          v[i] = keep + __shfl_xor_sync(0xffffffffu, give, 4 * w);
+        }
+      }
+      const int j = lane >> 2, t = j0 + 8 * (j >> 1) + 2 * (lane & 3) + (j & 1);
+      if (c0 < cols && t < un.ntok && MOE_IN_BOUNDS(row_base + t < p.tok_rows_routed, p.status))
+        p.part[(int64_t)(c0 >> 5) * p.tok_rows_routed + row_base + t] = v[0];
+    }
+  }
+}
+
 template <int MODE, bool FP8>
 __global__ void __launch_bounds__(Plan<FP8>::kThreads, 1)
     expert_gemm_tc_kernel(const __grid_constant__ typename ParamsOf<MODE>::type p) {
@@ -822,7 +983,10 @@ __global__ void __launch_bounds__(Plan<FP8>::kThreads, 1)
       const int64_t ld = shared ? p.ld_shared : p.ld_routed;
       const int cols = shared ? p.cols_shared : p.cols_routed;
       const uint32_t t_q = tmem_base + ((uint32_t)(q * 32) << 16) + base;
-      constexpr int kHalves = is_swiglu(MODE) ? 1 : 2;
+      constexpr int kHalves = MODE == kDh ? 0 : is_swiglu(MODE) ? 1 : 2;
+      if constexpr (MODE == kDh)
+        dh_epilogue(p, un, row_base, t_q, stride, reinterpret_cast<uint8_t*>(tile), un.f * p.tile_cols + rank_rows + 32 * q,
+                    sub, kEpiWarps / 4);
 #pragma unroll 1
       for (int hh = 0; hh < kHalves; ++hh) {
         // this warp's 32 output columns of the unit
@@ -833,7 +997,7 @@ __global__ void __launch_bounds__(Plan<FP8>::kThreads, 1)
           const int64_t row = row_base + tok;
           // gate of this lane's token, spread to the lanes that hold it below
           float my_gate = 1.0f;
-          if ((MODE == kGateDown || MODE == kDh) && !shared && p.gate_perm && tok < un.ntok &&
+          if (MODE == kGateDown && !shared && p.gate_perm && tok < un.ntok &&
               MOE_IN_BOUNDS(row < p.tok_rows_routed, p.status))
             my_gate = __ldg(p.gate_perm + row);
           // The block (32 features = this quadrant's TMEM lanes, x 32 tokens =
@@ -841,54 +1005,9 @@ __global__ void __launch_bounds__(Plan<FP8>::kThreads, 1)
           // group r give this thread features 16 hf + 8 e + lane / 4 (e = 0, 1)
           // and tokens 8 r + 2 (lane % 4) + 0..1, packed as bf16 pairs.
           uint32_t pk[2][4][2];
-          uint32_t pg[2][4][2], pu[2][4][2];  // training: g and u (keep), or dg and du
+          uint32_t pg[2][4][2], pu[2][4][2];  // kSwiGLUKeep: g and u
           const int tq = 2 * (lane & 3);
           const uint32_t tile_addr = smem_u32(tile);
-          // the shared-memory address of this lane's row for the transposing
-          // matrix moves: matrix m of (hf, rp) is column group r = 2 rp + m / 2
-          // and feature octet e = m % 2
-          auto mat_addr = [&](int i, int hf, int rp) {
-            const int m = lane >> 3, k = lane & 7;
-            const int t = 8 * (2 * rp + (m >> 1)) + k;  // token row this lane addresses
-            const int c = 2 * hf + (m & 1);             // feature chunk
-            return tile_addr + i * kTileBytes + t * 64 + ((c ^ ((t >> 1) & 3)) << 4);
-          };
-          if constexpr (MODE == kDh) {
-            // g and u of the block into tiles 0 and 1 (coalesced 16-byte loads,
-            // the tile's swizzle), then into the accumulator's layout
-            uint4 v[2][4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int t = 8 * i + (lane >> 2), c = c0 + 8 * (lane & 3);
-              const bool in = j0 + t < un.ntok && c < cols;  // 8 columns are all in or all out
-              const __nv_bfloat16* src = p.gu + (row_base + j0 + t) * 2 * cols + c;
-              v[0][i] = in ? __ldg(reinterpret_cast<const uint4*>(src)) : make_uint4(0, 0, 0, 0);
-              v[1][i] = in ? __ldg(reinterpret_cast<const uint4*>(src + cols)) : make_uint4(0, 0, 0, 0);
-            }
-            if (lane == 0) bulk_wait_group_read<0>();  // the previous block's stores have read the tiles
-            __syncwarp();
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int t = 8 * i + (lane >> 2);
-              const uint32_t at = tile_addr + t * 64 + (((lane & 3) ^ ((t >> 1) & 3)) << 4);
-              st_shared_v4(at, v[0][i]);
-              st_shared_v4(at + kTileBytes, v[1][i]);
-            }
-            __syncwarp();
-#pragma unroll
-            for (int hf = 0; hf < 2; ++hf)
-#pragma unroll
-              for (int rp = 0; rp < 2; ++rp) {
-                ldmatrix_x4_trans(mat_addr(0, hf, rp), pg[hf][2 * rp][0], pg[hf][2 * rp][1], pg[hf][2 * rp + 1][0],
-                                  pg[hf][2 * rp + 1][1]);
-                ldmatrix_x4_trans(mat_addr(1, hf, rp), pu[hf][2 * rp][0], pu[hf][2 * rp][1], pu[hf][2 * rp + 1][0],
-                                  pu[hf][2 * rp + 1][1]);
-              }
-            __syncwarp();
-          }
-          float dgate[4][2];  // kDh: sum over this lane's features of q h, per token
-#pragma unroll
-          for (int r = 0; r < 4; ++r) dgate[r][0] = dgate[r][1] = 0.f;
 #pragma unroll
           for (int hf = 0; hf < 2; ++hf) {
             uint32_t a[16];
@@ -905,45 +1024,23 @@ __global__ void __launch_bounds__(Plan<FP8>::kThreads, 1)
                   const float g0 = __uint_as_float(a[x]), g1 = __uint_as_float(a[x + 1]);
                   const float u0 = __uint_as_float(b[x]), u1 = __uint_as_float(b[x + 1]);
                   if (MODE == kSwiGLUKeep) {
+                    const uint64_t g = f32x2(g0, g1), u = f32x2(u0, u1);
                     pg[hf][r][e] = pack_bf16x2(g0, g1);
                     pu[hf][r][e] = pack_bf16x2(u0, u1);
-                    pk[hf][r][e] = pack_bf16x2(g0 * sigmoid_fast(g0) * u0, g1 * sigmoid_fast(g1) * u1);
+                    pk[hf][r][e] = f32x2_to_bf16x2(mul_f32x2(mul_f32x2(g, sigmoid_f32x2(g)), u));
                   } else {
                     pk[hf][r][e] = pack_bf16x2(silu_tanh(g0) * u0, silu_tanh(g1) * u1);
                   }
                 }
-            } else if (MODE == kDh) {
-              tmem_wait_ld();
-#pragma unroll
-              for (int r = 0; r < 4; ++r) {
-                const float w0 = __shfl_sync(0xffffffffu, my_gate, 8 * r + tq);
-                const float w1 = __shfl_sync(0xffffffffu, my_gate, 8 * r + tq + 1);
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                  const int x = 4 * r + 2 * e;
-                  const float q[2] = {__uint_as_float(a[x]), __uint_as_float(a[x + 1])};
-                  const float2 g2 = unpack_bf16x2(pg[hf][r][e]), u2 = unpack_bf16x2(pu[hf][r][e]);
-                  const float gv[2] = {g2.x, g2.y}, uv[2] = {u2.x, u2.y}, gate[2] = {w0, w1};
-                  float og[2], ou[2], oh[2];
-#pragma unroll
-                  for (int z = 0; z < 2; ++z) {
-                    const float sg = sigmoid_fast(gv[z]), act = gv[z] * sg, h = act * uv[z], dh = gate[z] * q[z];
-                    dgate[r][z] = fmaf(q[z], h, dgate[r][z]);
-                    ou[z] = dh * act;
-                    og[z] = dh * uv[z] * fmaf(sg, gv[z] - act, sg);  // sg (1 + g (1 - sg))
-                    oh[z] = gate[z] * h;
-                  }
-                  pg[hf][r][e] = pack_bf16x2(og[0], og[1]);
-                  pu[hf][r][e] = pack_bf16x2(ou[0], ou[1]);
-                  pk[hf][r][e] = pack_bf16x2(oh[0], oh[1]);
-                }
-              }
             } else {
               tmem_wait_ld();
 #pragma unroll
               for (int r = 0; r < 4; ++r) {
-                const float g0 = __shfl_sync(0xffffffffu, my_gate, 8 * r + tq);
-                const float g1 = __shfl_sync(0xffffffffu, my_gate, 8 * r + tq + 1);
+                float g0 = 1.0f, g1 = 1.0f;
+                if (MODE == kGateDown) {
+                  g0 = __shfl_sync(0xffffffffu, my_gate, 8 * r + tq);
+                  g1 = __shfl_sync(0xffffffffu, my_gate, 8 * r + tq + 1);
+                }
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                   const int x = 4 * r + 2 * e;
@@ -952,38 +1049,18 @@ __global__ void __launch_bounds__(Plan<FP8>::kThreads, 1)
               }
             }
           }
-          if constexpr (MODE == kDh) {
-            if (p.part && c0 < cols) {  // the block's 32 features of each token, in a fixed order
-#pragma unroll
-              for (int r = 0; r < 4; ++r)
-#pragma unroll
-                for (int z = 0; z < 2; ++z) {
-                  float v = dgate[r][z];
-                  v += __shfl_xor_sync(0xffffffffu, v, 4);
-                  v += __shfl_xor_sync(0xffffffffu, v, 8);
-                  v += __shfl_xor_sync(0xffffffffu, v, 16);
-                  const int t = j0 + 8 * r + tq + z;
-                  if (lane < 4 && t < un.ntok &&
-                      MOE_IN_BOUNDS(row_base + t < p.tok_rows_routed, p.status))
-                    p.part[(int64_t)(c0 >> 5) * p.tok_rows_routed + row_base + t] = v;
-                }
-            }
-          }
           // Transpose into this warp's [32 tokens][32 features] tile, 64-byte
           // swizzled (16-byte chunk c of token row t sits at chunk c ^ ((t >> 1) & 3)),
-          // with four transposing matrix stores: matrix m of store (hf, rp) is
-          // column group r = 2 rp + m / 2 and feature octet e = m % 2.
-          if (MODE != kDh) {
-            if (lane == 0) bulk_wait_group_read<0>();  // the previous block's store has read the tile
-            __syncwarp();
-          }
+          // with four transposing matrix stores.
+          if (lane == 0) bulk_wait_group_read<0>();  // the previous block's store has read the tile
+          __syncwarp();
           auto put = [&](int i, const uint32_t (&v)[2][4][2]) {
 #pragma unroll
             for (int hf = 0; hf < 2; ++hf)
 #pragma unroll
               for (int rp = 0; rp < 2; ++rp)
-                stmatrix_x4_trans(mat_addr(i, hf, rp), v[hf][2 * rp][0], v[hf][2 * rp][1], v[hf][2 * rp + 1][0],
-                                  v[hf][2 * rp + 1][1]);
+                stmatrix_x4_trans(tile_row_addr(tile_addr + i * kTileBytes, hf, rp), v[hf][2 * rp][0],
+                                  v[hf][2 * rp][1], v[hf][2 * rp + 1][0], v[hf][2 * rp + 1][1]);
           };
           put(0, pk);
           if constexpr (is_wide(MODE)) {
