@@ -353,9 +353,8 @@ __global__ void __launch_bounds__(kThreads, 1) wgrad_tc_kernel(const __grid_cons
         phase ^= 1u << s;
         // rows v .. (the next multiple of 16) - 1 of the four boxes, 128 bytes each
         const uint32_t at = smem_u32(smem + s * kStageBytes);
-        const int words = 8 * ((16 - v % 16));
-        for (int i = lane; i < 4 * words; i += 32)
-          st_shared_v4(at + (i / words) * kBox + v * 128 + (i % words) * 16, make_uint4(0, 0, 0, 0));
+        for (int r = v; r & 15; ++r)
+          st_shared_v4(at + (lane >> 3) * kBox + r * 128 + (lane & 7) * 16, make_uint4(0, 0, 0, 0));
         fence_proxy_async_smem();
         __syncwarp();
         // (an asynchronous store: a remote arrive would hold this warp for about 1000 cycles)
