@@ -4,11 +4,17 @@
 // dW_r = dz^T x, and its dx = (dz^T)^T W_r over the experts as rows). Both operands are row-major with the rows as the reduction,
 // so both are MN-major tiles: a 64 x 64 TMA box is 64 rows (k) of 128 bytes.
 //
-// CTA pairs (clusters of 2, cta_group::2): a unit is one 256 x 256 tile of one
-// group's matrix; CTA r loads 128 columns of A and 128 of B per 64 rows (32
-// KB, six stages) and keeps rows 128 r .. 128 r + 127 of the tile in its
-// tensor memory, in one of two 256-column buffers, so a unit's MMAs overlap
-// the previous unit's stores. Units are taken with a fixed stride.
+// CTA pairs (clusters of 2, cta_group::2): a unit is two 256 x 256 tiles of
+// one group's matrix that share an operand (side by side along M or along N;
+// one tile at an odd edge). Per 64 rows CTA r loads 128 columns of the shared
+// operand and 128 of each tile's own (48 KB, four stages), and keeps rows 128 r
+// .. 128 r + 127 of each tile in its tensor memory (256 columns a tile). What
+// bounds a long sum is the operands' way from L2: 48 KB feed 1024 cycles of
+// pair MMAs; with one tile per unit it was 64 KB, and the MMAs waited a quarter
+// of their time. A unit of one tile takes one of the two buffers, so it overlaps
+// its neighbour; between units of two tiles the first tile's MMAs of two stages
+// run while the second tile is still being read. Units are taken with a fixed
+// stride.
 //
 // A group's last stage may hold up to 15 rows of the next group inside its
 // last K = 16 step. They would enter the sum, and a NaN there cannot be
@@ -28,8 +34,10 @@ namespace {
 constexpr int kBK = 64;
 constexpr int kTile = 256;
 constexpr int kBox = 64 * kBK * 2;           // 8 KB
-constexpr int kStageBytes = 4 * kBox;        // A: two boxes, B: two boxes
-constexpr int kStages = 6;
+constexpr int kPart = 2 * kBox;              // 128 columns of an operand
+constexpr int kStageBytes = 3 * kPart;       // the shared operand, then each tile's own
+constexpr int kStages = 4;
+constexpr int kLead = 2;                     // stages whose second tile follows later at a unit's start
 constexpr int kEpiWarps = 8;
 constexpr int kThreads = 32 * (3 + kEpiWarps);
 constexpr int kOutTile = 32 * 128;           // 32 rows x 128 bytes per epilogue warp
@@ -41,7 +49,9 @@ struct Matrix {
   CUtensorMap a;    // [R, M]
   CUtensorMap b;    // [R, N]
   CUtensorMap out;  // [groups, M, N]
-  int M, N, mt, nt;
+  int M, N, mt, nt;  // units along M and N
+  int split_m;       // a unit's tiles lie along M (else along N)
+  int per_unit;      // tiles of a unit at most: 1 or 2
 };
 struct Params {
   Matrix mat[3];
@@ -57,8 +67,8 @@ struct Shared {
   uint64_t full[kStages];      // CTA 0: the stage's bytes of both CTAs landed (and were fixed)
   uint64_t empty[kStages];     // both: the MMAs finished reading the stage
   uint64_t landed[kStages];    // each CTA: its own bytes of a stage that needs fixing landed
-  uint64_t acc_full[2];        // both
-  uint64_t acc_empty[2];       // CTA 0
+  uint64_t acc_full[2];        // both: the buffer's tile is complete
+  uint64_t acc_empty[2];       // CTA 0: both CTAs' epilogues have read it
   uint64_t drained;            // both
   uint32_t tmem_base;
   uint32_t sink;               // target of CTA 1's signalling stores (never read)
@@ -69,6 +79,7 @@ static_assert(sizeof(Shared) <= 512, "barrier block");
 
 struct Unit {
   int g, mat, m0, n0, row0, rows;
+  int tiles;  // 1 or 2
 };
 MOE_DEV Unit decode(const Params& p, int u) {
   Unit t{};
@@ -81,11 +92,25 @@ MOE_DEV Unit decode(const Params& p, int u) {
     left -= p.mat[t.mat].mt * p.mat[t.mat].nt;
     ++t.mat;
   }
-  const int nt = p.mat[t.mat].nt;
-  t.m0 = left / nt * kTile;
-  t.n0 = (left - left / nt * nt) * kTile;
+  const Matrix& x = p.mat[t.mat];
+  const int mi = left / x.nt, ni = left - mi * x.nt;
+  t.m0 = mi * (x.split_m ? x.per_unit * kTile : kTile);
+  t.n0 = ni * (x.split_m ? kTile : x.per_unit * kTile);
+  t.tiles = x.per_unit == 2 && (x.split_m ? x.M - t.m0 : x.N - t.n0) > kTile ? 2 : 1;
   return t;
 }
+// Which accumulator buffers a unit takes: both, or the one whose turn it is.
+// Every role replays the same sequence.
+struct Buffers {
+  uint32_t next = 0, uses[2] = {0u, 0u};
+  uint32_t first = 0;
+  MOE_DEV void take(int tiles) {
+    first = tiles == 2 ? 0u : next;
+    next = tiles == 2 ? 0u : next ^ 1u;
+  }
+  // parity of the phase of the buffer's next use
+  MOE_DEV uint32_t parity(uint32_t b) const { return uses[b] & 1u; }
+};
 // A pair's units, u = pair, pair + pairs, ...: the next one is decoded while
 // the current one is worked on (its two table reads and divisions cost about
 // 900 cycles otherwise, in every role).
@@ -129,6 +154,7 @@ __global__ void __launch_bounds__(kThreads, 1) wgrad_tc_kernel(const __grid_cons
   const bool first = rank == 0;
   Walk walk(p, (int)(blockIdx.x >> 1), (int)(gridDim.x >> 1));
   Unit t;
+  Buffers buf;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
@@ -172,7 +198,11 @@ __global__ void __launch_bounds__(kThreads, 1) wgrad_tc_kernel(const __grid_cons
         const Matrix& x = p.mat[t.mat];
         const int nk = (t.rows + kBK - 1) / kBK;
         const bool ragged = tail_rows(t.rows) % 16 != 0;
-        const int ca = t.m0 + 128 * (int)rank, cb = t.n0 + 128 * (int)rank;
+        // the shared operand's columns, and the first tile's own
+        const CUtensorMap* ts = x.split_m ? &x.b : &x.a;
+        const CUtensorMap* to = x.split_m ? &x.a : &x.b;
+        const int cs = (x.split_m ? t.n0 : t.m0) + 128 * (int)rank, co = (x.split_m ? t.m0 : t.n0) + 128 * (int)rank;
+        const uint32_t bytes = (1 + t.tiles) * kPart;
         for (int kc = 0; kc < nk; ++kc, ++fills) {
             const uint32_t s = fills % kStages;
             if (!mbar_wait_cluster_bounded(&sh.empty[s], ((fills / kStages) & 1u) ^ 1u, abort_flag)) {
@@ -184,21 +214,21 @@ __global__ void __launch_bounds__(kThreads, 1) wgrad_tc_kernel(const __grid_cons
             const bool fix = ragged && kc == nk - 1;
             if (fix) {
               // this CTA's bytes land on its own barrier; the fixers hand the stage on
-              mbar_arrive_expect_tx(&sh.landed[s], kStageBytes);
+              mbar_arrive_expect_tx(&sh.landed[s], bytes);
               if (first) mbar_arrive_expect_tx(&sh.full[s], 8);
-              for (int c = 0; c < 2; ++c) {
-                tma_load_2d_hint(dst + c * kBox, &x.a, &sh.landed[s], ca + 64 * c, r, pol);
-                tma_load_2d_hint(dst + (2 + c) * kBox, &x.b, &sh.landed[s], cb + 64 * c, r, pol);
-              }
+              for (int c = 0; c < 2; ++c) tma_load_2d_hint(dst + c * kBox, ts, &sh.landed[s], cs + 64 * c, r, pol);
+              for (int h = 0; h < t.tiles; ++h)
+                for (int c = 0; c < 2; ++c)
+                  tma_load_2d_hint(dst + (1 + h) * kPart + c * kBox, to, &sh.landed[s], co + kTile * h + 64 * c, r, pol);
               fixes |= 1u << s;
               fix_phase ^= 1u << s;
             } else {
               const uint32_t bar = in_first(&sh.full[s]);
-              if (first) mbar_arrive_expect_tx(&sh.full[s], 2 * kStageBytes);
-              for (int c = 0; c < 2; ++c) {
-                tma_load_2d_pair(dst + c * kBox, &x.a, bar, ca + 64 * c, r, pol);
-                tma_load_2d_pair(dst + (2 + c) * kBox, &x.b, bar, cb + 64 * c, r, pol);
-              }
+              if (first) mbar_arrive_expect_tx(&sh.full[s], 2 * bytes);
+              for (int c = 0; c < 2; ++c) tma_load_2d_pair(dst + c * kBox, ts, bar, cs + 64 * c, r, pol);
+              for (int h = 0; h < t.tiles; ++h)
+                for (int c = 0; c < 2; ++c)
+                  tma_load_2d_pair(dst + (1 + h) * kPart + c * kBox, to, bar, co + kTile * h + 64 * c, r, pol);
               fixes &= ~(1u << s);
             }
           }
@@ -210,37 +240,60 @@ __global__ void __launch_bounds__(kThreads, 1) wgrad_tc_kernel(const __grid_cons
     if (first) {
       // the whole warp runs the loop, one elected lane issues
       const uint32_t idesc = idesc_bf16_f32(256, kTile) | kIdescAMn | kIdescBMn;
-      uint32_t consumed = 0, accs = 0;
+      uint32_t consumed = 0;
       bool ok = true;
+      auto wait = [&](uint64_t* bar, uint32_t parity) {
+        ok = __all_sync(0xffffffffu, mbar_wait_cluster_bounded(bar, parity, abort_flag));
+        if (ok) tc_fence_after();
+        return ok;
+      };
       while (ok && walk.take(p, t)) {
         const int rows = __shfl_sync(0xffffffffu, t.rows, 0);
+        const int tiles = __shfl_sync(0xffffffffu, t.tiles, 0);
         if (rows == 0) continue;
         const int nk = (rows + kBK - 1) / kBK;
         const int last_steps = (tail_rows(rows) + 15) / 16;
-        const uint32_t b = accs & 1u;
-        ok = __all_sync(0xffffffffu, mbar_wait_cluster_bounded(&sh.acc_empty[b], ((accs >> 1) & 1u) ^ 1u, abort_flag));
-        if (!ok) break;
-        ++accs;
-        tc_fence_after();
-        const uint32_t d = tmem_base + b * kTile;
-        for (int kc = 0; kc < nk; ++kc) {
-          const uint32_t s = consumed % kStages;
-          ok = __all_sync(0xffffffffu, mbar_wait_cluster_bounded(&sh.full[s], (consumed / kStages) & 1u, abort_flag));
-          if (!ok) break;
-          ++consumed;
-          tc_fence_after();
-          const uint64_t da = smem_desc_sw128_mn(smem_u32(smem) + s * kStageBytes, kBox);
-          const uint64_t db = da + (2 * kBox >> 4);
+        // tile operands by shared-memory part: A and B are the shared part 0 or the tile's own
+        const bool split_m = __shfl_sync(0xffffffffu, p.mat[t.mat].split_m, 0);
+        buf.take(tiles);
+        auto issue = [&](uint32_t j, int kc, int h, uint32_t b) {
+          const uint64_t shared = smem_desc_sw128_mn(smem_u32(smem) + (j % kStages) * kStageBytes, kBox);
+          const uint64_t own = shared + ((1 + h) * kPart >> 4);
+          const uint64_t da = split_m ? own : shared, db = split_m ? shared : own;
           const int steps = kc == nk - 1 ? last_steps : kBK / 16;
-          if (elect_one()) {
 #pragma unroll
-            for (int kk = 0; kk < kBK / 16; ++kk)
-              if (kk < steps) umma_bf16_pair(d, da + kk * (2048 >> 4), db + kk * (2048 >> 4), idesc, (kc | kk) != 0);
+          for (int kk = 0; kk < kBK / 16; ++kk)
+            if (kk < steps)
+              umma_bf16_pair(tmem_base + b * kTile, da + kk * (2048 >> 4), db + kk * (2048 >> 4), idesc, (kc | kk) != 0);
+        };
+        if (!wait(&sh.acc_empty[buf.first], buf.parity(buf.first) ^ 1u)) break;
+        ++buf.uses[buf.first];
+        const int lead = tiles == 2 ? (nk < kLead ? nk : kLead) : 0;
+        for (int kc = 0; kc < lead; ++kc) {
+          const uint32_t j = consumed + kc;
+          if (!wait(&sh.full[j % kStages], (j / kStages) & 1u)) break;
+          if (elect_one()) issue(j, kc, 0, 0);
+          __syncwarp();
+        }
+        if (!ok) break;
+        if (tiles == 2) {
+          if (!wait(&sh.acc_empty[1], buf.parity(1) ^ 1u)) break;
+          ++buf.uses[1];
+        }
+        for (int kc = 0; kc < nk; ++kc, ++consumed) {
+          const uint32_t s = consumed % kStages;
+          if (kc >= lead && !wait(&sh.full[s], (consumed / kStages) & 1u)) break;
+          if (elect_one()) {
+            if (kc >= lead) issue(consumed, kc, 0, buf.first);
+            if (tiles == 2) issue(consumed, kc, 1, 1);
             umma_commit_pair_both(smem_u32(&sh.empty[s]));
           }
           __syncwarp();
         }
-        if (ok && elect_one()) umma_commit_pair_both(smem_u32(&sh.acc_full[b]));
+        if (ok && elect_one()) {
+          umma_commit_pair_both(smem_u32(&sh.acc_full[buf.first]));
+          if (tiles == 2) umma_commit_pair_both(smem_u32(&sh.acc_full[1]));
+        }
         __syncwarp();
       }
       if (!ok && lane == 0) fail();
@@ -256,42 +309,39 @@ __global__ void __launch_bounds__(kThreads, 1) wgrad_tc_kernel(const __grid_cons
   } else if (warp < 2 + kEpiWarps) {
     const int q = warp & 3, ew = warp - 2, sub = ew >> 2;
     const uint32_t tile = smem_u32(out_tiles + ew * kOutTile);
-    uint32_t accs = 0;
+    // this warp's half of a tile's columns in 128-byte tile rows: converted to
+    // registers first, so that the buffer is free for the next MMAs before the stores
+    constexpr int kCols = F32 ? 32 : 64, kBlocks = kTile / kCols / 2;
     while (walk.take(p, t)) {
       if (t.rows == 0 && p.accumulate) continue;
       const Matrix& x = p.mat[t.mat];
-      const uint32_t b = accs & 1u;
       if (t.rows > 0) {
+        buf.take(t.tiles);
         int ok = 1;
-        if (lane == 0) ok = mbar_wait_cluster_bounded(&sh.acc_full[b], (accs >> 1) & 1u, abort_flag);
+        if (lane == 0)
+          for (int h = 0; h < t.tiles && ok; ++h)
+            ok = mbar_wait_cluster_bounded(&sh.acc_full[buf.first + h], buf.parity(buf.first + h), abort_flag);
         ok = __shfl_sync(0xffffffffu, ok, 0);
         if (!ok) {
           if (lane == 0) fail();
           break;
         }
-        ++accs;
         tc_fence_after();
       }
-      const int m = t.m0 + 128 * (int)rank + 32 * q;
-      const uint32_t t_q = tmem_base + ((uint32_t)(q * 32) << 16) + b * kTile;
-      // this warp's half of the columns in 128-byte tile rows: converted to
-      // registers first, so the accumulator is free for the next unit's MMAs
-      // before the stores
-      constexpr int kCols = F32 ? 32 : 64, kBlocks = kTile / kCols / 2;
+      const uint32_t t_q = tmem_base + ((uint32_t)(q * 32) << 16) + buf.first * kTile;
       uint32_t v[kBlocks][32];
-#pragma unroll
-      for (int i = 0; i < kBlocks; ++i) {
-        const int c = (2 * i + sub) * kCols;
+      auto read = [&](int h, int i) {  // block i of tile h to registers
+        const uint32_t at = t_q + h * kTile + (2 * i + sub) * kCols;
         if (t.rows == 0) {
 #pragma unroll
           for (int j = 0; j < 32; ++j) v[i][j] = 0u;
         } else if (F32) {
-          tmem_ld32(t_q + c, v[i]);
+          tmem_ld32(at, v[i]);
           tmem_wait_ld();
         } else {
           uint32_t w[32];
-          tmem_ld32(t_q + c, v[i]);
-          tmem_ld32(t_q + c + 32, w);
+          tmem_ld32(at, v[i]);
+          tmem_ld32(at + 32, w);
           tmem_wait_ld();
 #pragma unroll
           for (int j = 0; j < 16; ++j)
@@ -300,8 +350,11 @@ __global__ void __launch_bounds__(kThreads, 1) wgrad_tc_kernel(const __grid_cons
           for (int j = 0; j < 16; ++j)
             v[i][16 + j] = pack_bf16x2(__uint_as_float(w[2 * j]), __uint_as_float(w[2 * j + 1]));
         }
-      }
-      if (t.rows > 0) {
+      };
+      auto release = [&](int h) {
+        if (t.rows == 0) return;
+        const uint32_t b = buf.first + h;
+        ++buf.uses[b];
         tc_fence_before();
         __syncwarp();
         if (lane == 0) {
@@ -309,11 +362,11 @@ __global__ void __launch_bounds__(kThreads, 1) wgrad_tc_kernel(const __grid_cons
           else if (ew == 0) mbar_arrive_expect_tx(&sh.acc_empty[b], 4 * kEpiWarps);  // and CTA 1's warps' stores
           else mbar_arrive(&sh.acc_empty[b]);
         }
-      }
-#pragma unroll
-      for (int i = 0; i < kBlocks; ++i) {
-        const int n = t.n0 + (2 * i + sub) * kCols;
-        if (m >= x.M || n >= x.N) break;
+      };
+      auto store = [&](int h, int i) {
+        const int m = t.m0 + (x.split_m ? kTile * h : 0) + 128 * (int)rank + 32 * q;
+        const int n = t.n0 + (x.split_m ? 0 : kTile * h) + (2 * i + sub) * kCols;
+        if (m >= x.M || n >= x.N) return;
         if (lane == 0) bulk_wait_group_read<0>();  // the previous store has read the tile
         __syncwarp();
 #pragma unroll
@@ -327,6 +380,19 @@ __global__ void __launch_bounds__(kThreads, 1) wgrad_tc_kernel(const __grid_cons
           else tma_store_3d(&x.out, tile, n, m, t.g);
           bulk_commit_group();
         }
+      };
+#pragma unroll
+      for (int i = 0; i < kBlocks; ++i) read(0, i);
+      release(0);
+#pragma unroll
+      for (int i = 0; i < kBlocks; ++i) {
+        store(0, i);
+        if (t.tiles == 2) read(1, i);  // its registers are free again
+      }
+      if (t.tiles == 2) {
+        release(1);
+#pragma unroll
+        for (int i = 0; i < kBlocks; ++i) store(1, i);
       }
     }
     if (lane == 0) bulk_wait_group_all();
@@ -351,10 +417,13 @@ __global__ void __launch_bounds__(kThreads, 1) wgrad_tc_kernel(const __grid_cons
           break;
         }
         phase ^= 1u << s;
-        // rows v .. (the next multiple of 16) - 1 of the four boxes, 128 bytes each
+        // rows v .. (the next multiple of 16) - 1 of the four or six boxes, 128 bytes each
         const uint32_t at = smem_u32(smem + s * kStageBytes);
-        for (int r = v; r & 15; ++r)
-          st_shared_v4(at + (lane >> 3) * kBox + r * 128 + (lane & 7) * 16, make_uint4(0, 0, 0, 0));
+        for (int r = v; r & 15; ++r) {
+          const uint32_t row = at + (lane >> 3) * kBox + r * 128 + (lane & 7) * 16;
+          st_shared_v4(row, make_uint4(0, 0, 0, 0));
+          if (t.tiles == 2 && lane < 16) st_shared_v4(row + 4 * kBox, make_uint4(0, 0, 0, 0));
+        }
         fence_proxy_async_smem();
         __syncwarp();
         // (an asynchronous store: a remote arrive would hold this warp for about 1000 cycles)
@@ -405,8 +474,18 @@ cudaError_t launch_wgrad_tc(const WgradArgs& a, cudaStream_t s) {
     Matrix& x = p.mat[i];
     x.M = (int)w.M;
     x.N = w.N;
-    x.mt = (int)((w.M + kTile - 1) / kTile);
-    x.nt = (w.N + kTile - 1) / kTile;
+    // Two tiles side by side, along the dimension with an even number of them
+    // (all units then have two) or else along the longer one -- unless there
+    // are so few tiles that the coarser units leave pairs idle: a unit of two
+    // takes about 1.6 times a unit of one.
+    const int64_t tm = (w.M + kTile - 1) / kTile, tn = (w.N + kTile - 1) / kTile;
+    x.split_m = tm % 2 == tn % 2 ? tm >= tn : tm % 2 == 0;
+    const int64_t one = tm * tn, two = x.split_m ? (tm + 1) / 2 * tn : tm * ((tn + 1) / 2);
+    const int64_t pairs = device_sm_count() / 2;
+    auto rounds = [&](int64_t units) { return (units * a.groups + pairs - 1) / pairs; };
+    x.per_unit = 10 * rounds(one) <= 16 * rounds(two) ? 1 : 2;
+    x.mt = (int)(x.split_m ? (tm + x.per_unit - 1) / x.per_unit : tm);
+    x.nt = (int)(x.split_m ? tn : (tn + x.per_unit - 1) / x.per_unit);
     p.units_per_group += x.mt * x.nt;
     const uint64_t dims[3] = {(uint64_t)w.N, (uint64_t)w.M, (uint64_t)a.groups};
     const uint64_t stride[2] = {(uint64_t)w.N * elem, (uint64_t)w.N * w.M * elem};
