@@ -250,6 +250,7 @@ __global__ void __launch_bounds__(1024) dispatch_small_kernel(ChunkArgs ca, Scan
 // and the unit counters of the GEMMs start at zero.
 __global__ void __launch_bounds__(512) group_tables_kernel(const int32_t* __restrict__ counts_in, ScanArgs a,
                                                            unsigned* status, int* sched) {
+  griddep_launch_dependents();
   const int tid = threadIdx.x;
   if (tid < kSchedCounters) sched[tid] = 0;
   const int c = tid < a.N ? counts_in[tid] : 0;

@@ -601,7 +601,6 @@ __global__ void __launch_bounds__(Plan<FP8>::kThreads, 1)
   const int lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();  // 0: issues the pair MMAs and takes the units
   const bool first = rank == 0;
-  const int total_units = __ldg(p.unit_base + p.N + 1);
   // Weight rows of this CTA. SwiGLU: rows 128 r .. 128 r + 127 of the unit's
   // 256 features, taken from W1 (half 0) and from W3 (half 1). Down GEMM:
   // rows 256 r .. 256 r + 255 of the unit's 512 output columns, one
@@ -654,6 +653,11 @@ __global__ void __launch_bounds__(Plan<FP8>::kThreads, 1)
   tc_fence_before();
   cluster_sync();  // barriers and tensor memory of both CTAs are ready
   tc_fence_after();
+  // (programmatic launch: what a predecessor wrote, the unit tables among it,
+  // is read only after it has finished; the down GEMM's tables are older than
+  // its predecessor and its producer alone waits)
+  if (MODE != kGateDown) griddep_wait();
+  const int total_units = __ldg(p.unit_base + p.N + 1);
   const uint32_t tmem_base = sh.tmem_base;
   volatile int* abort_flag = &sh.abort_flag;
   auto peer = [&](const void* local) { return map_to_rank(smem_u32(local), rank ^ 1u); };
@@ -747,7 +751,7 @@ __global__ void __launch_bounds__(Plan<FP8>::kThreads, 1)
         if (u < 0) {
           // no units left for this CTA: the down GEMM may start on SMs as
           // they free up
-          if (is_swiglu(MODE)) griddep_launch_dependents();
+          if (MODE != kGateDown) griddep_launch_dependents();
           break;
         }
         const bool shared = un.g == p.N;
@@ -1390,9 +1394,9 @@ cudaError_t launch_expert_gemms_tc(const Problem& p, const GemmArgs& a, cudaStre
     gk.out_g = (__nv_bfloat16*)a.gu;
     gk.out_u = gk.out_g + p.F;
     gk.ld_g = 2 * (int64_t)p.F;
-    err = launch_one<kSwiGLUKeep, false>(gk, grid1, s, false);
+    err = launch_one<kSwiGLUKeep, false>(gk, grid1, s, a.sched_clear);
   } else {
-    err = fp8 ? launch_one<kSwiGLU, true>(g1, grid1, s, false) : launch_one<kSwiGLU, false>(g1, grid1, s, false);
+    err = fp8 ? launch_one<kSwiGLU, true>(g1, grid1, s, false) : launch_one<kSwiGLU, false>(g1, grid1, s, a.sched_clear);
   }
   if (err == cudaSuccess && between) err = cudaEventRecord(between, s);
   if (err != cudaSuccess) return err;
@@ -1477,8 +1481,9 @@ cudaError_t launch_experts_backward_tc(const Problem& p, const ExpertsBwdArgs& a
   h.a_rows_routed = p.F;
   h.gu = (const __nv_bfloat16*)a.gu;
   h.part = a.dgate_rows ? a.dgate_part : nullptr;
-  cudaError_t err = launch_one<kDh, false>(h, grid_of(p.F), s, false);
-  if (err == cudaSuccess && a.dgate_rows) err = launch_dgate_reduce(a.dgate_part, dgate_planes(p), p.R, a.dgate_rows, s);
+  cudaError_t err = launch_one<kDh, false>(h, grid_of(p.F), s, true);
+  if (err == cudaSuccess && a.dgate_rows)
+    err = launch_dgate_reduce(a.dgate_part, dgate_planes(p), p.R, a.dgate_rows, s);
   if (err != cudaSuccess) return err;
 
   if (a.dx_rows) {
@@ -1501,7 +1506,7 @@ cudaError_t launch_experts_backward_tc(const Problem& p, const ExpertsBwdArgs& a
     x.chunk_rows = cm;
     x.tok_rows_routed = x.out_rows_routed = p.R;
     x.a_rows_routed = p.d;
-    err = launch_one<kDx, false>(x, grid_of(p.d), s, false);
+    err = launch_one<kDx, false>(x, grid_of(p.d), s, true);
     if (err != cudaSuccess) return err;
   }
   if (!a.dW1) return cudaSuccess;
@@ -1517,6 +1522,7 @@ cudaError_t launch_experts_backward_tc(const Problem& p, const ExpertsBwdArgs& a
   w.grad_dtype = a.grad_dtype;
   w.accumulate = a.accumulate;
   w.status = a.status;
+  w.independent = a.dx_rows != nullptr;  // of the dx GEMM, which has waited for the dh GEMM
   return launch_wgrad_tc(w, s);
 }
 

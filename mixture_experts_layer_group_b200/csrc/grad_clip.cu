@@ -138,6 +138,7 @@ MOE_DEV double block_sum(double v) {
 template <int CAP>
 __global__ void __launch_bounds__(kThreads) square_sum_kernel(const __grid_constant__ Table<CAP> t,
                                                               double* __restrict__ part) {
+  griddep_launch_dependents();
   double sum = 0.0;
   for (int c = blockIdx.x; c < t.chunk0[t.n]; c += gridDim.x) {
     const Chunk ch = chunk_of(t, c);
@@ -149,6 +150,8 @@ __global__ void __launch_bounds__(kThreads) square_sum_kernel(const __grid_const
 
 __global__ void __launch_bounds__(kThreads) sum_parts_kernel(const double* __restrict__ part, int64_t n,
                                                              double* __restrict__ sumsq) {
+  griddep_launch_dependents();
+  griddep_wait();
   double sum = 0.0;
   for (int64_t i = threadIdx.x; i < n; i += kThreads) sum += part[i];
   sum = block_sum(sum);
@@ -200,6 +203,7 @@ template <int CAP>
 __global__ void __launch_bounds__(kThreads) clip_kernel(const __grid_constant__ Table<CAP> t,
                                                         const double* __restrict__ sumsq, float max_norm,
                                                         float* __restrict__ norm_out) {
+  griddep_wait();
   const double norm = sqrt(*sumsq);
   // a norm that is not finite leaves the gradients as they are
   const bool clip = norm > (double)max_norm && isfinite(norm);
@@ -267,9 +271,10 @@ template <int CAP>
 moe_status clip_batches(const moe_grad_tensor* x, int32_t n, const double* sumsq, float max_norm, float* norm_out,
                         bool* launched, cudaStream_t s) {
   return for_batches<CAP>(x, n, [&](const Table<CAP>& t, int chunks) {
-    clip_kernel<CAP><<<ctas(chunks), kThreads, 0, s>>>(t, sumsq, max_norm, *launched ? nullptr : norm_out);
+    const cudaError_t e =
+        launch_after(clip_kernel<CAP>, ctas(chunks), kThreads, s, t, sumsq, max_norm, *launched ? nullptr : norm_out);
     *launched = true;
-    return cudaGetLastError();
+    return e;
   });
 }
 
@@ -303,8 +308,7 @@ moe_status moe_grad_norm(const moe_grad_tensor* tensors, int32_t n, double* sums
   st = n <= kSmallTable ? norm_batches<kSmallTable>(tensors, n, part, &parts, s)
                         : norm_batches<kLargeTable>(tensors, n, part, &parts, s);
   if (st != MOE_OK) return st;
-  sum_parts_kernel<<<1, kThreads, 0, s>>>(part, parts, sumsq);
-  e = cudaGetLastError();
+  e = launch_after(sum_parts_kernel, 1, kThreads, s, part, parts, sumsq);
   if (e == cudaSuccess) e = note_device_use(ws, s);
   return e == cudaSuccess ? MOE_OK : cuda_fail(e);
 }
@@ -325,8 +329,7 @@ moe_status moe_grad_clip(const moe_grad_tensor* tensors, int32_t n, const double
     Table<kSmallTable> t;
     t.n = 0;
     t.chunk0[0] = 0;
-    clip_kernel<kSmallTable><<<1, kThreads, 0, s>>>(t, sumsq, max_norm, norm_out);
-    const cudaError_t e = cudaGetLastError();
+    const cudaError_t e = launch_after(clip_kernel<kSmallTable>, 1, kThreads, s, t, sumsq, max_norm, norm_out);
     if (e != cudaSuccess) return cuda_fail(e);
   }
   return MOE_OK;

@@ -222,12 +222,17 @@ struct WgradArgs {
   int grad_dtype;
   bool accumulate;   // fp32 only
   unsigned* status;
+  // The kernel before this one in the stream only starts after everything that
+  // this one reads is complete (it waited for that itself before it let its
+  // dependents start), and the two write different buffers: this one then need
+  // not wait for it to end before its own work.
+  bool independent;
 };
 cudaError_t launch_wgrad_tc(const WgradArgs& a, cudaStream_t s);
 int dgate_planes(const Problem& p);
 cudaError_t launch_experts_backward_tc(const Problem& p, const ExpertsBwdArgs& a, cudaStream_t s);
 cudaError_t launch_experts_backward_simt(const Problem& p, const ExpertsBwdArgs& a, cudaStream_t s);
-// dgate[r] = sum over the planes of part[plane][r], in order.
+// dgate[r] = sum over the planes of part[plane][r], in a fixed order.
 cudaError_t launch_dgate_reduce(const float* part, int planes, int64_t rows, float* dgate, cudaStream_t s);
 
 // The gradient of the logits (see route_bwd.cu), and the row tables of the
@@ -306,6 +311,22 @@ cudaError_t launch_combine_rows(const Problem& p, const void* routed_rows, const
                                 const void* more_rows = nullptr);
 
 int device_sm_count();
+
+// Launches a kernel with programmatic stream serialization: it may start while
+// its predecessor in the stream ends, and orders itself with griddep_wait().
+template <class... Params, class... Args>
+cudaError_t launch_after(void (*kernel)(Params...), unsigned blocks, unsigned threads, cudaStream_t s, Args&&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3(blocks, 1, 1);
+  cfg.blockDim = dim3(threads, 1, 1);
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<Params>(args)...);
+}
 
 // Keeps e as this host thread's moe_last_cuda_error() value.
 void record_cuda_error(cudaError_t e);

@@ -32,12 +32,13 @@ MOE_DEV float wmax(float v) {
 }
 
 constexpr int kDzTokens = 16;  // tokens of a CTA: 32-byte runs of the transposed dz
-constexpr int kDzWarps = 8;
+constexpr int kDzWarps = 16;
 
-// One warp per token, two in turn. Lane l holds experts 32 j + l, j < V; slot
+// One warp per token. Lane l holds experts 32 j + l, j < V; slot
 // i of the token sits in lane i.
 template <int V>
 __global__ void __launch_bounds__(32 * kDzWarps) route_dz_kernel(const __grid_constant__ RouteDzArgs a) {
+  griddep_launch_dependents();
   __shared__ __nv_bfloat16 tile[32 * V][kDzTokens + 2];  // [expert][token] (+2: rows start in different banks)
   if (blockIdx.x == 0 && threadIdx.x < kRouteTables) a.tables[threadIdx.x] = a.table_values[threadIdx.x];
   const int lane = threadIdx.x & 31;
@@ -146,6 +147,7 @@ __global__ void __launch_bounds__(32 * kDzWarps) route_dz_kernel(const __grid_co
 // dW = sum over the planes in order, rounded once (or added to an fp32 dW).
 __global__ void __launch_bounds__(256) join_planes_kernel(const float4* __restrict__ planes, int n, int64_t vecs,
                                                           void* __restrict__ dW, int f32, int accumulate) {
+  griddep_wait();
   const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
   if (i >= vecs) return;
   float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -187,9 +189,8 @@ cudaError_t launch_route_dz(const RouteDzArgs& a, cudaStream_t s) {
 cudaError_t launch_join_planes(const float* planes, int n, int64_t elems, void* dW, int grad_dtype, bool accumulate,
                                cudaStream_t s) {
   const int64_t vecs = elems / 4;
-  join_planes_kernel<<<(unsigned)((vecs + 255) / 256), 256, 0, s>>>(reinterpret_cast<const float4*>(planes), n, vecs,
-                                                                    dW, grad_dtype == MOE_F32, accumulate);
-  return cudaGetLastError();
+  return launch_after(join_planes_kernel, (unsigned)((vecs + 255) / 256), 256, s,
+                      reinterpret_cast<const float4*>(planes), n, vecs, dW, grad_dtype == MOE_F32, accumulate);
 }
 
 }  // namespace moe

@@ -278,22 +278,32 @@ cudaError_t launch_dw(const DwParams& p, cudaStream_t s) {
   return cudaGetLastError();
 }
 
-// One thread per row: the planes are added in order.
+// 32 rows per CTA; warp w adds planes w, w + 8, ..., then the warps' sums are
+// added in order (so that a row's planes are eight short chains of loads).
 __global__ void __launch_bounds__(256) dgate_reduce_kernel(const float* __restrict__ part, int planes, int64_t rows,
                                                            float* __restrict__ dgate) {
-  const int64_t r = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-  if (r >= rows) return;
+  griddep_launch_dependents();
+  griddep_wait();
+  __shared__ float sums[8][32];
+  const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t r = (int64_t)blockIdx.x * 32 + lane;
   float v = 0.f;
+  if (r < rows) {
 #pragma unroll 8
-  for (int i = 0; i < planes; ++i) v += part[i * rows + r];
+    for (int i = w; i < planes; i += 8) v += __ldg(part + i * rows + r);
+  }
+  sums[w][lane] = v;
+  __syncthreads();
+  if (w || r >= rows) return;
+#pragma unroll
+  for (int i = 1; i < 8; ++i) v += sums[i][lane];
   dgate[r] = v;
 }
 
 }  // namespace
 
 cudaError_t launch_dgate_reduce(const float* part, int planes, int64_t rows, float* dgate, cudaStream_t s) {
-  dgate_reduce_kernel<<<(unsigned)((rows + 255) / 256), 256, 0, s>>>(part, planes, rows, dgate);
-  return cudaGetLastError();
+  return launch_after(dgate_reduce_kernel, (unsigned)((rows + 31) / 32), 256, s, part, planes, rows, dgate);
 }
 
 cudaError_t launch_experts_backward_simt(const Problem& p, const ExpertsBwdArgs& a, cudaStream_t s) {

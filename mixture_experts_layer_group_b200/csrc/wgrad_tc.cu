@@ -61,6 +61,7 @@ struct Params {
   const int32_t* grp_rows;
   int accumulate;
   unsigned* status;
+  int independent;    // see WgradArgs
 };
 
 struct Shared {
@@ -152,9 +153,6 @@ __global__ void __launch_bounds__(kThreads, 1) wgrad_tc_kernel(const __grid_cons
   const int warp = uniform_warp_id(), lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
   const bool first = rank == 0;
-  Walk walk(p, (int)(blockIdx.x >> 1), (int)(gridDim.x >> 1));
-  Unit t;
-  Buffers buf;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
@@ -180,6 +178,10 @@ __global__ void __launch_bounds__(kThreads, 1) wgrad_tc_kernel(const __grid_cons
   tc_fence_before();
   cluster_sync();
   tc_fence_after();
+  if (!p.independent) griddep_wait();
+  Walk walk(p, (int)(blockIdx.x >> 1), (int)(gridDim.x >> 1));
+  Unit t;
+  Buffers buf;
   const uint32_t tmem_base = sh.tmem_base;
   volatile int* abort_flag = &sh.abort_flag;
   auto in_first = [&](const void* local) { return map_to_rank(smem_u32(local), 0u); };
@@ -233,6 +235,7 @@ __global__ void __launch_bounds__(kThreads, 1) wgrad_tc_kernel(const __grid_cons
             }
           }
       }
+      griddep_launch_dependents();
       if (!ok) fail();
     }
     __syncwarp();
@@ -448,6 +451,7 @@ __global__ void __launch_bounds__(kThreads, 1) wgrad_tc_kernel(const __grid_cons
       }
     }
   }
+  if (p.independent) griddep_wait();  // this grid ends after its predecessor
   tc_fence_before();
   cluster_sync();  // neither CTA leaves while the other may still touch its shared memory
   if (warp == 1) {
@@ -501,6 +505,7 @@ cudaError_t launch_wgrad_tc(const WgradArgs& a, cudaStream_t s) {
   p.grp_rows = a.grp_rows;
   p.accumulate = a.accumulate;
   p.status = a.status;
+  p.independent = a.independent;
   if (p.units == 0) return cudaSuccess;
 
   const bool f32 = a.grad_dtype == MOE_F32;
@@ -512,7 +517,9 @@ cudaError_t launch_wgrad_tc(const WgradArgs& a, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
   cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = 2;
   attr[0].val.clusterDim.y = 1;
@@ -539,6 +546,7 @@ cudaError_t launch_wgrad_tc(const WgradArgs& a, cudaStream_t s) {
   }
   if (p.units < clusters) clusters = p.units;
   cfg.gridDim = dim3(2 * clusters, 1, 1);
+  cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
@@ -568,6 +576,7 @@ cudaError_t launch_route_products_tc(const Problem& p, const RouteBwdArgs& a, cu
   w.grad_dtype = split ? (int)MOE_F32 : a.grad_dtype;
   w.accumulate = !split && a.accumulate;
   w.status = a.status;
+  w.independent = a.dx != nullptr;  // of the dx product, which has waited for dz
   const cudaError_t e = launch_wgrad_tc(w, s);
   if (e != cudaSuccess || !split) return e;
   return launch_join_planes(a.planes, a.splits, (int64_t)p.N * p.d, a.dW_r, a.grad_dtype, a.accumulate, s);
