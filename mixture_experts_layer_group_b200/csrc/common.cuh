@@ -517,17 +517,26 @@ MOE_DEV uint32_t f32x2_to_bf16x2(uint64_t v) {
   return pack_bf16x2(lo, hi);
 }
 
-// sigma(g) = 1 / (1 + 2^(-g log2 e)) of a pair, by the hardware's exponential
+// sigma(g) = 1 / (1 + 2^(-g log2 e)) of N pairs, by the hardware's exponential
 // and reciprocal; 0 where the power overflows.
-MOE_DEV uint64_t sigmoid_f32x2(uint64_t g) {
-  float x, y;
-  split_f32x2(mul_f32x2(g, f32x2(-1.4426950408889634f, -1.4426950408889634f)), x, y);
-  asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(x));
-  asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(y));
-  split_f32x2(add_f32x2(f32x2(x, y), f32x2(1.0f, 1.0f)), x, y);
-  asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(x));
-  asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(y));
-  return f32x2(x, y);
+template <int N>
+MOE_DEV void sigmoid_f32x2(const uint64_t (&g)[N], uint64_t (&s)[N]) {
+  float x[N], y[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) split_f32x2(mul_f32x2(g[i], f32x2(-1.4426950408889634f, -1.4426950408889634f)), x[i], y[i]);
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(x[i]));
+    asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(y[i]));
+  }
+#pragma unroll
+  for (int i = 0; i < N; ++i) split_f32x2(add_f32x2(f32x2(x[i], y[i]), f32x2(1.0f, 1.0f)), x[i], y[i]);
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(x[i]));
+    asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(y[i]));
+    s[i] = f32x2(x[i], y[i]);
+  }
 }
 MOE_DEV float2 unpack_bf16x2(uint32_t v) { return __bfloat1622float2(*reinterpret_cast<__nv_bfloat162*>(&v)); }
 

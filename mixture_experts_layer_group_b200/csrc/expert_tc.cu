@@ -166,10 +166,17 @@ static_assert(kMaxTok % (2 * kTokBox) == 0 && Plan<false>::kChunk <= kMaxTok && 
 
 // The forward's two GEMMs, the SwiGLU GEMM that also keeps g and u, and the
 // backward's two products on the weights (see BwdParams).
-enum Mode : int { kSwiGLU = 0, kGateDown = 1, kSwiGLUKeep = 2, kDh = 3, kDx = 4 };
+enum Mode : int { kSwiGLU = 0, kGateDown = 1, kSwiGLUKeep = 2, kDh = 3, kDx = 4, kDhWide = 5 };
 __host__ __device__ constexpr bool is_swiglu(int mode) { return mode == kSwiGLU || mode == kSwiGLUKeep; }
-__host__ __device__ constexpr bool is_bwd(int mode) { return mode == kDh || mode == kDx; }
-__host__ __device__ constexpr bool is_wide(int mode) { return mode == kSwiGLUKeep || mode == kDh; }
+__host__ __device__ constexpr bool is_dh(int mode) { return mode == kDh || mode == kDhWide; }
+__host__ __device__ constexpr bool is_bwd(int mode) { return is_dh(mode) || mode == kDx; }
+__host__ __device__ constexpr bool is_wide(int mode) { return mode == kSwiGLUKeep || is_dh(mode); }
+// One 128-row weight half per CTA instead of two: a unit then takes one of the
+// two accumulator buffers whatever its tokens, and its epilogue overlaps the
+// next unit's MMAs.
+__host__ __device__ constexpr bool one_half(int mode) { return mode == kDh; }
+// Weight bytes at the head of a bf16 stage.
+__host__ __device__ constexpr int a_bytes(int mode) { return one_half(mode) ? kHalfBytes : kATileBytes; }
 
 struct TcParams {
   // bf16 weights: bf16 maps of 64 x 128 boxes (128-byte swizzle; the down
@@ -216,8 +223,8 @@ struct TcParams {
 
 // The training modes' further parameters.
 //   kSwiGLUKeep  o_g, o_u: g and u halves of gu [R, 2 F]
-//   kDh  q^T = W2^T dy^T: A = W2 [N, d, F] taken MN-major (M = 512 of the F
-//        features, K = d), B = dy; epilogue dg, du, gate h -> o_g, o_u,
+//   kDh  q^T = W2^T dy^T: A = W2 [N, d, F] taken MN-major (M = 256, or in
+//        kDhWide 512, of the F features, K = d), B = dy; epilogue dg, du, gate h -> o_g, o_u,
 //        o_routed and the partial gate gradients
 //   kDx  dx^T = W1^T dg^T + W3^T du^T: A = W1 then W3 [N, F, d] MN-major
 //        (M = 512 of the d columns), B = dg then du; K = F twice
@@ -242,6 +249,10 @@ struct ParamsOf<kSwiGLUKeep> {
 };
 template <>
 struct ParamsOf<kDh> {
+  using type = BwdParams;
+};
+template <>
+struct ParamsOf<kDhWide> {
   using type = BwdParams;
 };
 template <>
@@ -289,9 +300,10 @@ MOE_DEV Unit decode_unit(const TcParams& p, int u) {
 // 0 and kCols / 2). bf16 (512 columns): buffers for n <= 128; FP8 (320):
 // n <= 64. The MMA issuer and every epilogue thread replay the same
 // sequence, so they agree on every placement.
-template <uint32_t kCols>
+// With one half per unit (kOne) every unit takes one of the two buffers.
+template <uint32_t kCols, bool kOne>
 struct AccPlan {
-  static constexpr uint32_t kHalf = (kCols / 4) & ~31u;
+  static constexpr uint32_t kHalf = kOne ? kCols / 2 : (kCols / 4) & ~31u;
   uint32_t next = 0;
   MOE_DEV void place(int n, uint32_t& mask, uint32_t& base, uint32_t& stride) const {
     if (n > (int)kHalf) {
@@ -470,19 +482,20 @@ struct GuBlock {
 // of a scheduler. The next block's g and u load meanwhile; the tiles of the
 // three results are written in place of g and u (one TMA store each), and the
 // sum over the block's features of q h is folded over the lanes after them.
-MOE_DEV void dh_epilogue(const BwdParams& p, const Unit& un, int64_t row_base, uint32_t t_q, uint32_t stride,
+MOE_DEV void dh_epilogue(const BwdParams& p, const Unit& un, int64_t row_base, uint32_t t_q, uint32_t stride, int halves,
                          uint8_t* tiles, int c_first, int sub, int subs) {
   const int lane = threadIdx.x & 31, cols = p.cols_routed;
   const uint32_t tile = smem_u32(tiles);
   const int tok_blocks = (un.ntok + 31) / 32;
   const int per_half = (tok_blocks - sub + subs - 1) / subs;  // this warp's blocks of a half (0: none)
   // (features at or past the matrix's width belong to a tile that reaches past it)
-  const int blocks = c_first >= cols ? 0 : c_first + 128 >= cols ? per_half : 2 * per_half;
+  if (halves == 2 && c_first + 128 >= cols) halves = 1;
+  const int blocks = c_first >= cols ? 0 : halves * per_half;
   if (blocks <= 0) return;
   auto c_of = [&](int b) { return c_first + (b >= per_half ? 128 : 0); };
   auto j_of = [&](int b) { return 32 * (sub + subs * (b >= per_half ? b - per_half : b)); };
   GuBlock gu;
-  gu.load(p.gu, cols, row_base + j_of(0), un.ntok - j_of(0), c_of(0));
+  gu.load(p.gu, cols, row_base + j_of(0), un.ntok - j_of(0), c_first);
 #pragma unroll 1
   for (int b = 0; b < blocks; ++b) {
     const int c0 = c_of(b), j0 = j_of(b);
@@ -499,7 +512,13 @@ MOE_DEV void dh_epilogue(const BwdParams& p, const Unit& un, int64_t row_base, u
     gu.put(tile);
     __syncwarp();
     if (b + 1 < blocks) gu.load(p.gu, cols, row_base + j_of(b + 1), un.ntok - j_of(b + 1), c_of(b + 1));
-    uint64_t dgate[4];
+    uint64_t dgate[4], gate[4];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int tq = 8 * r + 2 * (lane & 3);
+      gate[r] = f32x2(__shfl_sync(0xffffffffu, my_gate, tq), __shfl_sync(0xffffffffu, my_gate, tq + 1));
+      dgate[r] = 0;  // (0.0f, 0.0f)
+    }
     tmem_wait_ld();
 #pragma unroll
     for (int hf = 0; hf < 2; ++hf) {
@@ -511,21 +530,24 @@ MOE_DEV void dh_epilogue(const BwdParams& p, const Unit& un, int64_t row_base, u
         ldmatrix_x4_trans(at + kTileBytes, pu[2 * rp][0], pu[2 * rp][1], pu[2 * rp + 1][0], pu[2 * rp + 1][1]);
       }
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int tq = 8 * r + 2 * (lane & 3);
-        const uint64_t gate = f32x2(__shfl_sync(0xffffffffu, my_gate, tq), __shfl_sync(0xffffffffu, my_gate, tq + 1));
-        if (hf == 0) dgate[r] = 0;  // (0.0f, 0.0f)
+      for (int e = 0; e < 2; ++e) {
+        // four independent pairs side by side: the chain through the
+        // exponential and the reciprocal is long
+        uint64_t g[4], sg[4];
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
+        for (int r = 0; r < 4; ++r) g[r] = bf16x2_to_f32x2(pg[r][e]);
+        sigmoid_f32x2(g, sg);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
           const int x = 4 * r + 2 * e;
           const uint64_t q = f32x2(__uint_as_float(a[hf][x]), __uint_as_float(a[hf][x + 1]));
-          const uint64_t g = bf16x2_to_f32x2(pg[r][e]), u = bf16x2_to_f32x2(pu[r][e]);
-          const uint64_t s = sigmoid_f32x2(g), act = mul_f32x2(g, s), h = mul_f32x2(act, u), dh = mul_f32x2(gate, q);
+          const uint64_t u = bf16x2_to_f32x2(pu[r][e]);
+          const uint64_t act = mul_f32x2(g[r], sg[r]), h = mul_f32x2(act, u), dh = mul_f32x2(gate[r], q);
           dgate[r] = fma_f32x2(q, h, dgate[r]);
-          const uint64_t rest = fma_f32x2(act, f32x2(-1.0f, -1.0f), g);  // g - act
-          pg[r][e] = f32x2_to_bf16x2(mul_f32x2(mul_f32x2(dh, u), fma_f32x2(s, rest, s)));
+          const uint64_t rest = fma_f32x2(act, f32x2(-1.0f, -1.0f), g[r]);  // g - act
+          pg[r][e] = f32x2_to_bf16x2(mul_f32x2(mul_f32x2(dh, u), fma_f32x2(sg[r], rest, sg[r])));
           pu[r][e] = f32x2_to_bf16x2(mul_f32x2(dh, act));
-          ph[r][e] = f32x2_to_bf16x2(mul_f32x2(gate, h));
+          ph[r][e] = f32x2_to_bf16x2(mul_f32x2(gate[r], h));
         }
       }
       __syncwarp();  // every lane has read this half's chunks
@@ -606,7 +628,9 @@ __global__ void __launch_bounds__(Plan<FP8>::kThreads, 1)
   // rows 256 r .. 256 r + 255 of the unit's 512 output columns, one
   // contiguous 256-row box whose first and second 128 rows are halves 0 and
   // 1; so TMEM lane l of half h in CTA r is output column 256 r + 128 h + l.
-  const int rank_rows = (is_swiglu(MODE) ? 128 : 256) * (int)rank;
+  // One half: rows 128 r .. 128 r + 127 of the unit's 256.
+  constexpr int kABytes = FP8 ? PL::kABytes : a_bytes(MODE);
+  const int rank_rows = (is_swiglu(MODE) || one_half(MODE) ? 128 : 256) * (int)rank;
   // Readers of each unit id in each CTA (producer or MMA issuer, epilogue
   // leader, FP8 converter leader). The pair's cross-CTA signals are
   // asynchronous stores that complete transaction bytes on the other CTA's
@@ -761,7 +785,7 @@ __global__ void __launch_bounds__(Plan<FP8>::kThreads, 1)
         // single box beats several small ones even with rows to spare)
         const int tmap = half_n <= kTokBox ? 0 : (half_n <= 2 * kTokBox ? 1 : 2);
         const int nbox = 1 << tmap;  // in 32-row granules
-        const uint32_t tx = PL::kABytes + nbox * kBoxBytes;
+        const uint32_t tx = kABytes + nbox * kBoxBytes;
         // weight row (backward: first column of the expert's matrix)
         const int rowA = (shared || is_bwd(MODE) ? 0 : un.g * p.a_rows_per_expert) + un.f * p.tile_cols + rank_rows;
         const int rowB = __ldg(p.grp_row0 + un.g) + un.tok0 + (int)rank * half_n;
@@ -789,7 +813,7 @@ __global__ void __launch_bounds__(Plan<FP8>::kThreads, 1)
           (void)MOE_IN_BOUNDS(pos + tx <= (uint32_t)kRingBytes, p.status);
           sh.slot_off[s] = pos;
           uint8_t* a_dst = smem + pos;
-          uint8_t* b_dst = a_dst + PL::kABytes;
+          uint8_t* b_dst = a_dst + kABytes;
           if (FP8) {
             // every CTA's bytes complete on its own stage barrier, which its
             // converter warps wait on; the codes are 64 bytes per row
@@ -801,12 +825,12 @@ __global__ void __launch_bounds__(Plan<FP8>::kThreads, 1)
             const uint32_t full_bar = in_first(&sh.full[s]);
             if (first) mbar_arrive_expect_tx(&sh.full[s], 2 * tx);  // this CTA's bytes and the peer's
             if constexpr (is_bwd(MODE)) {
-              // 256 weight columns x 64 k as four 64 x 64 boxes (8 KB each, k-major rows of 128 bytes)
+              // 256 (128) weight columns x 64 k as four (two) 64 x 64 boxes (8 KB each, rows of 128 bytes per k)
               const bool second = MODE == kDx && kc >= seg;
               const int k0 = (second ? kc - seg : kc) * kBK;
               const CUtensorMap* ta = second ? &p.a1_routed : ta0;
 #pragma unroll
-              for (int c = 0; c < 4; ++c)
+              for (int c = 0; c < kABytes / kMnBox; ++c)
                 tma_load_3d_pair(a_dst + c * kMnBox, ta, full_bar, rowA + 64 * c, k0, un.g, pol);
               tma_load_2d_pair(b_dst, second ? &p.b1[tmap] : tb, full_bar, k0, rowB, pol_last);
               continue;
@@ -834,7 +858,7 @@ __global__ void __launch_bounds__(Plan<FP8>::kThreads, 1)
       // 290, and at N = 256 all of it hides behind the MMAs' 512.
       uint32_t consumed = 0;
       uint32_t uses[2] = {0u, 0u};
-      AccPlan<PL::kAccCols> plan;
+      AccPlan<PL::kAccCols, one_half(MODE)> plan;
       bool ok = true;
       auto wait = [&](uint64_t* bar, uint32_t parity) {
         return (bool)__all_sync(0xffffffffu, mbar_wait_cluster_bounded(bar, parity, abort_flag));
@@ -879,7 +903,7 @@ __global__ void __launch_bounds__(Plan<FP8>::kThreads, 1)
           const uint32_t off =
               __shfl_sync(0xffffffffu, *reinterpret_cast<volatile uint32_t*>(&sh.slot_off[s]), 0);
           const uint32_t stage_addr = smem_u32(smem) + off;
-          const uint64_t bdesc = smem_desc_sw128(stage_addr + PL::kABytes);  // the token box follows the weights
+          const uint64_t bdesc = smem_desc_sw128(stage_addr + kABytes);  // the token box follows the weights
           if (elect_one()) {
             if (FP8) {
               // A: the converted slot in tensor memory, 8 columns per 16 K
@@ -896,7 +920,7 @@ __global__ void __launch_bounds__(Plan<FP8>::kThreads, 1)
 #pragma unroll
               for (int kk = 0; kk < kBK / 16; ++kk) {
                 umma_bf16_pair(d0, adesc + kk * kStep, bdesc + kk * 2, idesc, (kc | kk) != 0);
-                umma_bf16_pair(d1, adesc + kHalf + kk * kStep, bdesc + kk * 2, idesc, (kc | kk) != 0);
+                if (!one_half(MODE)) umma_bf16_pair(d1, adesc + kHalf + kk * kStep, bdesc + kk * 2, idesc, (kc | kk) != 0);
               }
             }
             umma_commit_pair_both(smem_u32(&sh.empty[s]));
@@ -935,7 +959,7 @@ __global__ void __launch_bounds__(Plan<FP8>::kThreads, 1)
         reinterpret_cast<__nv_bfloat16*>(reinterpret_cast<uint8_t*>(tiles) + ew * PL::kTiles * kTileBytes);
     const bool leader = threadIdx.x == 64;
     uint32_t uses[2] = {0u, 0u};
-    AccPlan<PL::kAccCols> plan;
+    AccPlan<PL::kAccCols, one_half(MODE)> plan;
     for (int i = 0;; ++i) {
       // the leader takes the next unit and waits for its accumulator(s); the
       // epilogue warps then agree on the outcome and all run the unit or all leave
@@ -987,10 +1011,10 @@ __global__ void __launch_bounds__(Plan<FP8>::kThreads, 1)
       const int64_t ld = shared ? p.ld_shared : p.ld_routed;
       const int cols = shared ? p.cols_shared : p.cols_routed;
       const uint32_t t_q = tmem_base + ((uint32_t)(q * 32) << 16) + base;
-      constexpr int kHalves = MODE == kDh ? 0 : is_swiglu(MODE) ? 1 : 2;
-      if constexpr (MODE == kDh)
-        dh_epilogue(p, un, row_base, t_q, stride, reinterpret_cast<uint8_t*>(tile), un.f * p.tile_cols + rank_rows + 32 * q,
-                    sub, kEpiWarps / 4);
+      constexpr int kHalves = is_dh(MODE) ? 0 : is_swiglu(MODE) ? 1 : 2;
+      if constexpr (is_dh(MODE))
+        dh_epilogue(p, un, row_base, t_q, stride, one_half(MODE) ? 1 : 2, reinterpret_cast<uint8_t*>(tile),
+                    un.f * p.tile_cols + rank_rows + 32 * q, sub, kEpiWarps / 4);
 #pragma unroll 1
       for (int hh = 0; hh < kHalves; ++hh) {
         // this warp's 32 output columns of the unit
@@ -1028,10 +1052,12 @@ __global__ void __launch_bounds__(Plan<FP8>::kThreads, 1)
                   const float g0 = __uint_as_float(a[x]), g1 = __uint_as_float(a[x + 1]);
                   const float u0 = __uint_as_float(b[x]), u1 = __uint_as_float(b[x + 1]);
                   if (MODE == kSwiGLUKeep) {
-                    const uint64_t g = f32x2(g0, g1), u = f32x2(u0, u1);
+                    const uint64_t g[1] = {f32x2(g0, g1)}, u = f32x2(u0, u1);
+                    uint64_t sg[1];
+                    sigmoid_f32x2(g, sg);
                     pg[hf][r][e] = pack_bf16x2(g0, g1);
                     pu[hf][r][e] = pack_bf16x2(u0, u1);
-                    pk[hf][r][e] = f32x2_to_bf16x2(mul_f32x2(mul_f32x2(g, sigmoid_f32x2(g)), u));
+                    pk[hf][r][e] = f32x2_to_bf16x2(mul_f32x2(mul_f32x2(g[0], sg[0]), u));
                   } else {
                     pk[hf][r][e] = pack_bf16x2(silu_tanh(g0) * u0, silu_tanh(g1) * u1);
                   }
@@ -1445,14 +1471,25 @@ cudaError_t launch_expert_gemms_tc(const Problem& p, const GemmArgs& a, cudaStre
   return fp8 ? launch_one<kGateDown, true>(g2, grid2, s, !between) : launch_one<kGateDown, false>(g2, grid2, s, !between);
 }
 
+// Units of 512 features load 3/4 of the operand bytes per product, units of 256
+// hide their epilogue behind the next unit's products. The epilogue costs the
+// same at any K = d: with K = 7168 the first took 110 us where the second took
+// 130 (4096 rows x 2048 features), with K = 1280 267 against 256 us (57344 x
+// 896). With few units of 512 the smaller ones spread the
+// weights over more SMs.
+int dh_tile(const Problem& p) {
+  const int64_t chunks = p.R / kTcBM + (p.N < p.R ? p.N : p.R);  // about one partly filled unit row per group
+  return p.d > 2048 && chunks * ((p.F + kTcBN2 - 1) / kTcBN2) >= device_sm_count() / 4 ? kTcBN2 : kTcBNh;
+}
+
 int dgate_planes(const Problem& p) { return p.dtype == MOE_BF16 ? (p.F + 31) / 32 : (p.F + kSimtBN - 1) / kSimtBN; }
 
 cudaError_t launch_experts_backward_tc(const Problem& p, const ExpertsBwdArgs& a, cudaStream_t s) {
   const int sms = device_sm_count();
   constexpr int cm = Plan<false>::kChunk;
   const int64_t chunks_bound = (p.R + cm - 1) / cm + p.N;
-  auto grid_of = [&](int cols) {
-    const int64_t units = chunks_bound * ((cols + kTcBN2 - 1) / kTcBN2);
+  auto grid_of = [&](int cols, int tile) {
+    const int64_t units = chunks_bound * ((cols + tile - 1) / tile);
     return (int)(units < sms ? units : sms);
   };
 
@@ -1468,7 +1505,7 @@ cudaError_t launch_experts_backward_tc(const Problem& p, const ExpertsBwdArgs& a
   h.N = p.N;
   h.k_routed = p.d;
   h.cols_routed = p.F;
-  h.tile_cols = kTcBN2;
+  h.tile_cols = dh_tile(p);
   h.out_routed = (__nv_bfloat16*)a.gh;
   h.ld_routed = p.F;
   h.out_g = (__nv_bfloat16*)a.dg;
@@ -1481,9 +1518,8 @@ cudaError_t launch_experts_backward_tc(const Problem& p, const ExpertsBwdArgs& a
   h.a_rows_routed = p.F;
   h.gu = (const __nv_bfloat16*)a.gu;
   h.part = a.dgate_rows ? a.dgate_part : nullptr;
-  cudaError_t err = launch_one<kDh, false>(h, grid_of(p.F), s, true);
-  if (err == cudaSuccess && a.dgate_rows)
-    err = launch_dgate_reduce(a.dgate_part, dgate_planes(p), p.R, a.dgate_rows, s);
+  cudaError_t err = dh_tile(p) == kTcBN2 ? launch_one<kDhWide, false>(h, grid_of(p.F, kTcBN2), s, true)
+                                         : launch_one<kDh, false>(h, grid_of(p.F, kTcBNh), s, true);
   if (err != cudaSuccess) return err;
 
   if (a.dx_rows) {
@@ -1506,10 +1542,14 @@ cudaError_t launch_experts_backward_tc(const Problem& p, const ExpertsBwdArgs& a
     x.chunk_rows = cm;
     x.tok_rows_routed = x.out_rows_routed = p.R;
     x.a_rows_routed = p.d;
-    err = launch_one<kDx, false>(x, grid_of(p.d), s, true);
+    err = launch_one<kDx, false>(x, grid_of(p.d, kTcBN2), s, true);
     if (err != cudaSuccess) return err;
   }
-  if (!a.dW1) return cudaSuccess;
+  // (last: between the GEMMs its launch and its wait would stand in their way)
+  auto reduce_dgate = [&] {
+    return a.dgate_rows ? launch_dgate_reduce(a.dgate_part, dgate_planes(p), p.R, a.dgate_rows, s) : cudaSuccess;
+  };
+  if (!a.dW1) return reduce_dgate();
   WgradArgs w{};
   w.mat[0] = {a.dg, a.x_rows, a.dW1, p.F, p.d, p.F};
   w.mat[1] = {a.du, a.x_rows, a.dW3, p.F, p.d, p.F};
@@ -1523,7 +1563,8 @@ cudaError_t launch_experts_backward_tc(const Problem& p, const ExpertsBwdArgs& a
   w.accumulate = a.accumulate;
   w.status = a.status;
   w.independent = a.dx_rows != nullptr;  // of the dx GEMM, which has waited for the dh GEMM
-  return launch_wgrad_tc(w, s);
+  err = launch_wgrad_tc(w, s);
+  return err == cudaSuccess ? reduce_dgate() : err;
 }
 
 }  // namespace moe

@@ -23,6 +23,7 @@ constexpr int kTcBM = 256;
 constexpr int kTcBM8 = 160;
 constexpr int kTcBN1 = 256;
 constexpr int kTcBN2 = 512;
+constexpr int kTcBNh = 256;  // backward, first GEMM: weight columns of its smaller units
 constexpr int kSimtBM = 64;
 constexpr int kSimtBN = 64;
 constexpr int kChunkTokens = 32;  // dispatch: tokens per warp chunk
@@ -230,6 +231,7 @@ struct WgradArgs {
 };
 cudaError_t launch_wgrad_tc(const WgradArgs& a, cudaStream_t s);
 int dgate_planes(const Problem& p);
+int dh_tile(const Problem& p);  // weight columns of a unit of the first GEMM: kTcBNh or kTcBN2
 cudaError_t launch_experts_backward_tc(const Problem& p, const ExpertsBwdArgs& a, cudaStream_t s);
 cudaError_t launch_experts_backward_simt(const Problem& p, const ExpertsBwdArgs& a, cudaStream_t s);
 // dgate[r] = sum over the planes of part[plane][r], in a fixed order.

@@ -145,7 +145,7 @@ moe_status moe_experts_backward(const moe_cfg* cfg, int64_t rows, const int32_t*
   db.unit_base1 = at<int32_t>(ws, L.unit_base1);
   db.unit_base2 = at<int32_t>(ws, L.unit_base2);
   const bool tc = p.dtype == MOE_BF16;
-  e = launch_group_tables(p, counts, db, tc ? kTcBM : kSimtBM, tc ? kTcBN2 : kSimtBN, tc ? kTcBN2 : kSimtBN,
+  e = launch_group_tables(p, counts, db, tc ? kTcBM : kSimtBM, tc ? dh_tile(p) : kSimtBN, tc ? kTcBN2 : kSimtBN,
                           at<int>(ws, L.sched), s);
   if (e != cudaSuccess) return cuda_fail(e);
   ExpertsBwdArgs a{};

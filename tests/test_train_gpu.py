@@ -185,8 +185,10 @@ SHAPES = [
     ([40, 0, 129, 300, 7], 1280, 896),
     # one dense block
     ([517], 512, 1024),
+    # a long reduction over d, with enough rows and features for its larger units
+    ([30] * 17 + [0, 300, 257, 1], 2056, 1032),
 ]
-IDS = ["-".join(map(str, c)) + f"_{d}x{F}" for c, d, F in SHAPES]
+IDS = [("-".join(map(str, c)) if len(c) < 9 else f"{len(c)}groups") + f"_{d}x{F}" for c, d, F in SHAPES]
 
 
 @pytest.mark.parametrize("counts,d,F", SHAPES, ids=IDS)
@@ -817,7 +819,7 @@ def test_combine_and_dispatch_backward_are_each_others_transpose():
         assert torch.equal(more, out + (0 if sh is None else sh) + (0 if ro is None else ro))
 
 
-@pytest.mark.parametrize("counts,d,F", SHAPES[:5], ids=IDS[:5])
+@pytest.mark.parametrize("counts,d,F", SHAPES[:5] + SHAPES[-1:], ids=IDS[:5] + IDS[-1:])
 def test_debug_build_finds_no_index_out_of_bounds(counts, d, F):
     b = Block(counts, d, F, seed=11)
     y, gu = b.forward()
