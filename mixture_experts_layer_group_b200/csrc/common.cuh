@@ -210,6 +210,15 @@ MOE_DEV void tma_load_3d_pair(void* smem_dst, const void* tmap, uint32_t bar_clu
       : "memory");
 }
 
+// `bytes` contiguous bytes of this GPU's memory into shared memory, completing
+// transaction bytes on `bar`; both addresses and the size are multiples of 16.
+MOE_DEV void bulk_load(void* smem_dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                   smem_u32(smem_dst)),
+               "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(smem_u32(bar))
+               : "memory");
+}
+
 // 2-D tiled store of a shared-memory box to global memory (bulk group). The
 // box start (c0, c1) must be non-negative and c0 a multiple of 16 bytes'
 // worth of elements; rows/columns beyond the tensor are clipped.

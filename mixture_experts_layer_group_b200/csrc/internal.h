@@ -317,17 +317,19 @@ int device_sm_count();
 // Launches a kernel with programmatic stream serialization: it may start while
 // its predecessor in the stream ends, and orders itself with griddep_wait().
 template <class... Params, class... Args>
-cudaError_t launch_after(void (*kernel)(Params...), unsigned blocks, unsigned threads, cudaStream_t s, Args&&... args) {
+cudaError_t launch_after(void (*kernel)(Params...), unsigned blocks, unsigned threads, size_t smem, cudaStream_t s,
+                         const Args&... args) {
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.gridDim = dim3(blocks, 1, 1);
   cfg.blockDim = dim3(threads, 1, 1);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, static_cast<Params>(args)...);
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
 // Keeps e as this host thread's moe_last_cuda_error() value.

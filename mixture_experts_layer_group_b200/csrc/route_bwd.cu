@@ -189,7 +189,7 @@ cudaError_t launch_route_dz(const RouteDzArgs& a, cudaStream_t s) {
 cudaError_t launch_join_planes(const float* planes, int n, int64_t elems, void* dW, int grad_dtype, bool accumulate,
                                cudaStream_t s) {
   const int64_t vecs = elems / 4;
-  return launch_after(join_planes_kernel, (unsigned)((vecs + 255) / 256), 256, s,
+  return launch_after(join_planes_kernel, (unsigned)((vecs + 255) / 256), 256, 0, s,
                       reinterpret_cast<const float4*>(planes), n, vecs, dW, grad_dtype == MOE_F32, accumulate);
 }
 

@@ -303,7 +303,7 @@ __global__ void __launch_bounds__(256) dgate_reduce_kernel(const float* __restri
 }  // namespace
 
 cudaError_t launch_dgate_reduce(const float* part, int planes, int64_t rows, float* dgate, cudaStream_t s) {
-  return launch_after(dgate_reduce_kernel, (unsigned)((rows + 31) / 32), 256, s, part, planes, rows, dgate);
+  return launch_after(dgate_reduce_kernel, (unsigned)((rows + 31) / 32), 256, 0, s, part, planes, rows, dgate);
 }
 
 cudaError_t launch_experts_backward_simt(const Problem& p, const ExpertsBwdArgs& a, cudaStream_t s) {

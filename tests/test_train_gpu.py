@@ -562,8 +562,8 @@ def exact_norm(srcs):
 
 def check_clip(srcs, dsts, before, norm, max_norm):
     want = exact_norm(before)
-    # squares of a 16-byte vector are summed in fp32: up to 8 * 2^-24 relative, halved by the root
-    assert abs(norm - want) <= 2.0 ** -21 * want
+    # up to 32 squares are summed in fp32: up to 32 * 2^-24 = 2^-19 relative, halved by the root
+    assert abs(norm - want) <= 2.0 ** -20 * want
     c = min(1.0, max_norm / want) if want > 0 and math.isfinite(want) else 1.0
     for s, d, b in zip(srcs, dsts, before):
         eps = 2.0 ** -8 if b.dtype == torch.bfloat16 else 2.0 ** -23
@@ -617,7 +617,7 @@ def test_clip_mixes_types_and_is_deterministic():
     a = clip(srcs, 1e9)
     b = clip(srcs, 1e9, stream=torch.cuda.Stream())
     assert a == b
-    assert abs(a[1] - exact_norm(srcs)) <= 2.0 ** -21 * a[1]
+    assert abs(a[1] - exact_norm(srcs)) <= 2.0 ** -20 * a[1]
 
 
 @pytest.mark.parametrize("scale", [1e-30, 1e-22, 1e18, 1e25])
@@ -657,7 +657,7 @@ def test_clip_of_more_than_2_31_elements():
     t = torch.full((n,), 2.0 ** -10, dtype=torch.bfloat16, device="cuda")
     want = 2.0 ** -10 * math.sqrt(n)
     _, norm = clip([t], want / 4)
-    assert abs(norm - want) <= 2.0 ** -21 * want
+    assert abs(norm - want) <= 2.0 ** -20 * want
     lo, hi = torch.aminmax(t)
     assert float(lo) == float(hi) == 2.0 ** -12
 
@@ -754,7 +754,7 @@ def test_training_step(T, d, F, N, ns, k, score, normalize, dtype):
     want = exact_norm(layer.grads.values())
     before = {n: t.clone() for n, t in layer.grads.items()}
     norm = layer.clip(0.25 * want)
-    assert abs(float(norm) - want) <= 2.0 ** -21 * want
+    assert abs(float(norm) - want) <= 2.0 ** -20 * want
     for n, t in layer.grads.items():
         assert bool(((t - 0.25 * before[n]).abs() <= 2.0 ** -19 * before[n].abs()).all()), n
     if w["b"] is not None:
