@@ -188,6 +188,16 @@ MOE_DEV void tma_load_2d_hint(void* smem_dst, const void* tmap, uint64_t* bar, i
       : "memory");
 }
 
+// The same for a 3-D tensor map (c0 innermost).
+MOE_DEV void tma_load_3d_hint(void* smem_dst, const void* tmap, uint64_t* bar, int32_t c0, int32_t c1, int32_t c2,
+                              uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
+      " [%0], [%1, {%3, %4, %5}], [%2], %6;" ::"r"(smem_u32(smem_dst)),
+      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2), "l"(policy)
+      : "memory");
+}
+
 // 2-D tiled load issued by either CTA of a CTA pair: data lands in this CTA's
 // shared memory and the transaction bytes complete on `bar_cluster`, an
 // mbarrier of the pair's first CTA (cluster address). No multicast.
