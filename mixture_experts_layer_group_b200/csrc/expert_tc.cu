@@ -68,6 +68,7 @@
 // MOE_DEV_WAIT_TIMEOUT, drains its own copies and MMAs (bounded again),
 // frees its tensor memory and exits.
 
+#include <initializer_list>
 #include <mutex>
 
 #include "common.cuh"
@@ -238,6 +239,7 @@ struct BwdParams : TcParams {
   int64_t ld_g;
   const __nv_bfloat16* gu;   // [R, 2 F] (kDh)
   float* part;               // [ceil(F / 32), R] partial gate gradients, or null (kDh)
+  int beside;                // the next kernel runs beside this one (kDx)
 };
 template <int MODE>
 struct ParamsOf {
@@ -681,6 +683,8 @@ __global__ void __launch_bounds__(Plan<FP8>::kThreads, 1)
   // is read only after it has finished; the down GEMM's tables are older than
   // its predecessor and its producer alone waits)
   if (MODE != kGateDown) griddep_wait();
+  if constexpr (MODE == kDx)
+    if (p.beside && threadIdx.x == 0) griddep_launch_dependents();
   const int total_units = __ldg(p.unit_base + p.N + 1);
   const uint32_t tmem_base = sh.tmem_base;
   volatile int* abort_flag = &sh.abort_flag;
@@ -690,7 +694,8 @@ __global__ void __launch_bounds__(Plan<FP8>::kThreads, 1)
   uint32_t fills = 0;  // producer: stage fills issued
   if (warp == 0) {
     // ------------------------------------------------- scheduler + producer --
-    if (lane == 0) {
+    // (the whole warp runs the loop, one elected lane issues: see elect_one())
+    {
       // the down GEMM may start while the SwiGLU GEMM drains (programmatic
       // launch): nothing it loads may be read before that grid has finished
       if (MODE == kGateDown) griddep_wait();
@@ -704,7 +709,6 @@ __global__ void __launch_bounds__(Plan<FP8>::kThreads, 1)
       // order by the pair MMAs' commits, so the bytes in use form one circular
       // interval [offset of the oldest unfreed fill, head). A stage that does
       // not fit before the end restarts at 0.
-      uint32_t off_of[kSlots];
       uint32_t head = 0, oldest = 0;
       auto acquire = [&](uint32_t j, uint32_t sz, uint32_t& pos) -> bool {
         for (;;) {
@@ -714,7 +718,8 @@ __global__ void __launch_bounds__(Plan<FP8>::kThreads, 1)
             pos = head + sz <= (uint32_t)kRingBytes ? head : 0u;
             fits = true;
           } else if (inflight < (uint32_t)kSlots) {
-            const uint32_t tail = off_of[oldest % kSlots];
+            const uint32_t tail =
+                __shfl_sync(0xffffffffu, *reinterpret_cast<volatile uint32_t*>(&sh.slot_off[oldest % kSlots]), 0);
             if (tail < head) {  // in use: [tail, head)
               if (head + sz <= (uint32_t)kRingBytes) {
                 pos = head;
@@ -730,7 +735,8 @@ __global__ void __launch_bounds__(Plan<FP8>::kThreads, 1)
           }
           if (fits) return true;
           // wait for the oldest fill to be consumed
-          if (!mbar_wait_cluster_bounded(&sh.empty[oldest % kSlots], (oldest / kSlots) & 1u, abort_flag))
+          if (!__all_sync(0xffffffffu, mbar_wait_cluster_bounded(&sh.empty[oldest % kSlots], (oldest / kSlots) & 1u,
+                                                                 abort_flag)))
             return false;
           ++oldest;
         }
@@ -738,36 +744,38 @@ __global__ void __launch_bounds__(Plan<FP8>::kThreads, 1)
       bool ok = true;
       for (int i = 0;; ++i) {
         const int q = i % kRing;
-        int u;
+        int u = 0;
         if (first) {
-          if (!mbar_wait_cluster_bounded(&sh.ring_empty[q], ((i / kRing) & 1) ^ 1, abort_flag)) {
-            ok = false;
-            break;
+          ok = __all_sync(0xffffffffu, mbar_wait_cluster_bounded(&sh.ring_empty[q], ((i / kRing) & 1) ^ 1, abort_flag));
+          if (!ok) break;
+          if (lane == 0) {
+            u = atomicAdd(p.sched, 1);
+            if (u >= total_units) u = -1;
+            // the id itself is the 4 transaction bytes of the peer's ring_full
+            st_async_u32(peer(&sh.ring[q]), (uint32_t)u, peer(&sh.ring_full[q]));
+            sh.ring[q] = u;
           }
-          u = atomicAdd(p.sched, 1);
-          if (u >= total_units) u = -1;
-          // the id itself is the 4 transaction bytes of the peer's ring_full
-          st_async_u32(peer(&sh.ring[q]), (uint32_t)u, peer(&sh.ring_full[q]));
-          sh.ring[q] = u;
         } else {
           // this CTA's ring_full phase: one arrival (here) and the 4 bytes of CTA 0's store
-          mbar_arrive_expect_tx(&sh.ring_full[q], 4);
-          if (!mbar_wait_cluster_bounded(&sh.ring_full[q], (i / kRing) & 1, abort_flag)) {
-            ok = false;
-            break;
-          }
+          if (lane == 0) mbar_arrive_expect_tx(&sh.ring_full[q], 4);
+          ok = __all_sync(0xffffffffu, mbar_wait_cluster_bounded(&sh.ring_full[q], (i / kRing) & 1, abort_flag));
+          if (!ok) break;
           u = load_volatile(&sh.ring[q]);
-          st_async_u32(in_first(&sh.sink), 0u, in_first(&sh.ring_empty[q]));
+          __syncwarp();
+          if (lane == 0) st_async_u32(in_first(&sh.sink), 0u, in_first(&sh.ring_empty[q]));
         }
+        u = __shfl_sync(0xffffffffu, u, 0);
         Unit un{};
-        int K = 0;
+        int K = 0, row0 = 0;
         if (u >= 0) {
           un = decode_unit(p, u);
+          for (int* v : {&un.g, &un.f, &un.tok0, &un.ntok, &un.nchunks}) *v = __shfl_sync(0xffffffffu, *v, 0);
           K = un.g == p.N ? p.k_shared : p.k_routed;
+          row0 = __shfl_sync(0xffffffffu, __ldg(p.grp_row0 + un.g), 0);
         }
         const int seg = (K + kBK - 1) / kBK;  // K blocks of a segment
         const int nk = k_blocks<MODE>(seg);
-        if (first) {
+        if (first && lane == 0) {
           sh.ring_nk[q] = nk;
           sh.ring_ntok[q] = un.ntok;
           mbar_arrive(&sh.ring_full[q]);
@@ -775,7 +783,7 @@ __global__ void __launch_bounds__(Plan<FP8>::kThreads, 1)
         if (u < 0) {
           // no units left for this CTA: the down GEMM may start on SMs as
           // they free up
-          if (MODE != kGateDown) griddep_launch_dependents();
+          if (MODE != kGateDown && lane == 0) griddep_launch_dependents();
           break;
         }
         const bool shared = un.g == p.N;
@@ -788,12 +796,12 @@ __global__ void __launch_bounds__(Plan<FP8>::kThreads, 1)
         const uint32_t tx = kABytes + nbox * kBoxBytes;
         // weight row (backward: first column of the expert's matrix)
         const int rowA = (shared || is_bwd(MODE) ? 0 : un.g * p.a_rows_per_expert) + un.f * p.tile_cols + rank_rows;
-        const int rowB = __ldg(p.grp_row0 + un.g) + un.tok0 + (int)rank * half_n;
+        const int rowB = row0 + un.tok0 + (int)rank * half_n;
         // the unit's rows lie inside the group and its tensors (TMA clips a
         // box that reaches past them, and the last column tile of a matrix
         // whose height is not a multiple of the tile may start past it)
         (void)MOE_IN_BOUNDS(un.ntok >= 1 && un.ntok <= p.chunk_rows && un.tok0 >= 0 &&
-                                __ldg(p.grp_row0 + un.g) + un.tok0 + un.ntok <=
+                                row0 + un.tok0 + un.ntok <=
                                     (shared ? p.tok_rows_shared : p.tok_rows_routed) &&
                                 rowA >= 0 && rowA < (shared ? p.a_rows_shared : p.a_rows_routed) + p.tile_cols,
                             p.status);
@@ -808,22 +816,24 @@ __global__ void __launch_bounds__(Plan<FP8>::kThreads, 1)
             ok = false;
             break;
           }
-          off_of[s] = pos;
           head = pos + tx;
           (void)MOE_IN_BOUNDS(pos + tx <= (uint32_t)kRingBytes, p.status);
-          sh.slot_off[s] = pos;
-          uint8_t* a_dst = smem + pos;
-          uint8_t* b_dst = a_dst + kABytes;
-          if (FP8) {
-            // every CTA's bytes complete on its own stage barrier, which its
-            // converter warps wait on; the codes are 64 bytes per row
-            mbar_arrive_expect_tx(&sh.full[s], tx);
-            tma_load_2d_hint(a_dst, ta0, &sh.full[s], kc * kBK, rowA, pol);
-            if (MODE == kSwiGLU) tma_load_2d_hint(a_dst + kA8Bytes / 2, ta1, &sh.full[s], kc * kBK, rowA, pol);
-            tma_load_2d_hint(b_dst, tb, &sh.full[s], kc * kBK, rowB, pol_last);
-          } else {
+          if (lane == 0) sh.slot_off[s] = pos;
+          __syncwarp();
+          if (elect_one()) {
+            uint8_t* a_dst = smem + pos;
+            uint8_t* b_dst = a_dst + kABytes;
             const uint32_t full_bar = in_first(&sh.full[s]);
-            if (first) mbar_arrive_expect_tx(&sh.full[s], 2 * tx);  // this CTA's bytes and the peer's
+            if (FP8) {
+              // every CTA's bytes complete on its own stage barrier, which its
+              // converter warps wait on; the codes are 64 bytes per row
+              mbar_arrive_expect_tx(&sh.full[s], tx);
+              tma_load_2d_hint(a_dst, ta0, &sh.full[s], kc * kBK, rowA, pol);
+              if (MODE == kSwiGLU) tma_load_2d_hint(a_dst + kA8Bytes / 2, ta1, &sh.full[s], kc * kBK, rowA, pol);
+              tma_load_2d_hint(b_dst, tb, &sh.full[s], kc * kBK, rowB, pol_last);
+            } else if (first) {
+              mbar_arrive_expect_tx(&sh.full[s], 2 * tx);  // this CTA's bytes and the peer's
+            }
             if constexpr (is_bwd(MODE)) {
               // 256 (128) weight columns x 64 k as four (two) 64 x 64 boxes (8 KB each, rows of 128 bytes per k)
               const bool second = MODE == kDx && kc >= seg;
@@ -833,16 +843,17 @@ __global__ void __launch_bounds__(Plan<FP8>::kThreads, 1)
               for (int c = 0; c < kABytes / kMnBox; ++c)
                 tma_load_3d_pair(a_dst + c * kMnBox, ta, full_bar, rowA + 64 * c, k0, un.g, pol);
               tma_load_2d_pair(b_dst, second ? &p.b1[tmap] : tb, full_bar, k0, rowB, pol_last);
-              continue;
+            } else if (!FP8) {
+              tma_load_2d_pair(a_dst, ta0, full_bar, kc * kBK, rowA, pol);  // SwiGLU: 128 W1 rows; down: 256 rows
+              if (is_swiglu(MODE)) tma_load_2d_pair(a_dst + kHalfBytes, ta1, full_bar, kc * kBK, rowA, pol);
+              tma_load_2d_pair(b_dst, tb, full_bar, kc * kBK, rowB, pol_last);
             }
-            tma_load_2d_pair(a_dst, ta0, full_bar, kc * kBK, rowA, pol);  // SwiGLU: 128 W1 rows; down: 256 rows
-            if (is_swiglu(MODE)) tma_load_2d_pair(a_dst + kHalfBytes, ta1, full_bar, kc * kBK, rowA, pol);
-            tma_load_2d_pair(b_dst, tb, full_bar, kc * kBK, rowB, pol_last);
           }
+          __syncwarp();
         }
         if (!ok) break;
       }
-      if (!ok) {
+      if (!ok && lane == 0) {
         *abort_flag = 1;
         set_status(p.status, MOE_DEV_WAIT_TIMEOUT);
       }
@@ -1522,6 +1533,15 @@ cudaError_t launch_experts_backward_tc(const Problem& p, const ExpertsBwdArgs& a
                                          : launch_one<kDh, false>(h, grid_of(p.F, kTcBNh), s, true);
   if (err != cudaSuccess) return err;
 
+  // With few rows per group the dx GEMM is bound by reading the weights and the
+  // weight gradients by writing them (a B200 writes 3.9 TB/s), and both need only
+  // the dh GEMM: they then run beside each other, each on a part of the GPU. 32
+  // experts of 2048 x 7168: 1073 instead of 1135 us with 128 rows each; with 256
+  // there is nothing left to win (1497 against 1479). 16 experts of 896 x 1280
+  // with 37 rows in all: 78 instead of 89 us.
+  const int pairs = sms / 2;
+  const bool beside = a.dx_rows && a.dW1 && p.R <= (int64_t)p.N * 192;
+  const int dx_pairs = pairs * 3 / 7;
   if (a.dx_rows) {
     BwdParams x{};
     ok = make_weight_tmap(&x.a0_routed, a.W1, p.N, p.F, p.d) && make_weight_tmap(&x.a1_routed, a.W3, p.N, p.F, p.d) &&
@@ -1542,7 +1562,9 @@ cudaError_t launch_experts_backward_tc(const Problem& p, const ExpertsBwdArgs& a
     x.chunk_rows = cm;
     x.tok_rows_routed = x.out_rows_routed = p.R;
     x.a_rows_routed = p.d;
-    err = launch_one<kDx, false>(x, grid_of(p.d, kTcBN2), s, true);
+    x.beside = beside;
+    const int grid = grid_of(p.d, kTcBN2);
+    err = launch_one<kDx, false>(x, beside && grid > dx_pairs ? dx_pairs : grid, s, true);
     if (err != cudaSuccess) return err;
   }
   // (last: between the GEMMs its launch and its wait would stand in their way)
@@ -1563,6 +1585,7 @@ cudaError_t launch_experts_backward_tc(const Problem& p, const ExpertsBwdArgs& a
   w.accumulate = a.accumulate;
   w.status = a.status;
   w.independent = a.dx_rows != nullptr;  // of the dx GEMM, which has waited for the dh GEMM
+  w.max_pairs = beside ? pairs - dx_pairs : 0;
   err = launch_wgrad_tc(w, s);
   return err == cudaSuccess ? reduce_dgate() : err;
 }

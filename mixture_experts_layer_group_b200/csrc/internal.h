@@ -228,6 +228,7 @@ struct WgradArgs {
   // dependents start), and the two write different buffers: this one then need
   // not wait for it to end before its own work.
   bool independent;
+  int max_pairs;     // CTA pairs to use at most (0: all)
 };
 cudaError_t launch_wgrad_tc(const WgradArgs& a, cudaStream_t s);
 int dgate_planes(const Problem& p);

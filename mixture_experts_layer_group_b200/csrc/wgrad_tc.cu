@@ -587,10 +587,10 @@ bool make_rows_map(CUtensorMap* m, int* whole, const void* base, int64_t rows, i
 }
 
 // The units of one matrix: runs of tiles along one dimension.
-void choose_runs(Matrix& x, int64_t M, int N, int groups, bool keep) {
+void choose_runs(Matrix& x, int64_t M, int N, int groups, bool keep, int64_t pairs) {
   x.M = (int)M;
   x.N = N;
-  const int64_t tm = (M + kTile - 1) / kTile, tn = (N + kTile - 1) / kTile, pairs = device_sm_count() / 2;
+  const int64_t tm = (M + kTile - 1) / kTile, tn = (N + kTile - 1) / kTile;
   auto units = [&](bool along_m, int run) {
     return (along_m ? (tm + run - 1) / run * tn : tm * ((tn + run - 1) / run)) * groups;
   };
@@ -627,7 +627,7 @@ cudaError_t launch_wgrad_tc(const WgradArgs& a, cudaStream_t s) {
   for (int i = 0; i < a.nmat; ++i) {
     const WgradMatrix& w = a.mat[i];
     Matrix& x = p.mat[i];
-    choose_runs(x, w.M, w.N, a.groups, keep);
+    choose_runs(x, w.M, w.N, a.groups, keep, a.max_pairs > 0 ? a.max_pairs : device_sm_count() / 2);
     p.units_per_group += x.mt * x.nt;
     const uint64_t dims[3] = {(uint64_t)w.N, (uint64_t)w.M, (uint64_t)a.groups};
     const uint64_t stride[2] = {(uint64_t)w.N * elem, (uint64_t)w.N * w.M * elem};
@@ -683,6 +683,7 @@ cudaError_t launch_wgrad_tc(const WgradArgs& a, cudaStream_t s) {
     }
     clusters = known;
   }
+  if (a.max_pairs > 0 && a.max_pairs < clusters) clusters = a.max_pairs;
   if (p.units < clusters) clusters = p.units;
   cfg.gridDim = dim3(2 * clusters, 1, 1);
   cfg.numAttrs = 2;
