@@ -1493,7 +1493,10 @@ int dh_tile(const Problem& p) {
   return p.d > 2048 && chunks * ((p.F + kTcBN2 - 1) / kTcBN2) >= device_sm_count() / 4 ? kTcBN2 : kTcBNh;
 }
 
-int dgate_planes(const Problem& p) { return p.dtype == MOE_BF16 ? (p.F + 31) / 32 : (p.F + kSimtBN - 1) / kSimtBN; }
+int dgate_planes(const Problem& p) {
+  const int cols = p.dtype == MOE_BF16 ? 32 : simt_bwd_tile(p);
+  return (p.F + cols - 1) / cols;
+}
 
 cudaError_t launch_experts_backward_tc(const Problem& p, const ExpertsBwdArgs& a, cudaStream_t s) {
   const int sms = device_sm_count();

@@ -232,6 +232,7 @@ struct WgradArgs {
 };
 cudaError_t launch_wgrad_tc(const WgradArgs& a, cudaStream_t s);
 int dgate_planes(const Problem& p);
+int simt_bwd_tile(const Problem& p);  // fp32: rows and columns of a tile of the row products
 int dh_tile(const Problem& p);  // weight columns of a unit of the first GEMM: kTcBNh or kTcBN2
 cudaError_t launch_experts_backward_tc(const Problem& p, const ExpertsBwdArgs& a, cudaStream_t s);
 cudaError_t launch_experts_backward_simt(const Problem& p, const ExpertsBwdArgs& a, cudaStream_t s);

@@ -31,7 +31,8 @@ BwdLayout make_bwd_layout(const Problem& p) {
   L.dg = take(rf);
   L.du = take(rf);
   L.gh = take(rf);
-  L.part = take((size_t)dgate_planes(p) * p.R * 4);
+  // (narrowest tiles: a workspace for R rows also holds a call of fewer)
+  L.part = take((size_t)((p.F + 31) / 32) * p.R * 4);
   L.total = off;
   return L;
 }
@@ -145,7 +146,8 @@ moe_status moe_experts_backward(const moe_cfg* cfg, int64_t rows, const int32_t*
   db.unit_base1 = at<int32_t>(ws, L.unit_base1);
   db.unit_base2 = at<int32_t>(ws, L.unit_base2);
   const bool tc = p.dtype == MOE_BF16;
-  e = launch_group_tables(p, counts, db, tc ? kTcBM : kSimtBM, tc ? dh_tile(p) : kSimtBN, tc ? kTcBN2 : kSimtBN,
+  const int bs = tc ? 0 : simt_bwd_tile(p);
+  e = launch_group_tables(p, counts, db, tc ? kTcBM : bs, tc ? dh_tile(p) : bs, tc ? kTcBN2 : bs,
                           at<int>(ws, L.sched), s);
   if (e != cudaSuccess) return cuda_fail(e);
   ExpertsBwdArgs a{};
@@ -237,7 +239,11 @@ moe_status moe_route_backward(const moe_cfg* cfg, int64_t T, const void* x, cons
   if (e == cudaSuccess) e = cudaMemsetAsync(status, 0, 4, s);
   if (e != cudaSuccess) return cuda_fail(e);
   const bool tc = p.dtype == MOE_BF16;
-  const int64_t units = (T + kSimtBM - 1) / kSimtBM * ((p.d + kSimtBN - 1) / kSimtBN);  // fp32 row tiles
+  Problem one = p;  // the products' one group of T rows
+  one.F = p.d;
+  one.R = T;
+  const int bs = simt_bwd_tile(one);
+  const int64_t units = (T + bs - 1) / bs * ((p.d + bs - 1) / bs);  // fp32 row tiles
   if (units > (1ll << 31) - 1) return MOE_ERR_UNSUPPORTED;
   RouteDzArgs z{};
   z.logits = logits;

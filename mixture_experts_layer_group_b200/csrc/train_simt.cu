@@ -1,107 +1,34 @@
-// Backward products of fp32 layers on CUDA cores (tensor cores would round
-// the operands far beyond the fp32 tolerance): the grouped experts' three
-// stages and the router's two products, as 64 x 64 tiles of
-// C[m, n] = sum_k A(m, k) B(n, k) with fp32 accumulators.
+// Backward products of fp32 layers on CUDA cores: the grouped experts' three
+// stages and the router's two products, with fp32 accumulators.
 //
 //   dh     q = dy W2 per row, then per element (s = sigmoid(g), h = g s u)
 //            dgate += q h, du = gate q g s, dg = gate q u s (1 + g (1 - s)),
 //            gh = gate h
 //   dx     dx = dg W1 + du W3
 //   dW     dW1 = dg^T x, dW3 = du^T x, dW2 = dy^T gh over a group's rows
+//
+// Bound by the FP32 pipes where the rows are many: 8 groups of 512 rows, d 1024,
+// d_ff 1024 take 1390 us (51.5 GFLOP, 37 TFLOP/s) in tiles of 128 x 128 (8 x 8
+// outputs per thread, four 16-byte shared loads for 64 multiply-adds). Few rows
+// leave SMs idle and make long chains of dependent blocks, so small products
+// take 32 x 32 tiles whose sum is split over four groups of threads: 16 groups of
+// 32 rows, d 256, d_ff 512 take 85 us (0.8 GFLOP; 111 us in tiles of 64 x 64).
 #include <cmath>
+#include <type_traits>
 
-#include "common.cuh"
 #include "internal.h"
+#include "simt_gemm.cuh"
 
 namespace moe {
 namespace {
 
-constexpr int kBM = kSimtBM, kBN = kSimtBN, kBK = 32;
-constexpr int kThreads = 256;  // 16 x 16 threads, 4 x 4 outputs each
-constexpr int kVecs = kBM * kBK / 4 / kThreads;  // 16-byte loads per thread, operand and K step
-static_assert(kBM == kBN && kVecs * kThreads * 4 == kBM * kBK, "both operands load alike");
-
-// A strided operand: element (r, k) at p[r * rs + k * ks] for r < rows and
-// k < ks_len, zero elsewhere. One of the strides is 1, the other and the
-// bound along the unit stride are multiples of 4, so four consecutive
-// elements load as one aligned vector.
-struct Operand {
-  const float* p;
-  int64_t rs, ks, rows, len;
-};
-
-// Two buffers of a 32 x 64 block of each operand, [k][r]. The 16-byte column
-// groups of row k are permuted by k / 4, so that the four rows a k-contiguous
-// vector is spread over, and the reads along a row, hit all banks.
-struct Tile {
-  float a[2][kBK][kBM];
-  float b[2][kBK][kBN];
-};
-MOE_DEV int swz(int k, int r) { return r ^ (((k >> 2) & 7) << 2); }
-
-MOE_DEV void fetch(const Operand& o, int64_t r0, int64_t k0, float4 (&v)[kVecs]) {
-#pragma unroll
-  for (int i = 0; i < kVecs; ++i) {
-    const int t = threadIdx.x + i * kThreads;
-    const int64_t r = r0 + (o.ks == 1 ? t / (kBK / 4) : t % (kBM / 4) * 4);
-    const int64_t k = k0 + (o.ks == 1 ? t % (kBK / 4) * 4 : t / (kBM / 4));
-    v[i] = r < o.rows && k < o.len ? __ldg(reinterpret_cast<const float4*>(o.p + r * o.rs + k * o.ks))
-                                   : make_float4(0.f, 0.f, 0.f, 0.f);
-  }
-}
-MOE_DEV void put(float (&sm)[kBK][kBM], bool along_k, const float4 (&v)[kVecs]) {
-#pragma unroll
-  for (int i = 0; i < kVecs; ++i) {
-    const int t = threadIdx.x + i * kThreads;
-    if (along_k) {
-      const int r = t / (kBK / 4), k = t % (kBK / 4) * 4;
-      sm[k][swz(k, r)] = v[i].x;
-      sm[k + 1][swz(k, r)] = v[i].y;
-      sm[k + 2][swz(k, r)] = v[i].z;
-      sm[k + 3][swz(k, r)] = v[i].w;
-    } else {
-      const int r = t % (kBM / 4) * 4, k = t / (kBM / 4);
-      *reinterpret_cast<float4*>(&sm[k][swz(k, r)]) = v[i];
-    }
-  }
-}
-
-// acc[i][j] += sum_{k < K} A(m0 + 4 ty + i, k) B(n0 + 4 tx + j, k). The next
-// block's loads are in flight while a block is multiplied.
-MOE_DEV void gemm_tile(Tile& sm, const Operand& A, int64_t m0, const Operand& B, int64_t n0, int64_t K,
-                       float (&acc)[4][4]) {
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  if (K <= 0) return;
-  float4 va[kVecs], vb[kVecs];
-  fetch(A, m0, 0, va);
-  fetch(B, n0, 0, vb);
-  __syncthreads();  // the buffers' last readers are done
-  put(sm.a[0], A.ks == 1, va);
-  put(sm.b[0], B.ks == 1, vb);
-  int buf = 0;
-  for (int64_t k0 = 0; k0 < K; k0 += kBK, buf ^= 1) {
-    __syncthreads();
-    const bool more = k0 + kBK < K;
-    if (more) {
-      fetch(A, m0, k0 + kBK, va);
-      fetch(B, n0, k0 + kBK, vb);
-    }
-#pragma unroll
-    for (int kk = 0; kk < kBK; ++kk) {
-      const float4 a4 = *reinterpret_cast<const float4*>(&sm.a[buf][kk][swz(kk, 4 * ty)]);
-      const float4 b4 = *reinterpret_cast<const float4*>(&sm.b[buf][kk][swz(kk, 4 * tx)]);
-      const float a[4] = {a4.x, a4.y, a4.z, a4.w}, b[4] = {b4.x, b4.y, b4.z, b4.w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(a[i], b[j], acc[i][j]);
-    }
-    if (more) {
-      put(sm.a[buf ^ 1], A.ks == 1, va);
-      put(sm.b[buf ^ 1], B.ks == 1, vb);
-    }
-  }
-}
+using simt::kThreads;
+using simt::Operand;
+using simt::SplitTile;
+using BigTile = simt::Tile<128, 128, 16>;
+using MidTile = simt::Tile<64, 64, 32>;
+template <int B>
+using TileOf = std::conditional_t<B == 128, BigTile, std::conditional_t<B == 64, MidTile, SplitTile>>;
 
 struct Groups {
   const int32_t* unit_base;
@@ -111,7 +38,7 @@ struct Groups {
 };
 
 // Row-tile unit u -> its group, column tile and row tile (as the forward's).
-MOE_DEV void find_unit(const Groups& gr, int u, int& g, int& f, int& m) {
+MOE_DEV void find_unit(const Groups& gr, int bm, int u, int& g, int& f, int& m) {
   int lo = 0, hi = gr.N;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
@@ -119,10 +46,10 @@ MOE_DEV void find_unit(const Groups& gr, int u, int& g, int& f, int& m) {
     else hi = mid - 1;
   }
   g = lo;
-  const int mt = (gr.grp_rows[g] + kBM - 1) / kBM;
+  const int mt = (gr.grp_rows[g] + bm - 1) / bm;
   const int local = u - gr.unit_base[g];
   f = local / mt;
-  m = local % mt;
+  m = local - f * mt;
 }
 
 struct DhParams {
@@ -134,44 +61,74 @@ struct DhParams {
   float* dg;
   float* du;
   float* gh;
-  float* part;        // [ceil(F / 64), R] or null
+  float* part;        // [dgate_planes, R] or null
   int d, F;
   int64_t R;
 };
 
-__global__ void __launch_bounds__(kThreads) dh_simt_kernel(DhParams p) {
-  __shared__ Tile sm;
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+// Four neighbouring features c .. c + 3 (all in or all out: F is a multiple of
+// 8) of one row from q; returns their part of the gate's gradient.
+MOE_DEV float dh_quad(const DhParams& p, int64_t row, int c, const float* q, float gate) {
+  if (c >= p.F) return 0.f;
+  const float4 g4 = __ldg(reinterpret_cast<const float4*>(p.gu + row * 2 * p.F + c));
+  const float4 u4 = __ldg(reinterpret_cast<const float4*>(p.gu + row * 2 * p.F + p.F + c));
+  const float g[4] = {g4.x, g4.y, g4.z, g4.w}, u[4] = {u4.x, u4.y, u4.z, u4.w};
+  float dg[4], du[4], gh[4], dgate = 0.f;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float s = 1.f / (1.f + expf(-g[j])), a = g[j] * s, dh = gate * q[j];
+    dgate = fmaf(q[j], a * u[j], dgate);
+    du[j] = dh * a;
+    dg[j] = dh * u[j] * s * (1.f + g[j] * (1.f - s));
+    gh[j] = gate * a * u[j];
+  }
+  const int64_t at = row * p.F + c;
+  *reinterpret_cast<float4*>(p.dg + at) = make_float4(dg[0], dg[1], dg[2], dg[3]);
+  *reinterpret_cast<float4*>(p.du + at) = make_float4(du[0], du[1], du[2], du[3]);
+  *reinterpret_cast<float4*>(p.gh + at) = make_float4(gh[0], gh[1], gh[2], gh[3]);
+  return dgate;
+}
+
+template <int kB>
+__global__ void __launch_bounds__(kThreads, 2) dh_simt_kernel(DhParams p) {
+  using T = TileOf<kB>;
+  __shared__ T sm;
   const int total = p.gr.unit_base[p.gr.N + 1];
   for (int u = blockIdx.x; u < total; u += gridDim.x) {
     int g, f, m;
-    find_unit(p.gr, u, g, f, m);
+    find_unit(p.gr, kB, u, g, f, m);
     const int rows = p.gr.grp_rows[g];
     const int64_t row0 = p.gr.grp_row0[g];
-    float acc[4][4] = {};
-    gemm_tile(sm, Operand{p.dy + row0 * p.d, p.d, 1, rows, p.d}, (int64_t)m * kBM,
-              Operand{p.W2 + (int64_t)g * p.d * p.F, 1, p.F, p.F, p.d}, (int64_t)f * kBN, p.d, acc);
+    const Operand A{p.dy + row0 * p.d, p.d, 1, rows, p.d}, B{p.W2 + (int64_t)g * p.d * p.F, 1, p.F, p.F, p.d};
+    float* part = p.part ? p.part + (int64_t)f * p.R + row0 : nullptr;
+    if constexpr (kB > SplitTile::kB) {
+      float acc[T::kTM][T::kTN] = {};
+      sm.run(A, m * kB, B, f * kB, p.d, acc);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int r = m * kBM + 4 * ty + i;
-      const int64_t row = row0 + r;
-      const bool in = r < rows;
-      const float gate = in && p.gate ? p.gate[row] : 1.f;
-      float dgate = 0.f;
+      for (int i = 0; i < T::kTM; ++i) {
+        const int r = m * kB + T::row(i);
+        const bool in = r < rows;
+        const float gate = in && p.gate ? p.gate[row0 + r] : 1.f;
+        float dgate = 0.f;
+        if (in)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int c = f * kBN + 4 * tx + j;
-        if (!in || c >= p.F) continue;
-        const float gv = p.gu[row * 2 * p.F + c], uv = p.gu[row * 2 * p.F + p.F + c];
-        const float s = 1.f / (1.f + expf(-gv)), a = gv * s, q = acc[i][j], dh = gate * q;
-        dgate = fmaf(q, a * uv, dgate);
-        p.du[row * p.F + c] = dh * a;
-        p.dg[row * p.F + c] = dh * uv * s * (1.f + gv * (1.f - s));
-        p.gh[row * p.F + c] = gate * a * uv;
+          for (int j = 0; j < T::kTN; j += 4)
+            dgate += dh_quad(p, row0 + r, f * kB + T::col(j), &acc[i][j], gate);
+#pragma unroll
+        for (int off = 8; off > 0; off >>= 1) dgate += __shfl_xor_sync(0xffffffffu, dgate, off);
+        if (part && in && (threadIdx.x & 15) == 0) part[r] = dgate;
       }
+    } else {
+      float acc[4][4] = {}, q[4];
+      sm.run(A, m * kB, B, f * kB, p.d, acc);
+      sm.finish(acc, q);
+      const int r = m * kB + SplitTile::row();
+      const bool in = r < rows;
+      const float gate = in && p.gate ? p.gate[row0 + r] : 1.f;
+      float dgate = in ? dh_quad(p, row0 + r, f * kB + SplitTile::col(), q, gate) : 0.f;
 #pragma unroll
-      for (int off = 8; off > 0; off >>= 1) dgate += __shfl_xor_sync(0xffffffffu, dgate, off);
-      if (p.part && in && tx == 0) p.part[(int64_t)f * p.R + row] = dgate;
+      for (int off = 4; off > 0; off >>= 1) dgate += __shfl_xor_sync(0xffffffffu, dgate, off);
+      if (part && in && (threadIdx.x & 7) == 0) part[r] = dgate;
     }
   }
 }
@@ -187,30 +144,35 @@ struct DxParams {
   int64_t ld;       // a multiple of 4; columns F .. ld - 1 are zero
 };
 
-__global__ void __launch_bounds__(kThreads) dx_simt_kernel(DxParams p) {
-  __shared__ Tile sm;
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+template <int kB>
+__global__ void __launch_bounds__(kThreads, 2) dx_simt_kernel(DxParams p) {
+  using T = TileOf<kB>;
+  __shared__ T sm;
   const int total = p.gr.unit_base[p.gr.N + 1];
   for (int u = blockIdx.x; u < total; u += gridDim.x) {
     int g, f, m;
-    find_unit(p.gr, u, g, f, m);
+    find_unit(p.gr, kB, u, g, f, m);
     const int rows = p.gr.grp_rows[g];
     const int64_t row0 = p.gr.grp_row0[g], w0 = (int64_t)g * p.F * p.d;
-    float acc[4][4] = {};
-    gemm_tile(sm, Operand{p.d0 + row0 * p.ld, p.ld, 1, rows, p.ld}, (int64_t)m * kBM,
-              Operand{p.W0 + w0, 1, p.d, p.d, p.F}, (int64_t)f * kBN, p.F, acc);
+    float acc[kB == 128 ? 8 : 4][kB == 128 ? 8 : 4] = {};
+    sm.run(Operand{p.d0 + row0 * p.ld, p.ld, 1, rows, (int)p.ld}, m * kB, Operand{p.W0 + w0, 1, p.d, p.d, p.F}, f * kB,
+           p.F, acc);
     if (p.d1)
-      gemm_tile(sm, Operand{p.d1 + row0 * p.ld, p.ld, 1, rows, p.ld}, (int64_t)m * kBM,
-                Operand{p.W1 + w0, 1, p.d, p.d, p.F}, (int64_t)f * kBN, p.F, acc);
+      sm.run(Operand{p.d1 + row0 * p.ld, p.ld, 1, rows, (int)p.ld}, m * kB, Operand{p.W1 + w0, 1, p.d, p.d, p.F},
+             f * kB, p.F, acc);
+    auto put = [&](int r, int c, const float* v) {  // four columns (d is a multiple of 8)
+      if (r < rows && c < p.d)
+        *reinterpret_cast<float4*>(p.dx + (row0 + r) * p.d + c) = make_float4(v[0], v[1], v[2], v[3]);
+    };
+    if constexpr (kB > SplitTile::kB) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int r = m * kBM + 4 * ty + i;
-      if (r >= rows) continue;
+      for (int i = 0; i < T::kTM; ++i)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int c = f * kBN + 4 * tx + j;
-        if (c < p.d) p.dx[(row0 + r) * p.d + c] = acc[i][j];
-      }
+        for (int j = 0; j < T::kTN; j += 4) put(m * kB + T::row(i), f * kB + T::col(j), &acc[i][j]);
+    } else {
+      float v[4];
+      sm.finish(acc, v);
+      put(m * kB + SplitTile::row(), f * kB + SplitTile::col(), v);
     }
   }
 }
@@ -226,56 +188,63 @@ struct DwMatrix {
 struct DwParams {
   DwMatrix mat[3];
   int nmat, groups;
+  int per_group[3];  // tiles of a group's matrix
   const int32_t* grp_row0;
   const int32_t* grp_rows;
   int accumulate;
 };
 
-__global__ void __launch_bounds__(kThreads) dw_simt_kernel(DwParams p, int64_t units) {
-  __shared__ Tile sm;
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
-    int64_t left = u;
-    int i0 = 0;
-    int64_t per = 0;
-    for (;; ++i0) {
-      per = (int64_t)((p.mat[i0].M + kBM - 1) / kBM) * ((p.mat[i0].N + kBN - 1) / kBN);
-      if (i0 == p.nmat - 1 || left < per * p.groups) break;
-      left -= per * p.groups;
-    }
+template <class T, int kB>
+__global__ void __launch_bounds__(kThreads, 2) dw_simt_kernel(DwParams p, int units) {
+  __shared__ T sm;
+  for (int u = blockIdx.x; u < units; u += gridDim.x) {
+    int i0 = 0, left = u;
+    while (i0 < p.nmat - 1 && left >= p.per_group[i0] * p.groups) left -= p.per_group[i0++] * p.groups;
     const DwMatrix& x = p.mat[i0];
-    const int g = (int)(left / per);
-    const int64_t local = left % per;
-    const int nt = (x.N + kBN - 1) / kBN;
-    const int64_t m0 = local / nt * kBM, n0 = local % nt * kBN;
+    const int g = left / p.per_group[i0], local = left - g * p.per_group[i0];
+    const int nt = (x.N + kB - 1) / kB, mi = local / nt;
+    const int m0 = mi * kB, n0 = (local - mi * nt) * kB;
     const int64_t row0 = p.grp_row0[g];
-    float acc[4][4] = {};
     const int rows = p.grp_rows[g];
-    gemm_tile(sm, Operand{x.A + row0 * x.lda, 1, x.lda, x.lda, rows}, m0,
-              Operand{x.B + row0 * x.N, 1, x.N, x.N, rows}, n0, rows, acc);
+    float acc[T::kTM][T::kTN] = {};
+    sm.run(Operand{x.A + row0 * x.lda, 1, x.lda, (int)x.lda, rows}, m0, Operand{x.B + row0 * x.N, 1, x.N, x.N, rows}, n0,
+           rows, acc);
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < T::kTM; ++i)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int64_t m = m0 + 4 * ty + i, n = n0 + 4 * tx + j;
-        if (m >= x.M || n >= x.N) continue;
-        float* o = x.out + ((int64_t)g * x.M + m) * x.N + n;
-        *o = p.accumulate ? *o + acc[i][j] : acc[i][j];
+      for (int j = 0; j < T::kTN; j += 4) {
+        const int m = m0 + T::row(i), n = n0 + T::col(j);
+        if (m >= x.M || n >= x.N) continue;  // N is a multiple of 8: four columns are in or out
+        float4* o = reinterpret_cast<float4*>(x.out + ((int64_t)g * x.M + m) * x.N + n);
+        float4 v = make_float4(acc[i][j], acc[i][j + 1], acc[i][j + 2], acc[i][j + 3]);
+        if (p.accumulate) {
+          const float4 w = *o;
+          v = make_float4(w.x + v.x, w.y + v.y, w.z + v.z, w.w + v.w);
+        }
+        *o = v;
       }
   }
 }
 
-int64_t dw_units(const DwParams& p) {
-  int64_t n = 0;
-  for (int i = 0; i < p.nmat; ++i)
-    n += (int64_t)p.groups * ((p.mat[i].M + kBM - 1) / kBM) * ((p.mat[i].N + kBN - 1) / kBN);
-  return n;
+template <class T, int kB>
+cudaError_t launch_dw_tile(DwParams p, cudaStream_t s) {
+  int64_t units = 0;
+  for (int i = 0; i < p.nmat; ++i) {
+    const int64_t n = (int64_t)((p.mat[i].M + kB - 1) / kB) * ((p.mat[i].N + kB - 1) / kB);
+    units += n * p.groups;
+    p.per_group[i] = (int)n;
+  }
+  if (units > (1ll << 30)) return cudaErrorInvalidValue;
+  const int64_t cap = (int64_t)device_sm_count() * 4;
+  dw_simt_kernel<T, kB><<<(unsigned)(units < cap ? units : cap), kThreads, 0, s>>>(p, (int)units);
+  return cudaGetLastError();
 }
 
+// Tiles of 128 where they fill the GPU, of 64 otherwise.
 cudaError_t launch_dw(const DwParams& p, cudaStream_t s) {
-  const int64_t units = dw_units(p), cap = (int64_t)device_sm_count() * 8;
-  dw_simt_kernel<<<(unsigned)(units < cap ? units : cap), kThreads, 0, s>>>(p, units);
-  return cudaGetLastError();
+  int64_t big = 0;
+  for (int i = 0; i < p.nmat; ++i) big += (int64_t)(p.mat[i].M / 128) * (p.mat[i].N / 128) * p.groups;
+  return big >= 2 * device_sm_count() ? launch_dw_tile<BigTile, 128>(p, s) : launch_dw_tile<MidTile, 64>(p, s);
 }
 
 // 32 rows per CTA; warp w adds planes w, w + 8, ..., then the warps' sums are
@@ -306,18 +275,42 @@ cudaError_t launch_dgate_reduce(const float* part, int planes, int64_t rows, flo
   return launch_after(dgate_reduce_kernel, (unsigned)((rows + 31) / 32), 256, 0, s, part, planes, rows, dgate);
 }
 
+// The two row products' tiles: larger ones where they give every SM two of 128 or
+// four of 64. The whole backward with tiles of 128, 64 and 32: 8 groups of 512
+// rows (d 1024, d_ff 1024) 1390, 1510 and 1680 us, of 128 rows 669, 552 and 484
+// us; 16 groups of 256 rows (d 256, d_ff 512) 361, 257 and 290 us, of 32 rows
+// 234, 111 and 85 us.
+int simt_bwd_tile(const Problem& p) {
+  const int64_t cols = p.d + p.F, sms = device_sm_count();
+  if ((p.R + 127) / 128 * (cols / 128) >= 2 * sms) return 128;
+  return (p.R + 63) / 64 * (cols / 64) >= 4 * sms ? 64 : SplitTile::kB;
+}
+
+void launch_dh(const DhParams& h, int tile, cudaStream_t s) {
+  const int sms = device_sm_count();
+  if (tile == 128) dh_simt_kernel<128><<<sms * 2, kThreads, 0, s>>>(h);
+  else if (tile == 64) dh_simt_kernel<64><<<sms * 4, kThreads, 0, s>>>(h);
+  else dh_simt_kernel<32><<<sms * 6, kThreads, 0, s>>>(h);
+}
+void launch_dx(const DxParams& x, int tile, cudaStream_t s) {
+  const int sms = device_sm_count();
+  if (tile == 128) dx_simt_kernel<128><<<sms * 2, kThreads, 0, s>>>(x);
+  else if (tile == 64) dx_simt_kernel<64><<<sms * 4, kThreads, 0, s>>>(x);
+  else dx_simt_kernel<32><<<sms * 6, kThreads, 0, s>>>(x);
+}
+
 cudaError_t launch_experts_backward_simt(const Problem& p, const ExpertsBwdArgs& a, cudaStream_t s) {
-  const int grid = device_sm_count() * 6;
+  const int tile = simt_bwd_tile(p);
   const Groups g1{a.unit_base1, a.grp_row0, a.grp_rows, p.N}, g2{a.unit_base2, a.grp_row0, a.grp_rows, p.N};
   DhParams h{g1, (const float*)a.dy_rows, (const float*)a.W2, (const float*)a.gu, a.gate_rows, (float*)a.dg,
              (float*)a.du, (float*)a.gh, a.dgate_rows ? a.dgate_part : nullptr, p.d, p.F, p.R};
-  dh_simt_kernel<<<grid, kThreads, 0, s>>>(h);
+  launch_dh(h, tile, s);
   cudaError_t e = cudaGetLastError();
   if (e == cudaSuccess && a.dgate_rows) e = launch_dgate_reduce(a.dgate_part, dgate_planes(p), p.R, a.dgate_rows, s);
   if (e == cudaSuccess && a.dx_rows) {
     DxParams x{g2, (const float*)a.dg, (const float*)a.du, (const float*)a.W1, (const float*)a.W3, (float*)a.dx_rows,
                p.d, p.F, p.F};
-    dx_simt_kernel<<<grid, kThreads, 0, s>>>(x);
+    launch_dx(x, tile, s);
     e = cudaGetLastError();
   }
   if (e == cudaSuccess && a.dW1) {
@@ -338,11 +331,14 @@ cudaError_t launch_experts_backward_simt(const Problem& p, const ExpertsBwdArgs&
 cudaError_t launch_route_products_simt(const Problem& p, const RouteBwdArgs& a, cudaStream_t s) {
   const int32_t* row0 = a.tables + kRtRow0;
   const int32_t* rows = a.tables + kRtRows;
+  Problem one = p;  // one group of T rows
+  one.F = p.d;
+  one.R = p.T;
   cudaError_t e = cudaSuccess;
   if (a.dx) {
     DxParams x{Groups{a.tables + kRtUnits, row0, rows, 1}, a.dz, nullptr, (const float*)a.W_r, nullptr,
                (float*)a.dx, p.d, p.N, a.ld};
-    dx_simt_kernel<<<device_sm_count() * 6, kThreads, 0, s>>>(x);
+    launch_dx(x, simt_bwd_tile(one), s);
     e = cudaGetLastError();
   }
   if (e == cudaSuccess && a.dW_r) {

@@ -228,6 +228,17 @@ def test_experts_backward(counts, d, F, dtype, grad_dtype):
                 assert not out[name][e].any(), name
 
 
+def test_experts_backward_in_tiles_that_fill_the_gpu():
+    # fp32: 25 x 6 and more tiles of 128 x 128, ragged in every direction
+    b = Block([2100, 0, 1, 900, 130], 776, 1000, "f32", seed=21)
+    b.forward()
+    check_block(b, b.backward(), *b.exact())
+    # a workspace for these rows also holds a call of fewer
+    small = Block([40, 7], 776, 1000, "f32", seed=22)
+    assert (moe.experts_backward_workspace_size(small.cfg, 3000) <=
+            moe.experts_backward_workspace_size(small.cfg, 3131))
+
+
 def test_experts_backward_without_gates():
     b = Block([33, 0, 70], 136, 264, gate=False, seed=3)
     check_block(b, b.backward(), *b.exact())
