@@ -12,135 +12,136 @@
 // round dz to bf16 for them, as the experts' dg and du are (one rounding per
 // term of sums kept in fp32); dz is written both ways. fp32 layers keep fp32.
 //
-// The kernel reads the logits once and writes dz twice (2 T N of each): a few
-// microseconds at any size here, next to the products.
+// Only selected experts have a gradient, except under an unnormalised softmax
+// (normalised gates depend on ratios of the selected scores alone, so their
+// softmax is taken relative to the largest selected logit). So a CTA zeroes a
+// tile of 16 tokens in shared memory, half a warp per token works out its slots
+// and scatters them, and the tile is written out both ways in 16-byte vectors.
+// What bounds it is the chain launch - slot loads - scatter - stores: ROUTE_DZ_FIGURE
 #include "common.cuh"
 #include "internal.h"
 
 namespace moe {
 namespace {
 
-MOE_DEV float wsum(float v) {
+template <int W>
+MOE_DEV float gsum(float v) {  // over W neighbouring lanes
 #pragma unroll
-  for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+  for (int off = W / 2; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
   return v;
 }
-MOE_DEV float wmax(float v) {
+template <int W>
+MOE_DEV float gmax(float v) {
 #pragma unroll
-  for (int off = 16; off > 0; off >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, off));
+  for (int off = W / 2; off > 0; off >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, off));
   return v;
 }
 
 constexpr int kDzTokens = 16;  // tokens of a CTA: 32-byte runs of the transposed dz
-constexpr int kDzWarps = 16;
+constexpr int kDzSlots = 16;   // lanes of a token
+constexpr int kDzThreads = kDzTokens * kDzSlots;
+static_assert(kMaxTopK <= kDzSlots && kRouteTables <= kDzThreads, "a slot per lane, a table entry per thread");
 
-// One warp per token. Lane l holds experts 32 j + l, j < V; slot
-// i of the token sits in lane i.
-template <int V>
-__global__ void __launch_bounds__(32 * kDzWarps) route_dz_kernel(const __grid_constant__ RouteDzArgs a) {
+// kDense: unnormalised softmax, where every expert's logit has a gradient.
+template <bool kDense>
+__global__ void __launch_bounds__(kDzThreads) route_dz_kernel(const __grid_constant__ RouteDzArgs a) {
   griddep_launch_dependents();
-  __shared__ __nv_bfloat16 tile[32 * V][kDzTokens + 2];  // [expert][token] (+2: rows start in different banks)
-  if (blockIdx.x == 0 && threadIdx.x < kRouteTables) a.tables[threadIdx.x] = a.table_values[threadIdx.x];
-  const int lane = threadIdx.x & 31;
-  const int N = a.N, k = a.k;
+  extern __shared__ float4 dz_smem[];
+  float* tile = reinterpret_cast<float*>(dz_smem);  // [token][expert], pitch ld
+  const int tid = threadIdx.x;
+  if (blockIdx.x == 0 && tid < kRouteTables) a.tables[tid] = a.table_values[tid];
+  const int N = a.N, k = a.k, ld = (int)a.ld;
   const int64_t t0 = (int64_t)blockIdx.x * kDzTokens;
-  for (int w = threadIdx.x >> 5; w < kDzTokens; w += kDzWarps) {
-    const int64_t t = t0 + w;
-    if (t >= a.T) break;
-    float s[V], om[V], ds[V];  // scores, 1 - sigmoid, gradient of the scores
-#pragma unroll
-    for (int j = 0; j < V; ++j) {
-      s[j] = 32 * j + lane < N ? __ldg(a.logits + t * N + 32 * j + lane) : -INFINITY;
-      om[j] = 1.f;
-      ds[j] = 0.f;
-    }
-    // this lane's slot: its expert (-1: none) and logit, and whether it is the expert's first slot
-    int e = lane < k ? __ldg(a.idx + t * k + lane) : -1;
-    if (lane < k && (e < 0 || e >= N)) {
-      set_status(a.status, MOE_DEV_BAD_EXPERT);
-      e = -1;
-    }
-    float my_s = e >= 0 ? __ldg(a.logits + t * N + e) : -INFINITY;
-    const unsigned same = __match_any_sync(0xffffffffu, e);
-    const bool firsts = e >= 0 && lane == __ffs(same) - 1;
-    float dG = 0.f;
-    if (a.slot_pos) {
-      // the gradient of the slot's gate is that of the row the dispatch gave it:
-      // slot_pos lists the token's rows by ascending expert
-      int rank = 0;
-      for (int i = 0; i < k; ++i) {
-        const int ei = __shfl_sync(0xffffffffu, firsts ? e : -1, i);
-        rank += ei >= 0 && ei < e;
-      }
-      if (firsts) {
-        const int32_t row = __ldg(a.slot_pos + t * k + rank);
-        if (row >= 0 && row < a.T * k) dG = __ldg(a.dgates + row);
-      }
-    } else if (e >= 0) {
-      dG = __ldg(a.dgates + t * k + lane);
-    }
-    if (a.score_fn == MOE_SOFTMAX) {
-      float m = -INFINITY;
-#pragma unroll
-      for (int j = 0; j < V; ++j) m = fmaxf(m, s[j]);
-      m = wmax(m);
-      float sum = 0.f;
-#pragma unroll
-      for (int j = 0; j < V; ++j) {
-        s[j] = 32 * j + lane < N ? expf(s[j] - m) : 0.f;
-        sum += s[j];
-      }
-      const float inv = 1.f / wsum(sum);
-#pragma unroll
-      for (int j = 0; j < V; ++j) s[j] *= inv;
-      my_s = e >= 0 ? expf(my_s - m) * inv : 0.f;
-    } else {
-#pragma unroll
-      for (int j = 0; j < V; ++j) {
-        const float z = s[j];
-        s[j] = 32 * j + lane < N ? 1.f / (1.f + expf(-z)) : 0.f;
-        om[j] = 1.f / (1.f + expf(z));  // 1 - s without its cancellation
-      }
-      my_s = e >= 0 ? 1.f / (1.f + expf(-my_s)) : 0.f;
-    }
-    float my_ds = a.route_scale * dG;
-    float mean = 0.f;  // sum of ds_i s_i over the slots (zero for normalised gates)
-    if (a.normalize) {
-      const float Z = wsum(my_s), dot = wsum(dG * my_s);
-      my_ds = a.route_scale / Z * (dG - dot / Z);
-    } else if (a.score_fn == MOE_SOFTMAX) {
-      mean = wsum(my_ds * my_s);
-    }
-    for (int i = 0; i < k; ++i) {
-      const int ei = __shfl_sync(0xffffffffu, e, i);
-      const float v = __shfl_sync(0xffffffffu, my_ds, i);
-      if (ei < 0 || lane != (ei & 31)) continue;
-#pragma unroll
-      for (int j = 0; j < V; ++j)
-        if (j == ei >> 5) ds[j] += v;
-    }
-#pragma unroll
-    for (int j = 0; j < V; ++j) {
-      const int col = 32 * j + lane;
-      const float dz = a.score_fn == MOE_SOFTMAX ? s[j] * (ds[j] - mean) : ds[j] * s[j] * om[j];
-      if (a.dz) {
-        // (columns N .. ld - 1 are zero)
-        if (col < a.ld) a.dz[t * a.ld + col] = col < N ? dz : 0.f;
-      } else if (col < N) {
-        const __nv_bfloat16 v = __float2bfloat16_rn(dz);
-        a.dz16[t * a.ld + col] = v;
-        tile[col][w] = v;
-      }
-    }
+  const int w = tid / kDzSlots, slot = tid % kDzSlots;
+  const int64_t t = t0 + w;
+  const bool live = t < a.T && slot < k;
+  int e = live ? __ldg(a.idx + t * k + slot) : -1;  // -1: none
+  if (live && (e < 0 || e >= N)) {
+    set_status(a.status, MOE_DEV_BAD_EXPERT);
+    e = -1;
   }
-  if (a.dz || !a.dz16_t) return;
+  const float z = e >= 0 ? __ldg(a.logits + t * N + e) : -INFINITY;
+  for (int i = tid; i < kDzTokens * ld / 4; i += kDzThreads) dz_smem[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+  // (the other half of the warp is another token)
+  const unsigned same = __match_any_sync(0xffffffffu, (w & 1) << 16 | (e & 0xffff));
+  const bool first = e >= 0 && (tid & 31) == __ffs(same) - 1;  // the expert's first slot
+  float dG = 0.f;
+  if (a.slot_pos) {
+    // the gradient of the slot's gate is that of the row the dispatch gave it:
+    // slot_pos lists the token's rows by ascending expert
+    int rank = 0;
+    for (int i = 0; i < k; ++i) {
+      const int ei = __shfl_sync(0xffffffffu, first ? e : -1, i, kDzSlots);
+      rank += ei >= 0 && ei < e;
+    }
+    if (first) {
+      const int32_t row = __ldg(a.slot_pos + t * k + rank);
+      if (row >= 0 && row < a.T * k) dG = __ldg(a.dgates + row);
+    }
+  } else if (e >= 0) {
+    dG = __ldg(a.dgates + t * k + slot);
+  }
+  float sc = 0.f, slope = 1.f;  // the score (up to Z) and what its logit's gradient takes from it
+  if (a.score_fn == MOE_SIGMOID) {
+    sc = e >= 0 ? 1.f / (1.f + expf(-z)) : 0.f;
+    slope = sc * (1.f / (1.f + expf(z)));  // 1 - s without its cancellation
+  } else if (!kDense) {
+    const float m = gmax<kDzSlots>(z);
+    sc = e >= 0 ? expf(z - m) : 0.f;
+    slope = sc;
+  }
+  float ds = a.route_scale * dG;
+  if (a.normalize) {
+    const float Z = gsum<kDzSlots>(sc), dot = gsum<kDzSlots>(dG * sc);
+    ds = a.route_scale / Z * (dG - dot / Z);
+  }
+  float sum = 0.f;  // over the slots that name this expert
+  for (int i = 0; i < k; ++i) {
+    const int ei = __shfl_sync(0xffffffffu, e, i, kDzSlots);
+    const float v = __shfl_sync(0xffffffffu, ds, i, kDzSlots);
+    if (ei == e) sum += v;
+  }
   __syncthreads();
-  for (int i = threadIdx.x; i < N * (kDzTokens / 2); i += blockDim.x) {
-    const int n = i / (kDzTokens / 2), c = i % (kDzTokens / 2) * 2;
-    // a pair that starts inside T may end one past it, in the row's padding
-    if (t0 + c < a.T)
-      *reinterpret_cast<uint32_t*>(a.dz16_t + (int64_t)n * a.ld_t + t0 + c) =
-          *reinterpret_cast<const uint32_t*>(&tile[n][c]);
+  if (first) tile[w * ld + e] = kDense ? sum : sum * slope;
+  __syncthreads();
+  if constexpr (kDense) {
+    // a warp per token: s_j (ds_j - sum ds_i s_i) over all experts
+    const int lane = tid & 31;
+    for (int i = tid / 32; i < kDzTokens && t0 + i < a.T; i += kDzThreads / 32) {
+      const float* logits = a.logits + (t0 + i) * N;
+      float* row = tile + i * ld;
+      float m = -INFINITY, Z = 0.f, dot = 0.f;
+      for (int j = lane; j < N; j += 32) m = fmaxf(m, __ldg(logits + j));
+      m = gmax<32>(m);
+      for (int j = lane; j < N; j += 32) {
+        const float x = expf(__ldg(logits + j) - m);
+        Z += x;
+        dot = fmaf(x, row[j], dot);
+      }
+      const float inv = 1.f / gsum<32>(Z), mean = gsum<32>(dot) * inv;
+      for (int j = lane; j < N; j += 32) row[j] = expf(__ldg(logits + j) - m) * inv * (row[j] - mean);
+    }
+    __syncthreads();
+  }
+  const int tokens = (int)(a.T - t0 < kDzTokens ? a.T - t0 : kDzTokens);
+  if (a.dz) {  // (columns N .. ld - 1 are zero)
+    float4* out = reinterpret_cast<float4*>(a.dz + t0 * ld);
+    for (int i = tid; i < tokens * ld / 4; i += kDzThreads) out[i] = dz_smem[i];
+    return;
+  }
+  uint4* out = reinterpret_cast<uint4*>(a.dz16 + t0 * ld);
+  for (int i = tid; i < tokens * ld / 8; i += kDzThreads) {
+    const float4 u = dz_smem[2 * i], v = dz_smem[2 * i + 1];
+    out[i] = make_uint4(pack_bf16x2(u.x, u.y), pack_bf16x2(u.z, u.w), pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+  }
+  if (!a.dz16_t) return;
+  for (int i = tid; i < 2 * N; i += kDzThreads) {
+    const int n = i >> 1, c = (i & 1) * 8;
+    if (c >= tokens) continue;  // eight that start inside T may end in the row's padding
+    const float* x = tile + c * ld + n;
+    *reinterpret_cast<uint4*>(a.dz16_t + n * a.ld_t + t0 + c) =
+        make_uint4(pack_bf16x2(x[0], x[ld]), pack_bf16x2(x[2 * ld], x[3 * ld]), pack_bf16x2(x[4 * ld], x[5 * ld]),
+                   pack_bf16x2(x[6 * ld], x[7 * ld]));
   }
 }
 
@@ -177,12 +178,9 @@ __global__ void __launch_bounds__(256) join_planes_kernel(const float4* __restri
 
 cudaError_t launch_route_dz(const RouteDzArgs& a, cudaStream_t s) {
   const unsigned blocks = (unsigned)((a.T + kDzTokens - 1) / kDzTokens);
-  const int V = (a.N + 31) / 32, threads = 32 * kDzWarps;
-  if (V <= 1) route_dz_kernel<1><<<blocks, threads, 0, s>>>(a);
-  else if (V <= 2) route_dz_kernel<2><<<blocks, threads, 0, s>>>(a);
-  else if (V <= 4) route_dz_kernel<4><<<blocks, threads, 0, s>>>(a);
-  else if (V <= 8) route_dz_kernel<8><<<blocks, threads, 0, s>>>(a);
-  else route_dz_kernel<16><<<blocks, threads, 0, s>>>(a);
+  const size_t smem = (size_t)kDzTokens * a.ld * 4;
+  if (a.score_fn == MOE_SOFTMAX && !a.normalize) route_dz_kernel<true><<<blocks, kDzThreads, smem, s>>>(a);
+  else route_dz_kernel<false><<<blocks, kDzThreads, smem, s>>>(a);
   return cudaGetLastError();
 }
 

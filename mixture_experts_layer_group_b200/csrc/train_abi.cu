@@ -58,16 +58,15 @@ RouteLayout make_route_layout(const Problem& p) {
   L.ld = (p.N + 7) / 8 * 8;
   L.ld_t = (p.T + 7) / 8 * 8;
   L.splits = 1;
-  if (tc) {
-    // dW_r is N x d summed over all tokens: few tiles with a long sum. The
-    // tokens are split so that about one tile per CTA pair runs at a time,
-    // each over 256 tokens or more.
-    const int64_t tiles = (int64_t)((p.N + 255) / 256) * ((p.d + 255) / 256);
-    int64_t n = kRouterTargetSms / 2 / tiles;
-    if (n > p.T / 256) n = p.T / 256;
-    if (n > kMaxRouteSplits) n = kMaxRouteSplits;
-    if (n > 1) L.splits = (int)n;
-  }
+  // dW_r is N x d summed over all tokens: few tiles with a long sum. The tokens
+  // are split so that about one tile of 256 per CTA pair runs at a time (bf16,
+  // each over 256 tokens or more), or four tiles of 64 per SM (fp32).
+  const int side = tc ? 256 : 64, least = tc ? 256 : 64;
+  const int64_t tiles = (int64_t)((p.N + side - 1) / side) * ((p.d + side - 1) / side);
+  int64_t n = (tc ? kRouterTargetSms / 2 : 4 * kRouterTargetSms) / tiles;
+  if (n > p.T / least) n = p.T / least;
+  if (n > kMaxRouteSplits) n = kMaxRouteSplits;
+  if (n > 1) L.splits = (int)n;
   L.status = take(256);
   L.tables = take(kRouteTables * 4);
   L.dz = take((size_t)p.T * L.ld * p.elem);

@@ -240,7 +240,10 @@ cudaError_t launch_dw_tile(DwParams p, cudaStream_t s) {
   return cudaGetLastError();
 }
 
-// Tiles of 128 where they fill the GPU, of 64 otherwise.
+// Tiles of 128 where they fill the GPU, of 64 otherwise. The whole backward with
+// 64 against 128: 8 groups, d 1024, d_ff 1024 (1536 tiles of 128) of 512 rows
+// 1539 and 1390 us, of 16 rows 171 and 148 us. The router's few tiles (16 of
+// them at 64 experts, d 1024, 4096 tokens) took 242 and 529 us without a split.
 cudaError_t launch_dw(const DwParams& p, cudaStream_t s) {
   int64_t big = 0;
   for (int i = 0; i < p.nmat; ++i) big += (int64_t)(p.mat[i].M / 128) * (p.mat[i].N / 128) * p.groups;
@@ -342,14 +345,17 @@ cudaError_t launch_route_products_simt(const Problem& p, const RouteBwdArgs& a, 
     e = cudaGetLastError();
   }
   if (e == cudaSuccess && a.dW_r) {
+    const bool split = a.splits > 1;
     DwParams w{};
-    w.mat[0] = {a.dz, (const float*)a.x, (float*)a.dW_r, p.N, p.d, a.ld};
+    w.mat[0] = {a.dz, (const float*)a.x, split ? a.planes : (float*)a.dW_r, p.N, p.d, a.ld};
     w.nmat = 1;
-    w.groups = 1;
-    w.grp_row0 = row0;
-    w.grp_rows = rows;
-    w.accumulate = a.accumulate;
-    e = launch_dw(w, s);
+    w.groups = a.splits;
+    w.grp_row0 = a.tables + kRtSplit0;
+    w.grp_rows = a.tables + kRtSplitRows;
+    w.accumulate = !split && a.accumulate;
+    e = launch_dw_tile<MidTile, 64>(w, s);
+    if (e == cudaSuccess && split)
+      e = launch_join_planes(a.planes, a.splits, (int64_t)p.N * p.d, a.dW_r, a.grad_dtype, a.accumulate, s);
   }
   return e;
 }
