@@ -168,21 +168,28 @@ static_assert(kMaxTok % (2 * kTokBox) == 0 && Plan<false>::kChunk <= kMaxTok && 
 
 // The forward's two GEMMs, the SwiGLU GEMM that also keeps g and u, and the
 // backward's two products on the weights (see BwdParams).
-enum Mode : int { kSwiGLU = 0, kGateDown = 1, kSwiGLUKeep = 2, kDh = 3, kDx = 4, kDhWide = 5, kDownEdge = 6, kDxEdge = 7 };
+enum Mode : int { kSwiGLU = 0, kGateDown = 1, kSwiGLUKeep = 2, kDh = 3, kDx = 4, kDhWide = 5, kDownEdge = 6, kDxEdge = 7,
+                  kKeepEdge = 8 };
+__host__ __device__ constexpr bool is_keep(int mode) { return mode == kSwiGLUKeep || mode == kKeepEdge; }
 __host__ __device__ constexpr bool is_down(int mode) { return mode == kGateDown || mode == kDownEdge; }
 __host__ __device__ constexpr bool is_dx(int mode) { return mode == kDx || mode == kDxEdge; }
-__host__ __device__ constexpr bool is_swiglu(int mode) { return mode == kSwiGLU || mode == kSwiGLUKeep; }
+__host__ __device__ constexpr bool is_swiglu(int mode) { return mode == kSwiGLU || is_keep(mode); }
 __host__ __device__ constexpr bool is_dh(int mode) { return mode == kDh || mode == kDhWide; }
 __host__ __device__ constexpr bool is_bwd(int mode) { return is_dh(mode) || is_dx(mode); }
-__host__ __device__ constexpr bool is_wide(int mode) { return mode == kSwiGLUKeep || is_dh(mode); }
+__host__ __device__ constexpr bool is_wide(int mode) { return is_keep(mode) || is_dh(mode); }
 // One 128-row weight half per CTA instead of two: a unit then takes one of the
 // two accumulator buffers whatever its tokens, and its epilogue overlaps the
 // next unit's MMAs.
 __host__ __device__ constexpr bool one_half(int mode) { return mode == kDh; }
-// The down and dx GEMMs of a matrix whose last unit of 512 columns has 256 or
-// fewer left (edge_halves()): that unit takes one half as well, 128 rows per CTA.
-// A mode of its own, because the decision per unit costs the other shapes 0.5 %.
-__host__ __device__ constexpr bool may_halve(int mode) { return mode == kDownEdge || mode == kDxEdge; }
+// GEMMs of a matrix whose last unit has half its columns or fewer left
+// (edge_halves()): that unit takes one half as well, 128 weight rows per CTA. The
+// down and dx GEMMs have 256 columns of 512 then; the SwiGLU GEMM 128 features,
+// whose half holds 64 rows of W1 over 64 rows of W3 in either CTA, and the
+// warps of TMEM lanes 64 .. 127 hand u to those of lanes 0 .. 63 in shared memory.
+// Modes of their own, because the decision per unit costs the other shapes 0.5 %.
+__host__ __device__ constexpr bool may_halve(int mode) {
+  return mode == kDownEdge || mode == kDxEdge || mode == kKeepEdge;
+}
 // Weight bytes at the head of a bf16 stage.
 __host__ __device__ constexpr int a_bytes(int mode) { return one_half(mode) ? kHalfBytes : kATileBytes; }
 
@@ -240,6 +247,7 @@ struct TcParams {
 // so a box past the expert's last row or column loads zeros.
 struct BwdParams : TcParams {
   CUtensorMap b1[kTokMaps];  // du (kDx)
+  CUtensorMap a0_edge, a1_edge;  // W1 and W3 in boxes of 64 rows (kKeepEdge)
   CUtensorMap o_g, o_u;
   __nv_bfloat16* out_g;      // row stride ld_g
   __nv_bfloat16* out_u;
@@ -254,6 +262,10 @@ struct ParamsOf {
 };
 template <>
 struct ParamsOf<kSwiGLUKeep> {
+  using type = BwdParams;
+};
+template <>
+struct ParamsOf<kKeepEdge> {
   using type = BwdParams;
 };
 template <>
@@ -377,6 +389,8 @@ MOE_DEV void epi_sync() { asm volatile("bar.sync 1, %0;" ::"n"(32 * kWarps) : "m
 // Barrier among the FP8 converter warps only (id 2).
 template <int kWarps>
 MOE_DEV void cvt_sync() { asm volatile("bar.sync 2, %0;" ::"n"(32 * kWarps) : "memory"); }
+// The two epilogue warps that share the blocks of a SwiGLU unit of one half (ids 0..3).
+MOE_DEV void edge_sync(int id) { asm volatile("bar.sync %0, 64;" ::"r"(3 + id) : "memory"); }
 
 // Two e4m3 codes (bytes i and i + 1 of w, i = 0 or 2) -> the bf16 pair of
 // their values times 2^-120. For a code s eeee mmm the bf16 bit pattern
@@ -651,9 +665,11 @@ __global__ void __launch_bounds__(Plan<FP8>::kThreads, 1)
   // signalling thread about 1000 cycles.
   constexpr int kRingReaders = FP8 ? 3 : 2;
   const int half_cols = is_swiglu(MODE) ? 0 : 128;
-  // whether a unit takes one half of its 512 columns
+  constexpr int kEdgeRows = is_swiglu(MODE) ? 64 : 128;  // a CTA's output columns of a unit that takes one half
+  // whether a unit does
   auto halved = [&](int f, bool shared) {
-    return may_halve(MODE) && f * kTcBN2 + kTcBN2 / 2 >= (shared ? p.cols_shared : p.cols_routed);
+    constexpr int kCols = is_swiglu(MODE) ? kTcBN1 : kTcBN2;
+    return may_halve(MODE) && f * kCols + kCols / 2 >= (shared ? p.cols_shared : p.cols_routed);
   };
 
   if (threadIdx.x == 0) {
@@ -813,7 +829,7 @@ __global__ void __launch_bounds__(Plan<FP8>::kThreads, 1)
         const uint32_t tx = a_len + nbox * kBoxBytes;
         // weight row (backward: first column of the expert's matrix)
         const int rowA = (shared || is_bwd(MODE) ? 0 : un.g * p.a_rows_per_expert) + un.f * p.tile_cols +
-                         (half ? 128 * (int)rank : rank_rows);
+                         (half ? kEdgeRows * (int)rank : rank_rows);
         const int rowB = row0 + un.tok0 + (int)rank * half_n;
         // the unit's rows lie inside the group and its tensors (TMA clips a
         // box that reaches past them, and the last column tile of a matrix
@@ -862,6 +878,12 @@ __global__ void __launch_bounds__(Plan<FP8>::kThreads, 1)
                 if (c * kMnBox < (int)a_len)
                   tma_load_3d_pair(a_dst + c * kMnBox, ta, full_bar, rowA + 64 * c, k0, un.g, pol);
               tma_load_2d_pair(b_dst, second ? &p.b1[tmap] : tb, full_bar, k0, rowB, pol_last);
+            } else if (MODE == kKeepEdge && half) {
+              if constexpr (MODE == kKeepEdge) {
+                tma_load_2d_pair(a_dst, &p.a0_edge, full_bar, kc * kBK, rowA, pol);
+                tma_load_2d_pair(a_dst + kHalfBytes / 2, &p.a1_edge, full_bar, kc * kBK, rowA, pol);
+              }
+              tma_load_2d_pair(b_dst, tb, full_bar, kc * kBK, rowB, pol_last);
             } else if (!FP8) {
               tma_load_2d_pair(a_dst, ta0, full_bar, kc * kBK, rowA, pol);  // SwiGLU: 128 W1 rows; down: 256 rows
               if (is_swiglu(MODE)) tma_load_2d_pair(a_dst + kHalfBytes, ta1, full_bar, kc * kBK, rowA, pol);
@@ -1047,7 +1069,7 @@ __global__ void __launch_bounds__(Plan<FP8>::kThreads, 1)
       const bool half = halved(un.f, shared);
       const int halves = is_dh(MODE) ? 0 : is_swiglu(MODE) || half ? 1 : 2;
       // this warp's first output column of the unit
-      const int c_first = un.f * p.tile_cols + (half ? 128 * (int)rank : rank_rows) + 32 * q;
+      const int c_first = un.f * p.tile_cols + (half ? kEdgeRows * (int)rank : rank_rows) + 32 * q;
       if constexpr (is_dh(MODE))
         dh_epilogue(p, un, row_base, t_q, stride, one_half(MODE) || half ? 1 : 2, reinterpret_cast<uint8_t*>(tile),
                     c_first, sub, kEpiWarps / 4);
@@ -1069,16 +1091,51 @@ __global__ void __launch_bounds__(Plan<FP8>::kThreads, 1)
           // group r give this thread features 16 hf + 8 e + lane / 4 (e = 0, 1)
           // and tokens 8 r + 2 (lane % 4) + 0..1, packed as bf16 pairs.
           uint32_t pk[2][4][2];
-          uint32_t pg[2][4][2], pu[2][4][2];  // kSwiGLUKeep: g and u
+          uint32_t pg[2][4][2], pu[2][4][2];  // is_keep: g and u
           const int tq = 2 * (lane & 3);
           const uint32_t tile_addr = smem_u32(tile);
+          if (MODE == kKeepEdge && half && q >= 2) {
+            // u of the features of quadrant q - 2, in the layout that its warp reads it
+            if (lane == 0) bulk_wait_group_read<0>();
+            __syncwarp();
+            float4* u_out = reinterpret_cast<float4*>(tile) + lane;
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf) {
+              uint32_t b[16];
+              tmem_ld16x256b_x4(t_q + ((uint32_t)(16 * hf) << 16) + j0, b);
+              tmem_wait_ld();
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                u_out[32 * (4 * hf + i)] = make_float4(__uint_as_float(b[4 * i]), __uint_as_float(b[4 * i + 1]),
+                                                       __uint_as_float(b[4 * i + 2]), __uint_as_float(b[4 * i + 3]));
+            }
+            edge_sync(2 * sub + (q & 1));  // written
+            edge_sync(2 * sub + (q & 1));  // read
+            continue;
+          }
+          const bool from_peer = MODE == kKeepEdge && half;
+          // (the warp of quadrant q + 2 with the same blocks is epilogue warp 4 sub + q)
+          const float4* u_in = reinterpret_cast<const float4*>(reinterpret_cast<const uint8_t*>(tiles) +
+                                                               (4 * sub + q) * PL::kTiles * kTileBytes) + lane;
+          if (from_peer) edge_sync(2 * sub + (q & 1));
 #pragma unroll
           for (int hf = 0; hf < 2; ++hf) {
             uint32_t a[16];
             tmem_ld16x256b_x4(t_q + ((uint32_t)(16 * hf) << 16) + hh * stride + j0, a);
             if (is_swiglu(MODE)) {
               uint32_t b[16];
-              tmem_ld16x256b_x4(t_q + ((uint32_t)(16 * hf) << 16) + stride + j0, b);  // u of the same features
+              if (from_peer) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                  const float4 v = u_in[32 * (4 * hf + i)];
+                  b[4 * i] = __float_as_uint(v.x);
+                  b[4 * i + 1] = __float_as_uint(v.y);
+                  b[4 * i + 2] = __float_as_uint(v.z);
+                  b[4 * i + 3] = __float_as_uint(v.w);
+                }
+              } else {
+                tmem_ld16x256b_x4(t_q + ((uint32_t)(16 * hf) << 16) + stride + j0, b);  // u of the same features
+              }
               tmem_wait_ld();
 #pragma unroll
               for (int r = 0; r < 4; ++r)
@@ -1087,7 +1144,7 @@ __global__ void __launch_bounds__(Plan<FP8>::kThreads, 1)
                   const int x = 4 * r + 2 * e;
                   const float g0 = __uint_as_float(a[x]), g1 = __uint_as_float(a[x + 1]);
                   const float u0 = __uint_as_float(b[x]), u1 = __uint_as_float(b[x + 1]);
-                  if (MODE == kSwiGLUKeep) {
+                  if (is_keep(MODE)) {
                     const uint64_t g[1] = {f32x2(g0, g1)}, u = f32x2(u0, u1);
                     uint64_t sg[1];
                     sigmoid_f32x2(g, sg);
@@ -1115,6 +1172,7 @@ __global__ void __launch_bounds__(Plan<FP8>::kThreads, 1)
               }
             }
           }
+          if (from_peer) edge_sync(2 * sub + (q & 1));  // u has been read
           // Transpose into this warp's [32 tokens][32 features] tile, 64-byte
           // swizzled (16-byte chunk c of token row t sits at chunk c ^ ((t >> 1) & 3)),
           // with four transposing matrix stores.
@@ -1390,7 +1448,7 @@ cudaError_t launch_one(const typename ParamsOf<MODE>::type& prm, int max_units, 
 // Whether the last unit of a matrix of this width takes one half. 57344 rows of
 // 896 features, d 1280 (units of 512, 512 and 256 columns): the training forward
 // 429 us without, 413 with; the backward 895 and 864.
-bool edge_halves(int cols) { return (cols + kTcBN2 / 2 - 1) / (kTcBN2 / 2) % 2 == 1; }
+bool edge_halves(int cols, int tile) { return (cols + tile / 2 - 1) / (tile / 2) % 2 == 1; }
 
 }  // namespace
 
@@ -1461,7 +1519,12 @@ cudaError_t launch_expert_gemms_tc(const Problem& p, const GemmArgs& a, cudaStre
     gk.out_g = (__nv_bfloat16*)a.gu;
     gk.out_u = gk.out_g + p.F;
     gk.ld_g = 2 * (int64_t)p.F;
-    err = launch_one<kSwiGLUKeep, false>(gk, grid1, s, a.sched_clear);
+    const bool edge = edge_halves(p.F, kTcBN1);
+    if (edge && (!make_tmap(&gk.a0_edge, a.W1, (uint64_t)p.N * p.F, p.d, 64) ||
+                 !make_tmap(&gk.a1_edge, a.W3, (uint64_t)p.N * p.F, p.d, 64)))
+      return cudaErrorInvalidValue;
+    err = edge ? launch_one<kKeepEdge, false>(gk, grid1, s, a.sched_clear)
+               : launch_one<kSwiGLUKeep, false>(gk, grid1, s, a.sched_clear);
   } else {
     err = fp8 ? launch_one<kSwiGLU, true>(g1, grid1, s, false) : launch_one<kSwiGLU, false>(g1, grid1, s, a.sched_clear);
   }
@@ -1511,7 +1574,7 @@ cudaError_t launch_expert_gemms_tc(const Problem& p, const GemmArgs& a, cudaStre
   const int grid2 = (int)(units2 < sms ? units2 : sms);
   // the down GEMM overlaps the SwiGLU GEMM's drain unless an event must be
   // recorded between the two
-  if (!fp8 && edge_halves(p.d)) return launch_one<kDownEdge, false>(g2, grid2, s, !between);
+  if (!fp8 && edge_halves(p.d, kTcBN2)) return launch_one<kDownEdge, false>(g2, grid2, s, !between);
   return fp8 ? launch_one<kGateDown, true>(g2, grid2, s, !between) : launch_one<kGateDown, false>(g2, grid2, s, !between);
 }
 
@@ -1601,7 +1664,7 @@ cudaError_t launch_experts_backward_tc(const Problem& p, const ExpertsBwdArgs& a
     x.beside = beside;
     const int grid = grid_of(p.d, kTcBN2);
     const int ctas = beside && grid > dx_pairs ? dx_pairs : grid;
-    err = edge_halves(p.d) ? launch_one<kDxEdge, false>(x, ctas, s, true) : launch_one<kDx, false>(x, ctas, s, true);
+    err = edge_halves(p.d, kTcBN2) ? launch_one<kDxEdge, false>(x, ctas, s, true) : launch_one<kDx, false>(x, ctas, s, true);
     if (err != cudaSuccess) return err;
   }
   // (last: between the GEMMs its launch and its wait would stand in their way)
