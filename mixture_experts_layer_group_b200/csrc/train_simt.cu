@@ -8,11 +8,13 @@
 //   dW     dW1 = dg^T x, dW3 = du^T x, dW2 = dy^T gh over a group's rows
 //
 // Bound by the FP32 pipes where the rows are many: 8 groups of 512 rows, d 1024,
-// d_ff 1024 take 1390 us (51.5 GFLOP, 37 TFLOP/s) in tiles of 128 x 128 (8 x 8
+// d_ff 1024 take 1345 us (51.5 GFLOP, 38 TFLOP/s) in tiles of 128 x 128 (8 x 8
 // outputs per thread, four 16-byte shared loads for 64 multiply-adds). Few rows
 // leave SMs idle and make long chains of dependent blocks, so small products
 // take 32 x 32 tiles whose sum is split over four groups of threads: 16 groups of
-// 32 rows, d 256, d_ff 512 take 85 us (0.8 GFLOP; 111 us in tiles of 64 x 64).
+// 32 rows, d 256, d_ff 512 take 70 us (0.8 GFLOP; 85 us before the dx product and
+// the weight gradients, which need only dh, ran beside each other; 111 us before
+// that in tiles of 64 x 64).
 #include <cmath>
 #include <type_traits>
 
@@ -93,6 +95,8 @@ template <int kB>
 __global__ void __launch_bounds__(kThreads, 2) dh_simt_kernel(DhParams p) {
   using T = TileOf<kB>;
   __shared__ T sm;
+  griddep_launch_dependents();
+  griddep_wait();
   const int total = p.gr.unit_base[p.gr.N + 1];
   for (int u = blockIdx.x; u < total; u += gridDim.x) {
     int g, f, m;
@@ -148,6 +152,8 @@ template <int kB>
 __global__ void __launch_bounds__(kThreads, 2) dx_simt_kernel(DxParams p) {
   using T = TileOf<kB>;
   __shared__ T sm;
+  griddep_wait();
+  griddep_launch_dependents();  // (only now: the weight gradients read what dx waited for)
   const int total = p.gr.unit_base[p.gr.N + 1];
   for (int u = blockIdx.x; u < total; u += gridDim.x) {
     int g, f, m;
@@ -192,11 +198,14 @@ struct DwParams {
   const int32_t* grp_row0;
   const int32_t* grp_rows;
   int accumulate;
+  int independent;  // runs beside its predecessor, whose own predecessor wrote what it reads
 };
 
 template <class T, int kB>
 __global__ void __launch_bounds__(kThreads, 2) dw_simt_kernel(DwParams p, int units) {
   __shared__ T sm;
+  griddep_launch_dependents();
+  if (!p.independent) griddep_wait();
   for (int u = blockIdx.x; u < units; u += gridDim.x) {
     int i0 = 0, left = u;
     while (i0 < p.nmat - 1 && left >= p.per_group[i0] * p.groups) left -= p.per_group[i0++] * p.groups;
@@ -224,6 +233,7 @@ __global__ void __launch_bounds__(kThreads, 2) dw_simt_kernel(DwParams p, int un
         *o = v;
       }
   }
+  if (p.independent) griddep_wait();  // this grid ends after its predecessor
 }
 
 template <class T, int kB>
@@ -236,8 +246,7 @@ cudaError_t launch_dw_tile(DwParams p, cudaStream_t s) {
   }
   if (units > (1ll << 30)) return cudaErrorInvalidValue;
   const int64_t cap = (int64_t)device_sm_count() * 4;
-  dw_simt_kernel<T, kB><<<(unsigned)(units < cap ? units : cap), kThreads, 0, s>>>(p, (int)units);
-  return cudaGetLastError();
+  return launch_after(dw_simt_kernel<T, kB>, (unsigned)(units < cap ? units : cap), kThreads, 0, s, p, (int)units);
 }
 
 // Tiles of 128 where they fill the GPU, of 64 otherwise. The whole backward with
@@ -279,7 +288,7 @@ cudaError_t launch_dgate_reduce(const float* part, int planes, int64_t rows, flo
 }
 
 // The two row products' tiles: larger ones where they give every SM two of 128 or
-// four of 64. The whole backward with tiles of 128, 64 and 32: 8 groups of 512
+// four of 64. The whole backward (dx before the weight gradients, not beside them) with tiles of 128, 64 and 32: 8 groups of 512
 // rows (d 1024, d_ff 1024) 1390, 1510 and 1680 us, of 128 rows 669, 552 and 484
 // us; 16 groups of 256 rows (d 256, d_ff 512) 361, 257 and 290 us, of 32 rows
 // 234, 111 and 85 us.
@@ -289,17 +298,17 @@ int simt_bwd_tile(const Problem& p) {
   return (p.R + 63) / 64 * (cols / 64) >= 4 * sms ? 64 : SplitTile::kB;
 }
 
-void launch_dh(const DhParams& h, int tile, cudaStream_t s) {
-  const int sms = device_sm_count();
-  if (tile == 128) dh_simt_kernel<128><<<sms * 2, kThreads, 0, s>>>(h);
-  else if (tile == 64) dh_simt_kernel<64><<<sms * 4, kThreads, 0, s>>>(h);
-  else dh_simt_kernel<32><<<sms * 6, kThreads, 0, s>>>(h);
+cudaError_t launch_dh(const DhParams& h, int tile, cudaStream_t s) {
+  const unsigned sms = device_sm_count();
+  if (tile == 128) return launch_after(dh_simt_kernel<128>, sms * 2, kThreads, 0, s, h);
+  if (tile == 64) return launch_after(dh_simt_kernel<64>, sms * 4, kThreads, 0, s, h);
+  return launch_after(dh_simt_kernel<32>, sms * 6, kThreads, 0, s, h);
 }
-void launch_dx(const DxParams& x, int tile, cudaStream_t s) {
-  const int sms = device_sm_count();
-  if (tile == 128) dx_simt_kernel<128><<<sms * 2, kThreads, 0, s>>>(x);
-  else if (tile == 64) dx_simt_kernel<64><<<sms * 4, kThreads, 0, s>>>(x);
-  else dx_simt_kernel<32><<<sms * 6, kThreads, 0, s>>>(x);
+cudaError_t launch_dx(const DxParams& x, int tile, cudaStream_t s) {
+  const unsigned sms = device_sm_count();
+  if (tile == 128) return launch_after(dx_simt_kernel<128>, sms * 2, kThreads, 0, s, x);
+  if (tile == 64) return launch_after(dx_simt_kernel<64>, sms * 4, kThreads, 0, s, x);
+  return launch_after(dx_simt_kernel<32>, sms * 6, kThreads, 0, s, x);
 }
 
 cudaError_t launch_experts_backward_simt(const Problem& p, const ExpertsBwdArgs& a, cudaStream_t s) {
@@ -307,14 +316,11 @@ cudaError_t launch_experts_backward_simt(const Problem& p, const ExpertsBwdArgs&
   const Groups g1{a.unit_base1, a.grp_row0, a.grp_rows, p.N}, g2{a.unit_base2, a.grp_row0, a.grp_rows, p.N};
   DhParams h{g1, (const float*)a.dy_rows, (const float*)a.W2, (const float*)a.gu, a.gate_rows, (float*)a.dg,
              (float*)a.du, (float*)a.gh, a.dgate_rows ? a.dgate_part : nullptr, p.d, p.F, p.R};
-  launch_dh(h, tile, s);
-  cudaError_t e = cudaGetLastError();
-  if (e == cudaSuccess && a.dgate_rows) e = launch_dgate_reduce(a.dgate_part, dgate_planes(p), p.R, a.dgate_rows, s);
+  cudaError_t e = launch_dh(h, tile, s);
   if (e == cudaSuccess && a.dx_rows) {
     DxParams x{g2, (const float*)a.dg, (const float*)a.du, (const float*)a.W1, (const float*)a.W3, (float*)a.dx_rows,
                p.d, p.F, p.F};
-    launch_dx(x, tile, s);
-    e = cudaGetLastError();
+    e = launch_dx(x, tile, s);
   }
   if (e == cudaSuccess && a.dW1) {
     DwParams w{};
@@ -326,8 +332,10 @@ cudaError_t launch_experts_backward_simt(const Problem& p, const ExpertsBwdArgs&
     w.grp_row0 = a.grp_row0;
     w.grp_rows = a.grp_rows;
     w.accumulate = a.accumulate;
+    w.independent = a.dx_rows != nullptr;
     e = launch_dw(w, s);
   }
+  if (e == cudaSuccess && a.dgate_rows) e = launch_dgate_reduce(a.dgate_part, dgate_planes(p), p.R, a.dgate_rows, s);
   return e;
 }
 
@@ -341,8 +349,7 @@ cudaError_t launch_route_products_simt(const Problem& p, const RouteBwdArgs& a, 
   if (a.dx) {
     DxParams x{Groups{a.tables + kRtUnits, row0, rows, 1}, a.dz, nullptr, (const float*)a.W_r, nullptr,
                (float*)a.dx, p.d, p.N, a.ld};
-    launch_dx(x, simt_bwd_tile(one), s);
-    e = cudaGetLastError();
+    e = launch_dx(x, simt_bwd_tile(one), s);
   }
   if (e == cudaSuccess && a.dW_r) {
     const bool split = a.splits > 1;
@@ -353,6 +360,7 @@ cudaError_t launch_route_products_simt(const Problem& p, const RouteBwdArgs& a, 
     w.grp_row0 = a.tables + kRtSplit0;
     w.grp_rows = a.tables + kRtSplitRows;
     w.accumulate = !split && a.accumulate;
+    w.independent = a.dx != nullptr;
     e = launch_dw_tile<MidTile, 64>(w, s);
     if (e == cudaSuccess && split)
       e = launch_join_planes(a.planes, a.splits, (int64_t)p.N * p.d, a.dW_r, a.grad_dtype, a.accumulate, s);
