@@ -469,8 +469,8 @@ MOE_API moe_status moe_ep_reorder(int32_t world, int32_t local_experts, const in
  *   gu [rows, 2 d_ff] out, cfg->dtype, 16-byte aligned: a row's g, then its u
  * Other arguments, workspace and errors as for moe_experts. bf16: h is
  * computed from the unrounded g and u with the hardware exponential (where
- * moe_experts uses the hardware tanh), so y may differ from moe_experts' in
- * its last bit.
+ * moe_experts uses the hardware tanh), and fp32 sums are taken in another order,
+ * so y may differ from moe_experts' in its last bits.
  */
 MOE_API moe_status moe_experts_train(const moe_cfg* cfg, int64_t rows, const int32_t* counts, const void* x_rows,
                                      const float* gate_rows, const void* W1, const void* W3, const void* W2,

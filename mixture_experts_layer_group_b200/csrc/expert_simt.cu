@@ -35,7 +35,6 @@ struct SimtParams {
   float* out_shared;
   int64_t ld_shared;
   const float* gate_perm;
-  float* gu;              // [R, 2 F]: g then u of the routed rows (null: not kept)
 };
 
 template <bool kSwiGLU>
@@ -113,11 +112,6 @@ __global__ void __launch_bounds__(kThreads) expert_gemm_simt_kernel(SimtParams p
         if (kSwiGLU) {
           const float gv = acc0[i][j];
           v = gv / (1.0f + expf(-gv)) * acc1[i][j];
-          if (p.gu && !shared) {
-            float* keep = p.gu + row * 2 * p.ld_routed + (int64_t)f * kBN + c;
-            keep[0] = gv;
-            keep[p.ld_routed] = acc1[i][j];
-          }
         } else {
           v = acc0[i][j] * gate;
         }
@@ -136,7 +130,7 @@ cudaError_t launch_expert_gemms_simt(const Problem& p, const GemmArgs& a, cudaSt
   SimtParams g1{(const float*)a.x_perm, (const float*)a.x, (const float*)a.W1, (const float*)a.W3,
                 (const float*)a.Ws1, (const float*)a.Ws3, a.unit_base1, a.grp_row0, a.grp_rows,
                 p.N, p.d, p.d, p.F, p.nsF, p.F, (float*)a.h_perm, p.F, (float*)a.h_sh, p.nsF,
-                nullptr, (float*)a.gu};
+                nullptr};
   expert_gemm_simt_kernel<true><<<grid, kThreads, 0, s>>>(g1);
   cudaError_t err = cudaGetLastError();
   if (err == cudaSuccess && between) err = cudaEventRecord(between, s);
@@ -144,7 +138,7 @@ cudaError_t launch_expert_gemms_simt(const Problem& p, const GemmArgs& a, cudaSt
   SimtParams g2{(const float*)a.h_perm, (const float*)a.h_sh, (const float*)a.W2, nullptr,
                 (const float*)a.Ws2, nullptr, a.unit_base2, a.grp_row0, a.grp_rows, p.N, p.F, p.nsF,
                 p.d, p.d, p.d, (float*)a.y_rows, p.d, (float*)a.y_rows + p.R * (int64_t)p.d, p.d,
-                a.gate_perm, nullptr};
+                a.gate_perm};
   expert_gemm_simt_kernel<false><<<grid, kThreads, 0, s>>>(g2);
   return cudaGetLastError();
 }

@@ -577,7 +577,9 @@ static moe_status experts_device(const moe_cfg* cfg, int64_t rows, const int32_t
   db.unit_base1 = at<int32_t>(ws, L.unit_base1);
   db.unit_base2 = at<int32_t>(ws, L.unit_base2);
   const bool tc = p.dtype == MOE_BF16;
-  e = launch_group_tables(p, counts, db, tc ? kTcBM : kSimtBM, tc ? kTcBN1 : kSimtBN, tc ? kTcBN2 : kSimtBN,
+  const int bs = gu ? simt_tile(p) : kSimtBM;  // fp32
+  static_assert(kSimtBM == kSimtBN, "square tiles");
+  e = launch_group_tables(p, counts, db, tc ? kTcBM : bs, tc ? kTcBN1 : simt_cols(bs), tc ? kTcBN2 : simt_cols(bs),
                           at<int>(ws, L.sched), s);
   if (e != cudaSuccess) return cuda_fail(e);
   GemmArgs ga;
@@ -599,7 +601,8 @@ static moe_status experts_device(const moe_cfg* cfg, int64_t rows, const int32_t
   ga.sched = at<int>(ws, L.sched);
   ga.sched_clear = true;
   ga.gu = gu;
-  e = tc ? launch_expert_gemms_tc(p, ga, s, nullptr) : launch_expert_gemms_simt(p, ga, s, nullptr);
+  e = tc ? launch_expert_gemms_tc(p, ga, s, nullptr)
+         : gu ? launch_experts_train_simt(p, ga, s) : launch_expert_gemms_simt(p, ga, s, nullptr);
   if (e == cudaSuccess) e = note_device_use(ws, s);
   return e == cudaSuccess ? MOE_OK : cuda_fail(e);
 }

@@ -2,9 +2,10 @@
 // with operands contiguous along either index, for the layers stored in fp32
 // (tensor cores would round the operands to TF32). 256 threads.
 //
-// Each output is one chain of fused multiply-adds over ascending k, whatever
-// the tile (SplitTile excepted: four chains, added in order), so a result does
-// not depend on the tile that computed it.
+// Sums are taken in two levels: chains of kChain fused multiply-adds over
+// ascending k, and the chains' sums added up in order. One chain of 4096 terms is
+// off by about 1.2e-6 of the result; in two levels 3e-7. The order depends on
+// the tile's shape alone, so results are the same each time.
 #pragma once
 
 #include "common.cuh"
@@ -13,6 +14,7 @@ namespace moe {
 namespace simt {
 
 constexpr int kThreads = 256;
+constexpr int kChain = 128;
 
 // A strided operand: element (r, k) at p[r * rs + k * ks] for r < rows and
 // k < len, zero elsewhere. One of the strides is 1, the other and the bound
@@ -27,13 +29,14 @@ struct Operand {
 // Column r of row k in a [k][rows] block: the 16-byte column groups of row k
 // are permuted by k / 4, so that the four rows a k-contiguous vector is spread
 // over, and the reads along a row, fall on different banks.
-MOE_DEV int swz(int k, int r) { return r ^ (((k >> 2) & 7) << 2); }
+template <int ROWS>
+MOE_DEV int swz(int k, int r) { return r ^ (((k >> 2) & (ROWS >= 32 ? 7 : ROWS / 4 - 1)) << 2); }
 
 // A ROWS x BK block of an operand: global to registers, registers to [k][r].
 template <int ROWS, int BK>
 struct Block {
-  static constexpr int kVecs = ROWS * BK / 4 / kThreads;
-  static_assert(kVecs * kThreads * 4 == ROWS * BK, "whole vectors per thread");
+  static constexpr int kAll = ROWS * BK / 4, kVecs = kAll < kThreads ? 1 : kAll / kThreads;
+  static_assert(kAll < kThreads || kVecs * kThreads == kAll, "whole vectors per thread");
   float4 v[kVecs];
   MOE_DEV void fetch(const Operand& o, int r0, int k0) {
 #pragma unroll
@@ -41,7 +44,7 @@ struct Block {
       const int t = threadIdx.x + i * kThreads;
       const int r = r0 + (o.ks == 1 ? t / (BK / 4) : t % (ROWS / 4) * 4);
       const int k = k0 + (o.ks == 1 ? t % (BK / 4) * 4 : t / (ROWS / 4));
-      v[i] = r < o.rows && k < o.len ? __ldg(reinterpret_cast<const float4*>(o.p + r * o.rs + k * o.ks))
+      v[i] = t < kAll && r < o.rows && k < o.len ? __ldg(reinterpret_cast<const float4*>(o.p + r * o.rs + k * o.ks))
                                      : make_float4(0.f, 0.f, 0.f, 0.f);
     }
   }
@@ -49,34 +52,96 @@ struct Block {
 #pragma unroll
     for (int i = 0; i < kVecs; ++i) {
       const int t = threadIdx.x + i * kThreads;
+      if (t >= kAll) break;
       if (along_k) {
         const int r = t / (BK / 4), k = t % (BK / 4) * 4;
-        sm[k][swz(k, r)] = v[i].x;
-        sm[k + 1][swz(k, r)] = v[i].y;
-        sm[k + 2][swz(k, r)] = v[i].z;
-        sm[k + 3][swz(k, r)] = v[i].w;
+        sm[k][swz<ROWS>(k, r)] = v[i].x;
+        sm[k + 1][swz<ROWS>(k, r)] = v[i].y;
+        sm[k + 2][swz<ROWS>(k, r)] = v[i].z;
+        sm[k + 3][swz<ROWS>(k, r)] = v[i].w;
       } else {
         const int r = t % (ROWS / 4) * 4, k = t / (ROWS / 4);
-        *reinterpret_cast<float4*>(&sm[k][swz(k, r)]) = v[i];
+        *reinterpret_cast<float4*>(&sm[k][swz<ROWS>(k, r)]) = v[i];
       }
     }
   }
 };
 
+// What a thread has summed: the running chain, and the chains before it, in
+// registers or, for tiles whose chain takes 64 of them, in shared memory (each
+// thread its own column).
+template <int TM, int TN, bool kRegs = (TM * TN <= 16)>
+struct Sum {
+  float v[TM][TN] = {};
+  float t[TM][TN] = {};
+  bool any = false;
+  MOE_DEV void flush(float4 (*)[kThreads]) {
+    any = true;
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+      for (int j = 0; j < TN; ++j) {
+        t[i][j] += v[i][j];
+        v[i][j] = 0.f;
+      }
+  }
+  MOE_DEV void total(float4 (*)[kThreads]) {
+    if (any) flush(nullptr);
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+      for (int j = 0; j < TN; ++j) v[i][j] = any ? t[i][j] : v[i][j];
+  }
+};
+template <int TM, int TN>
+struct Sum<TM, TN, false> {
+  float v[TM][TN] = {};
+  bool any = false;
+  MOE_DEV void flush(float4 (*t)[kThreads]) {
+    add(t);
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+      for (int j = 0; j < TN; j += 4) {
+        t[(i * TN + j) / 4][threadIdx.x] = make_float4(v[i][j], v[i][j + 1], v[i][j + 2], v[i][j + 3]);
+        v[i][j] = v[i][j + 1] = v[i][j + 2] = v[i][j + 3] = 0.f;
+      }
+    any = true;
+  }
+  MOE_DEV void total(float4 (*t)[kThreads]) { add(t); }
+
+ private:
+  MOE_DEV void add(float4 (*t)[kThreads]) {
+    if (!any) return;
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+      for (int j = 0; j < TN; j += 4) {
+        const float4 w = t[(i * TN + j) / 4][threadIdx.x];
+        v[i][j] = w.x + v[i][j];
+        v[i][j + 1] = w.y + v[i][j + 1];
+        v[i][j + 2] = w.z + v[i][j + 2];
+        v[i][j + 3] = w.w + v[i][j + 3];
+      }
+  }
+};
+
 // Thread (tx, ty) of 16 x 16 holds rows 4 ty + 64 i + 0..3 and columns 4 tx + 64
-// j + 0..3 of a BM x BN tile, in acc[4 i + ..][4 j + ..].
+// j + 0..3 of a BM x BN tile, in v[4 i + ..][4 j + ..].
 template <int BM, int BN, int BK>
 struct Tile {
   static constexpr int kTM = BM / 16, kTN = BN / 16;
+  using Acc = Sum<kTM, kTN>;
   float a[2][BK][BM];
   float b[2][BK][BN];
+  float4 chains[kTM * kTN <= 16 ? 1 : kTM * kTN / 4][kThreads];
 
   MOE_DEV static int row(int i) { return 4 * ((int)threadIdx.x >> 4) + 64 * (i / 4) + i % 4; }
   MOE_DEV static int col(int j) { return 4 * ((int)threadIdx.x & 15) + 64 * (j / 4) + j % 4; }
 
   // acc += the products over k < K; the next block's loads are in flight while
   // one is multiplied
-  MOE_DEV void run(const Operand& A, int m0, const Operand& B, int n0, int K, float (&acc)[kTM][kTN]) {
+  MOE_DEV void run(const Operand& A, int m0, const Operand& B, int n0, int K, Acc& acc) {
     if (K <= 0) return;
     Block<BM, BK> va;
     Block<BN, BK> vb;
@@ -98,85 +163,100 @@ struct Tile {
         float x[kTM], y[kTN];
 #pragma unroll
         for (int i = 0; i < kTM; i += 4)
-          *reinterpret_cast<float4*>(x + i) = *reinterpret_cast<const float4*>(&a[buf][kk][swz(kk, row(i))]);
+          *reinterpret_cast<float4*>(x + i) = *reinterpret_cast<const float4*>(&a[buf][kk][swz<BM>(kk, row(i))]);
 #pragma unroll
         for (int j = 0; j < kTN; j += 4)
-          *reinterpret_cast<float4*>(y + j) = *reinterpret_cast<const float4*>(&b[buf][kk][swz(kk, col(j))]);
+          *reinterpret_cast<float4*>(y + j) = *reinterpret_cast<const float4*>(&b[buf][kk][swz<BN>(kk, col(j))]);
 #pragma unroll
         for (int i = 0; i < kTM; ++i)
 #pragma unroll
-          for (int j = 0; j < kTN; ++j) acc[i][j] = fmaf(x[i], y[j], acc[i][j]);
+          for (int j = 0; j < kTN; ++j) acc.v[i][j] = fmaf(x[i], y[j], acc.v[i][j]);
       }
       if (more) {
         va.put(a[buf ^ 1], A.ks == 1);
         vb.put(b[buf ^ 1], B.ks == 1);
       }
+      if ((k0 + BK) % kChain == 0) acc.flush(chains);
     }
   }
+  MOE_DEV void finish(Acc& acc) { acc.total(chains); }
 };
 
-// A 32 x 32 tile for groups of few rows: four groups of 64 threads each take a
-// quarter of every 64-deep block, so a tile's chain over k is four times
-// shorter and a small product spreads over more threads.
+// A tile of BM (8 or 32) x 32 for groups of few rows: kGroups groups of threads
+// each take their part of every 64-deep block, so a tile's chain over k is as
+// much shorter and a small product spreads over more threads. Such products wait
+// for memory more than they compute, so two blocks are in flight (three
+// spill: 32 rows of 256 x 512 matrices 78 instead of 70 us).
+template <int BM>
 struct SplitTile {
-  static constexpr int kB = 32, kBK = 64, kGroups = 4;
+  static constexpr int kCols = 32, kBK = 64, kAhead = 2;
+  static constexpr int kPart = BM / 4 * (kCols / 4), kGroups = kThreads / kPart;  // threads of a group, groups
+  using Acc = Sum<4, 4>;
   union {
     struct {
-      float a[2][kBK][kB];
-      float b[2][kBK][kB];
+      float a[2][kBK][BM];
+      float b[2][kBK][kCols];
     };
-    float sum[kGroups][kB][kB];
+    float sum[kGroups][BM][kCols];
   };
-  // After finish(), thread t holds row t / 8, columns 4 (t % 8) + 0..3.
+  // After finish(), thread t holds row t / 8 (none at or past BM), columns 4 (t % 8) + 0..3.
   MOE_DEV static int row() { return threadIdx.x / 8; }
   MOE_DEV static int col() { return threadIdx.x % 8 * 4; }
 
-  MOE_DEV void run(const Operand& A, int m0, const Operand& B, int n0, int K, float (&acc)[4][4]) {
+  MOE_DEV void run(const Operand& A, int m0, const Operand& B, int n0, int K, Acc& acc) {
     if (K <= 0) return;
-    const int t = threadIdx.x & 63, g = threadIdx.x >> 6, tx = t & 7, ty = t >> 3;
-    Block<kB, kBK> va, vb;
-    va.fetch(A, m0, 0);
-    vb.fetch(B, n0, 0);
-    __syncthreads();
-    va.put(a[0], A.ks == 1);
-    vb.put(b[0], B.ks == 1);
+    const int t = threadIdx.x % kPart, g = threadIdx.x / kPart, tx = t & 7, ty = t >> 3;
+    Block<BM, kBK> va[kAhead];
+    Block<kCols, kBK> vb[kAhead];
+#pragma unroll
+    for (int s = 0; s < kAhead; ++s) {  // (past K: zeros)
+      va[s].fetch(A, m0, s * kBK);
+      vb[s].fetch(B, n0, s * kBK);
+    }
+    __syncthreads();  // the buffers' last readers are done
     int buf = 0;
-    for (int k0 = 0; k0 < K; k0 += kBK, buf ^= 1) {
-      __syncthreads();
-      const bool more = k0 + kBK < K;
-      if (more) {
-        va.fetch(A, m0, k0 + kBK);
-        vb.fetch(B, n0, k0 + kBK);
-      }
+    for (int k1 = 0; k1 < K; k1 += kAhead * kBK) {
 #pragma unroll
-      for (int q = 0; q < kBK / kGroups; ++q) {
-        const int kk = g * (kBK / kGroups) + q;
-        float x[4], y[4];
-        *reinterpret_cast<float4*>(x) = *reinterpret_cast<const float4*>(&a[buf][kk][swz(kk, 4 * ty)]);
-        *reinterpret_cast<float4*>(y) = *reinterpret_cast<const float4*>(&b[buf][kk][swz(kk, 4 * tx)]);
+      for (int s = 0; s < kAhead; ++s, buf ^= 1) {
+        const int k0 = k1 + s * kBK;
+        if (k0 >= K) break;
+        va[s].put(a[buf], A.ks == 1);
+        vb[s].put(b[buf], B.ks == 1);
+        if (k0 + kAhead * kBK < K) {
+          va[s].fetch(A, m0, k0 + kAhead * kBK);
+          vb[s].fetch(B, n0, k0 + kAhead * kBK);
+        }
+        __syncthreads();  // (the other buffer is read no longer, either)
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int q = 0; q < kBK / kGroups; ++q) {
+          const int kk = g * (kBK / kGroups) + q;
+          float x[4], y[4];
+          *reinterpret_cast<float4*>(x) = *reinterpret_cast<const float4*>(&a[buf][kk][swz<BM>(kk, 4 * ty)]);
+          *reinterpret_cast<float4*>(y) = *reinterpret_cast<const float4*>(&b[buf][kk][swz<kCols>(kk, 4 * tx)]);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(x[i], y[j], acc[i][j]);
-      }
-      if (more) {
-        va.put(a[buf ^ 1], A.ks == 1);
-        vb.put(b[buf ^ 1], B.ks == 1);
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) acc.v[i][j] = fmaf(x[i], y[j], acc.v[i][j]);
+        }
+        if ((k0 / kBK + 1) % (kChain / (kBK / kGroups)) == 0) acc.flush(nullptr);
       }
     }
   }
   // The four groups' sums, in order, as this thread's part of the tile.
-  MOE_DEV void finish(const float (&acc)[4][4], float (&out)[4]) {
-    const int t = threadIdx.x & 63, g = threadIdx.x >> 6, tx = t & 7, ty = t >> 3;
+  MOE_DEV void finish(Acc& acc, float (&out)[4]) {
+    const int t = threadIdx.x % kPart, g = threadIdx.x / kPart, tx = t & 7, ty = t >> 3;
+    acc.total(nullptr);
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      *reinterpret_cast<float4*>(&sum[g][4 * ty + i][4 * tx]) = make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
+      *reinterpret_cast<float4*>(&sum[g][4 * ty + i][4 * tx]) =
+          make_float4(acc.v[i][0], acc.v[i][1], acc.v[i][2], acc.v[i][3]);
     __syncthreads();
 #pragma unroll
     for (int j = 0; j < 4; ++j) out[j] = 0.f;
 #pragma unroll
     for (int q = 0; q < kGroups; ++q) {
+      if (row() >= BM) break;
       const float4 v = *reinterpret_cast<const float4*>(&sum[q][row()][col()]);
       out[0] += v.x;
       out[1] += v.y;

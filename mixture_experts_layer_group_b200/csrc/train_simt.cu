@@ -29,8 +29,24 @@ using simt::Operand;
 using simt::SplitTile;
 using BigTile = simt::Tile<128, 128, 16>;
 using MidTile = simt::Tile<64, 64, 32>;
+// Tiles by their rows: 128, 64, or split ones of 32 or 8 rows and 32 columns.
+__host__ __device__ constexpr bool is_split(int rows) { return rows <= 32; }
 template <int B>
-using TileOf = std::conditional_t<B == 128, BigTile, std::conditional_t<B == 64, MidTile, SplitTile>>;
+using TileOf = std::conditional_t<B == 128, BigTile, std::conditional_t<B == 64, MidTile, SplitTile<B < 32 ? 8 : 32>>>;
+
+template <class T>
+MOE_DEV T& tile_smem() {
+  extern __shared__ float4 simt_smem[];
+  return *reinterpret_cast<T*>(simt_smem);
+}
+template <class T, class... Params, class... Args>
+cudaError_t launch_tile(void (*kernel)(Params...), unsigned blocks, cudaStream_t s, const Args&... args) {
+  if (sizeof(T) > 48 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(T));
+    if (e != cudaSuccess) return e;
+  }
+  return launch_after(kernel, blocks, kThreads, sizeof(T), s, args...);
+}
 
 struct Groups {
   const int32_t* unit_base;
@@ -94,7 +110,8 @@ MOE_DEV float dh_quad(const DhParams& p, int64_t row, int c, const float* q, flo
 template <int kB>
 __global__ void __launch_bounds__(kThreads, 2) dh_simt_kernel(DhParams p) {
   using T = TileOf<kB>;
-  __shared__ T sm;
+  constexpr int kBN = simt_cols(kB);
+  T& sm = tile_smem<T>();
   griddep_launch_dependents();
   griddep_wait();
   const int total = p.gr.unit_base[p.gr.N + 1];
@@ -105,9 +122,10 @@ __global__ void __launch_bounds__(kThreads, 2) dh_simt_kernel(DhParams p) {
     const int64_t row0 = p.gr.grp_row0[g];
     const Operand A{p.dy + row0 * p.d, p.d, 1, rows, p.d}, B{p.W2 + (int64_t)g * p.d * p.F, 1, p.F, p.F, p.d};
     float* part = p.part ? p.part + (int64_t)f * p.R + row0 : nullptr;
-    if constexpr (kB > SplitTile::kB) {
-      float acc[T::kTM][T::kTN] = {};
-      sm.run(A, m * kB, B, f * kB, p.d, acc);
+    if constexpr (!is_split(kB)) {
+      typename T::Acc acc;
+      sm.run(A, m * kB, B, f * kBN, p.d, acc);
+      sm.finish(acc);
 #pragma unroll
       for (int i = 0; i < T::kTM; ++i) {
         const int r = m * kB + T::row(i);
@@ -117,24 +135,87 @@ __global__ void __launch_bounds__(kThreads, 2) dh_simt_kernel(DhParams p) {
         if (in)
 #pragma unroll
           for (int j = 0; j < T::kTN; j += 4)
-            dgate += dh_quad(p, row0 + r, f * kB + T::col(j), &acc[i][j], gate);
+            dgate += dh_quad(p, row0 + r, f * kBN + T::col(j), &acc.v[i][j], gate);
 #pragma unroll
         for (int off = 8; off > 0; off >>= 1) dgate += __shfl_xor_sync(0xffffffffu, dgate, off);
         if (part && in && (threadIdx.x & 15) == 0) part[r] = dgate;
       }
     } else {
-      float acc[4][4] = {}, q[4];
-      sm.run(A, m * kB, B, f * kB, p.d, acc);
+      typename T::Acc acc;
+      float q[4];
+      sm.run(A, m * kB, B, f * kBN, p.d, acc);
       sm.finish(acc, q);
-      const int r = m * kB + SplitTile::row();
-      const bool in = r < rows;
+      const int r = m * kB + T::row();
+      const bool in = T::row() < kB && r < rows;
       const float gate = in && p.gate ? p.gate[row0 + r] : 1.f;
-      float dgate = in ? dh_quad(p, row0 + r, f * kB + SplitTile::col(), q, gate) : 0.f;
+      float dgate = in ? dh_quad(p, row0 + r, f * kBN + T::col(), q, gate) : 0.f;
 #pragma unroll
       for (int off = 4; off > 0; off >>= 1) dgate += __shfl_xor_sync(0xffffffffu, dgate, off);
       if (part && in && (threadIdx.x & 7) == 0) part[r] = dgate;
     }
   }
+}
+
+// out[r][c] = gate_r sum_k A[r][k] B[c][k]: g and u of the training forward (B = W1
+// and W3, halves of gu), and its down product.
+struct FwdParams {
+  Groups gr;
+  const float* A;    // [R, K]
+  const float* B0;   // [N, cols, K]
+  const float* B1;   // a second such matrix, or null
+  const float* gate; // [R] or null
+  float* out;        // [R, cols], or [R, 2 cols]
+  int K, cols;
+};
+
+template <int kB>
+__global__ void __launch_bounds__(kThreads, 2) fwd_simt_kernel(FwdParams p) {
+  using T = TileOf<kB>;
+  constexpr int kBN = simt_cols(kB);
+  T& sm = tile_smem<T>();
+  griddep_launch_dependents();
+  griddep_wait();
+  const int mats = p.B1 ? 2 : 1, total = p.gr.unit_base[p.gr.N + 1] * mats;
+  const int64_t ldo = (int64_t)p.cols * mats;
+  for (int u = blockIdx.x; u < total; u += gridDim.x) {
+    int g, f, m;
+    find_unit(p.gr, kB, u / mats, g, f, m);
+    const int which = u % mats, rows = p.gr.grp_rows[g];
+    const int64_t row0 = p.gr.grp_row0[g];
+    const float* B = (which ? p.B1 : p.B0) + (int64_t)g * p.cols * p.K;
+    typename T::Acc acc;
+    sm.run(Operand{p.A + row0 * p.K, p.K, 1, rows, p.K}, m * kB, Operand{B, p.K, 1, p.cols, p.K}, f * kBN, p.K, acc);
+    auto put = [&](int r, int c, const float* v) {  // four columns (their number is a multiple of 8)
+      if (r >= rows || c >= p.cols) return;
+      const float gate = p.gate ? p.gate[row0 + r] : 1.f;
+      *reinterpret_cast<float4*>(p.out + (row0 + r) * ldo + which * p.cols + c) =
+          make_float4(gate * v[0], gate * v[1], gate * v[2], gate * v[3]);
+    };
+    if constexpr (!is_split(kB)) {
+      sm.finish(acc);
+#pragma unroll
+      for (int i = 0; i < T::kTM; ++i)
+#pragma unroll
+        for (int j = 0; j < T::kTN; j += 4) put(m * kB + T::row(i), f * kBN + T::col(j), &acc.v[i][j]);
+    } else {
+      float v[4];
+      sm.finish(acc, v);
+      if (T::row() < kB) put(m * kB + T::row(), f * kBN + T::col(), v);
+    }
+  }
+}
+
+// h = silu(g) u, four features per thread.
+__global__ void __launch_bounds__(256) swiglu_kernel(const float* __restrict__ gu, int F, int64_t vecs, float* __restrict__ h) {
+  griddep_launch_dependents();
+  griddep_wait();
+  const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
+  if (i >= vecs) return;
+  const int64_t r = i / (F / 4), c = i % (F / 4) * 4;
+  const float4 g = *reinterpret_cast<const float4*>(gu + r * 2 * F + c);
+  const float4 u = *reinterpret_cast<const float4*>(gu + r * 2 * F + F + c);
+  auto act = [](float a, float b) { return a / (1.f + expf(-a)) * b; };
+  *reinterpret_cast<float4*>(h + r * F + c) = make_float4(act(g.x, u.x), act(g.y, u.y), act(g.z, u.z), act(g.w, u.w));
 }
 
 struct DxParams {
@@ -151,7 +232,8 @@ struct DxParams {
 template <int kB>
 __global__ void __launch_bounds__(kThreads, 2) dx_simt_kernel(DxParams p) {
   using T = TileOf<kB>;
-  __shared__ T sm;
+  constexpr int kBN = simt_cols(kB);
+  T& sm = tile_smem<T>();
   griddep_wait();
   griddep_launch_dependents();  // (only now: the weight gradients read what dx waited for)
   const int total = p.gr.unit_base[p.gr.N + 1];
@@ -160,25 +242,26 @@ __global__ void __launch_bounds__(kThreads, 2) dx_simt_kernel(DxParams p) {
     find_unit(p.gr, kB, u, g, f, m);
     const int rows = p.gr.grp_rows[g];
     const int64_t row0 = p.gr.grp_row0[g], w0 = (int64_t)g * p.F * p.d;
-    float acc[kB == 128 ? 8 : 4][kB == 128 ? 8 : 4] = {};
-    sm.run(Operand{p.d0 + row0 * p.ld, p.ld, 1, rows, (int)p.ld}, m * kB, Operand{p.W0 + w0, 1, p.d, p.d, p.F}, f * kB,
+    typename T::Acc acc;
+    sm.run(Operand{p.d0 + row0 * p.ld, p.ld, 1, rows, (int)p.ld}, m * kB, Operand{p.W0 + w0, 1, p.d, p.d, p.F}, f * kBN,
            p.F, acc);
     if (p.d1)
       sm.run(Operand{p.d1 + row0 * p.ld, p.ld, 1, rows, (int)p.ld}, m * kB, Operand{p.W1 + w0, 1, p.d, p.d, p.F},
-             f * kB, p.F, acc);
+             f * kBN, p.F, acc);
     auto put = [&](int r, int c, const float* v) {  // four columns (d is a multiple of 8)
       if (r < rows && c < p.d)
         *reinterpret_cast<float4*>(p.dx + (row0 + r) * p.d + c) = make_float4(v[0], v[1], v[2], v[3]);
     };
-    if constexpr (kB > SplitTile::kB) {
+    if constexpr (!is_split(kB)) {
+      sm.finish(acc);
 #pragma unroll
       for (int i = 0; i < T::kTM; ++i)
 #pragma unroll
-        for (int j = 0; j < T::kTN; j += 4) put(m * kB + T::row(i), f * kB + T::col(j), &acc[i][j]);
+        for (int j = 0; j < T::kTN; j += 4) put(m * kB + T::row(i), f * kBN + T::col(j), &acc.v[i][j]);
     } else {
       float v[4];
       sm.finish(acc, v);
-      put(m * kB + SplitTile::row(), f * kB + SplitTile::col(), v);
+      if (T::row() < kB) put(m * kB + T::row(), f * kBN + T::col(), v);
     }
   }
 }
@@ -203,7 +286,7 @@ struct DwParams {
 
 template <class T, int kB>
 __global__ void __launch_bounds__(kThreads, 2) dw_simt_kernel(DwParams p, int units) {
-  __shared__ T sm;
+  T& sm = tile_smem<T>();
   griddep_launch_dependents();
   if (!p.independent) griddep_wait();
   for (int u = blockIdx.x; u < units; u += gridDim.x) {
@@ -215,9 +298,10 @@ __global__ void __launch_bounds__(kThreads, 2) dw_simt_kernel(DwParams p, int un
     const int m0 = mi * kB, n0 = (local - mi * nt) * kB;
     const int64_t row0 = p.grp_row0[g];
     const int rows = p.grp_rows[g];
-    float acc[T::kTM][T::kTN] = {};
+    typename T::Acc acc;
     sm.run(Operand{x.A + row0 * x.lda, 1, x.lda, (int)x.lda, rows}, m0, Operand{x.B + row0 * x.N, 1, x.N, x.N, rows}, n0,
            rows, acc);
+    sm.finish(acc);
 #pragma unroll
     for (int i = 0; i < T::kTM; ++i)
 #pragma unroll
@@ -225,7 +309,7 @@ __global__ void __launch_bounds__(kThreads, 2) dw_simt_kernel(DwParams p, int un
         const int m = m0 + T::row(i), n = n0 + T::col(j);
         if (m >= x.M || n >= x.N) continue;  // N is a multiple of 8: four columns are in or out
         float4* o = reinterpret_cast<float4*>(x.out + ((int64_t)g * x.M + m) * x.N + n);
-        float4 v = make_float4(acc[i][j], acc[i][j + 1], acc[i][j + 2], acc[i][j + 3]);
+        float4 v = make_float4(acc.v[i][j], acc.v[i][j + 1], acc.v[i][j + 2], acc.v[i][j + 3]);
         if (p.accumulate) {
           const float4 w = *o;
           v = make_float4(w.x + v.x, w.y + v.y, w.z + v.z, w.w + v.w);
@@ -246,7 +330,7 @@ cudaError_t launch_dw_tile(DwParams p, cudaStream_t s) {
   }
   if (units > (1ll << 30)) return cudaErrorInvalidValue;
   const int64_t cap = (int64_t)device_sm_count() * 4;
-  return launch_after(dw_simt_kernel<T, kB>, (unsigned)(units < cap ? units : cap), kThreads, 0, s, p, (int)units);
+  return launch_tile<T>(dw_simt_kernel<T, kB>, (unsigned)(units < cap ? units : cap), s, p, (int)units);
 }
 
 // Tiles of 128 where they fill the GPU, of 64 otherwise. The whole backward with
@@ -292,27 +376,52 @@ cudaError_t launch_dgate_reduce(const float* part, int planes, int64_t rows, flo
 // rows (d 1024, d_ff 1024) 1390, 1510 and 1680 us, of 128 rows 669, 552 and 484
 // us; 16 groups of 256 rows (d 256, d_ff 512) 361, 257 and 290 us, of 32 rows
 // 234, 111 and 85 us.
-int simt_bwd_tile(const Problem& p) {
+int simt_tile(const Problem& p) {
   const int64_t cols = p.d + p.F, sms = device_sm_count();
   if ((p.R + 127) / 128 * (cols / 128) >= 2 * sms) return 128;
-  return (p.R + 63) / 64 * (cols / 64) >= 4 * sms ? 64 : SplitTile::kB;
+  if ((p.R + 63) / 64 * (cols / 64) >= 4 * sms) return 64;
+  return p.R <= 8 * (int64_t)p.N ? 8 : 32;
 }
 
 cudaError_t launch_dh(const DhParams& h, int tile, cudaStream_t s) {
   const unsigned sms = device_sm_count();
-  if (tile == 128) return launch_after(dh_simt_kernel<128>, sms * 2, kThreads, 0, s, h);
-  if (tile == 64) return launch_after(dh_simt_kernel<64>, sms * 4, kThreads, 0, s, h);
-  return launch_after(dh_simt_kernel<32>, sms * 6, kThreads, 0, s, h);
+  if (tile == 128) return launch_tile<TileOf<128>>(dh_simt_kernel<128>, sms * 2, s, h);
+  if (tile == 64) return launch_tile<TileOf<64>>(dh_simt_kernel<64>, sms * 4, s, h);
+  if (tile == 32) return launch_tile<TileOf<32>>(dh_simt_kernel<32>, sms * 6, s, h);
+  return launch_tile<TileOf<8>>(dh_simt_kernel<8>, sms * 6, s, h);
 }
 cudaError_t launch_dx(const DxParams& x, int tile, cudaStream_t s) {
   const unsigned sms = device_sm_count();
-  if (tile == 128) return launch_after(dx_simt_kernel<128>, sms * 2, kThreads, 0, s, x);
-  if (tile == 64) return launch_after(dx_simt_kernel<64>, sms * 4, kThreads, 0, s, x);
-  return launch_after(dx_simt_kernel<32>, sms * 6, kThreads, 0, s, x);
+  if (tile == 128) return launch_tile<TileOf<128>>(dx_simt_kernel<128>, sms * 2, s, x);
+  if (tile == 64) return launch_tile<TileOf<64>>(dx_simt_kernel<64>, sms * 4, s, x);
+  if (tile == 32) return launch_tile<TileOf<32>>(dx_simt_kernel<32>, sms * 6, s, x);
+  return launch_tile<TileOf<8>>(dx_simt_kernel<8>, sms * 6, s, x);
+}
+
+cudaError_t launch_fwd(const FwdParams& f, int tile, cudaStream_t s) {
+  const unsigned sms = device_sm_count();
+  if (tile == 128) return launch_tile<TileOf<128>>(fwd_simt_kernel<128>, sms * 2, s, f);
+  if (tile == 64) return launch_tile<TileOf<64>>(fwd_simt_kernel<64>, sms * 4, s, f);
+  if (tile == 32) return launch_tile<TileOf<32>>(fwd_simt_kernel<32>, sms * 6, s, f);
+  return launch_tile<TileOf<8>>(fwd_simt_kernel<8>, sms * 6, s, f);
+}
+
+cudaError_t launch_experts_train_simt(const Problem& p, const GemmArgs& a, cudaStream_t s) {
+  const int tile = simt_tile(p);
+  const Groups g1{a.unit_base1, a.grp_row0, a.grp_rows, p.N}, g2{a.unit_base2, a.grp_row0, a.grp_rows, p.N};
+  cudaError_t e = launch_fwd(FwdParams{g1, (const float*)a.x_perm, (const float*)a.W1, (const float*)a.W3, nullptr,
+                                       (float*)a.gu, p.d, p.F}, tile, s);
+  const int64_t vecs = p.R * (int64_t)(p.F / 4);
+  if (e == cudaSuccess)
+    e = launch_after(swiglu_kernel, (unsigned)((vecs + 255) / 256), 256, 0, s, (const float*)a.gu, p.F, vecs,
+                     (float*)a.h_perm);
+  if (e != cudaSuccess) return e;
+  return launch_fwd(FwdParams{g2, (const float*)a.h_perm, (const float*)a.W2, nullptr, a.gate_perm,
+                              (float*)a.y_rows, p.F, p.d}, tile, s);
 }
 
 cudaError_t launch_experts_backward_simt(const Problem& p, const ExpertsBwdArgs& a, cudaStream_t s) {
-  const int tile = simt_bwd_tile(p);
+  const int tile = simt_tile(p);
   const Groups g1{a.unit_base1, a.grp_row0, a.grp_rows, p.N}, g2{a.unit_base2, a.grp_row0, a.grp_rows, p.N};
   DhParams h{g1, (const float*)a.dy_rows, (const float*)a.W2, (const float*)a.gu, a.gate_rows, (float*)a.dg,
              (float*)a.du, (float*)a.gh, a.dgate_rows ? a.dgate_part : nullptr, p.d, p.F, p.R};
@@ -344,12 +453,13 @@ cudaError_t launch_route_products_simt(const Problem& p, const RouteBwdArgs& a, 
   const int32_t* rows = a.tables + kRtRows;
   Problem one = p;  // one group of T rows
   one.F = p.d;
+  one.N = 1;
   one.R = p.T;
   cudaError_t e = cudaSuccess;
   if (a.dx) {
     DxParams x{Groups{a.tables + kRtUnits, row0, rows, 1}, a.dz, nullptr, (const float*)a.W_r, nullptr,
                (float*)a.dx, p.d, p.N, a.ld};
-    e = launch_dx(x, simt_bwd_tile(one), s);
+    e = launch_dx(x, simt_tile(one), s);
   }
   if (e == cudaSuccess && a.dW_r) {
     const bool split = a.splits > 1;

@@ -210,7 +210,8 @@ def test_experts_train_forward(counts, d, F, dtype):
             assert rel(gu[r], torch.cat([g, u], 1)) <= BF16_ONE
             assert rel(y[r], ref) <= BF16_TWO
     if dtype == "f32":
-        assert torch.equal(y, plain)
+        # the same sums in another order, each within the bound above of the exact ones
+        assert rel(y, plain.double()) <= 2 * (d + F + 16) * 2.0 ** -23
     else:
         assert rel(y, plain) <= 2 * BF16_TWO
 
