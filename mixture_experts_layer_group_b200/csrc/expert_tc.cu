@@ -1590,7 +1590,7 @@ int dh_tile(const Problem& p) {
 }
 
 int dgate_planes(const Problem& p) {
-  const int cols = p.dtype == MOE_BF16 ? 32 : simt_cols(simt_tile(p));
+  const int cols = p.dtype == MOE_BF16 ? 32 : simt_cols(simt_bwd_tile(p));
   return (p.F + cols - 1) / cols;
 }
 

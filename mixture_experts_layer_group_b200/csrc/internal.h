@@ -232,7 +232,8 @@ struct WgradArgs {
 };
 cudaError_t launch_wgrad_tc(const WgradArgs& a, cudaStream_t s);
 int dgate_planes(const Problem& p);
-int simt_tile(const Problem& p);  // training in fp32: rows of a tile of the row products
+int simt_train_tile(const Problem& p);  // fp32: rows of a tile of the training forward's products
+int simt_bwd_tile(const Problem& p);    // and of the backward's row products
 __host__ __device__ constexpr int simt_cols(int tile) { return tile < 32 ? 32 : tile; }  // and its columns
 cudaError_t launch_experts_train_simt(const Problem& p, const GemmArgs& a, cudaStream_t s);
 int dh_tile(const Problem& p);  // weight columns of a unit of the first GEMM: kTcBNh or kTcBN2

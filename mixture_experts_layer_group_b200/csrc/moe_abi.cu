@@ -577,7 +577,7 @@ static moe_status experts_device(const moe_cfg* cfg, int64_t rows, const int32_t
   db.unit_base1 = at<int32_t>(ws, L.unit_base1);
   db.unit_base2 = at<int32_t>(ws, L.unit_base2);
   const bool tc = p.dtype == MOE_BF16;
-  const int bs = gu ? simt_tile(p) : kSimtBM;  // fp32
+  const int bs = gu ? simt_train_tile(p) : kSimtBM;  // fp32
   static_assert(kSimtBM == kSimtBN, "square tiles");
   e = launch_group_tables(p, counts, db, tc ? kTcBM : bs, tc ? kTcBN1 : simt_cols(bs), tc ? kTcBN2 : simt_cols(bs),
                           at<int>(ws, L.sched), s);

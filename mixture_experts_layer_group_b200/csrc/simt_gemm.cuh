@@ -67,64 +67,72 @@ struct Block {
   }
 };
 
-// What a thread has summed: the running chain, and the chains before it, in
-// registers or, for tiles whose chain takes 64 of them, in shared memory (each
-// thread its own column).
-template <int TM, int TN, bool kRegs = (TM * TN <= 16)>
-struct Sum {
-  float v[TM][TN] = {};
-  float t[TM][TN] = {};
-  bool any = false;
-  MOE_DEV void flush(float4 (*)[kThreads]) {
-    any = true;
-#pragma unroll
-    for (int i = 0; i < TM; ++i)
-#pragma unroll
-      for (int j = 0; j < TN; ++j) {
-        t[i][j] += v[i][j];
-        v[i][j] = 0.f;
-      }
-  }
-  MOE_DEV void total(float4 (*)[kThreads]) {
-    if (any) flush(nullptr);
-#pragma unroll
-    for (int i = 0; i < TM; ++i)
-#pragma unroll
-      for (int j = 0; j < TN; ++j) v[i][j] = any ? t[i][j] : v[i][j];
-  }
-};
+// What a thread has summed: the running chain (pairs of columns, for packed
+// multiply-adds), and the chains before it, in registers or, for tiles whose
+// chain takes 64 of them, in shared memory (each thread its own column).
 template <int TM, int TN>
-struct Sum<TM, TN, false> {
-  float v[TM][TN] = {};
+struct Sum {
+  static constexpr bool kRegs = TM * TN <= 16;
+  uint64_t c[TM][TN / 2] = {};
+  float v[TM][TN];  // the result, after total()
+  float t[kRegs ? TM : 1][kRegs ? TN : 1] = {};
   bool any = false;
-  MOE_DEV void flush(float4 (*t)[kThreads]) {
-    add(t);
+  MOE_DEV void flush(float4 (*chains)[kThreads]) {
+    total(chains);
 #pragma unroll
     for (int i = 0; i < TM; ++i)
 #pragma unroll
       for (int j = 0; j < TN; j += 4) {
-        t[(i * TN + j) / 4][threadIdx.x] = make_float4(v[i][j], v[i][j + 1], v[i][j + 2], v[i][j + 3]);
-        v[i][j] = v[i][j + 1] = v[i][j + 2] = v[i][j + 3] = 0.f;
+        if constexpr (kRegs) {
+          for (int q = 0; q < 4; ++q) t[i][j + q] = v[i][j + q];
+        } else {
+          chains[(i * TN + j) / 4][threadIdx.x] = make_float4(v[i][j], v[i][j + 1], v[i][j + 2], v[i][j + 3]);
+        }
+        c[i][j / 2] = c[i][j / 2 + 1] = 0;  // (0.0f, 0.0f)
       }
     any = true;
   }
-  MOE_DEV void total(float4 (*t)[kThreads]) { add(t); }
-
- private:
-  MOE_DEV void add(float4 (*t)[kThreads]) {
-    if (!any) return;
+  MOE_DEV void total(float4 (*chains)[kThreads]) {
 #pragma unroll
     for (int i = 0; i < TM; ++i)
 #pragma unroll
       for (int j = 0; j < TN; j += 4) {
-        const float4 w = t[(i * TN + j) / 4][threadIdx.x];
-        v[i][j] = w.x + v[i][j];
-        v[i][j + 1] = w.y + v[i][j + 1];
-        v[i][j + 2] = w.z + v[i][j + 2];
-        v[i][j + 3] = w.w + v[i][j + 3];
+        split_f32x2(c[i][j / 2], v[i][j], v[i][j + 1]);
+        split_f32x2(c[i][j / 2 + 1], v[i][j + 2], v[i][j + 3]);
+        if (!any) continue;
+        float4 w;
+        if constexpr (kRegs) w = make_float4(t[i][j], t[i][j + 1], t[i][j + 2], t[i][j + 3]);
+        else w = chains[(i * TN + j) / 4][threadIdx.x];
+        v[i][j] += w.x;
+        v[i][j + 1] += w.y;
+        v[i][j + 2] += w.z;
+        v[i][j + 3] += w.w;
       }
   }
 };
+
+// c[i][..] += x[i] y[..], both read from shared memory in groups of four.
+template <int TM, int TN, class X, class Y>
+MOE_DEV void outer(uint64_t (&c)[TM][TN / 2], X x_at, Y y_at) {
+  uint64_t y[TN / 2];
+#pragma unroll
+  for (int j = 0; j < TN; j += 4) {
+    const ulonglong2 w = *reinterpret_cast<const ulonglong2*>(y_at(j));
+    y[j / 2] = w.x;
+    y[j / 2 + 1] = w.y;
+  }
+#pragma unroll
+  for (int i = 0; i < TM; i += 4) {
+    const float4 w = *reinterpret_cast<const float4*>(x_at(i));
+    const float x[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const uint64_t xx = f32x2(x[q], x[q]);
+#pragma unroll
+      for (int j = 0; j < TN / 2; ++j) c[i + q][j] = fma_f32x2(xx, y[j], c[i + q][j]);
+    }
+  }
+}
 
 // Thread (tx, ty) of 16 x 16 holds rows 4 ty + 64 i + 0..3 and columns 4 tx + 64
 // j + 0..3 of a BM x BN tile, in v[4 i + ..][4 j + ..].
@@ -159,19 +167,9 @@ struct Tile {
         vb.fetch(B, n0, k0 + BK);
       }
 #pragma unroll
-      for (int kk = 0; kk < BK; ++kk) {
-        float x[kTM], y[kTN];
-#pragma unroll
-        for (int i = 0; i < kTM; i += 4)
-          *reinterpret_cast<float4*>(x + i) = *reinterpret_cast<const float4*>(&a[buf][kk][swz<BM>(kk, row(i))]);
-#pragma unroll
-        for (int j = 0; j < kTN; j += 4)
-          *reinterpret_cast<float4*>(y + j) = *reinterpret_cast<const float4*>(&b[buf][kk][swz<BN>(kk, col(j))]);
-#pragma unroll
-        for (int i = 0; i < kTM; ++i)
-#pragma unroll
-          for (int j = 0; j < kTN; ++j) acc.v[i][j] = fmaf(x[i], y[j], acc.v[i][j]);
-      }
+      for (int kk = 0; kk < BK; ++kk)
+        outer<kTM, kTN>(acc.c, [&](int i) { return &a[buf][kk][swz<BM>(kk, row(i))]; },
+                        [&](int j) { return &b[buf][kk][swz<BN>(kk, col(j))]; });
       if (more) {
         va.put(a[buf ^ 1], A.ks == 1);
         vb.put(b[buf ^ 1], B.ks == 1);
@@ -230,13 +228,8 @@ struct SplitTile {
 #pragma unroll
         for (int q = 0; q < kBK / kGroups; ++q) {
           const int kk = g * (kBK / kGroups) + q;
-          float x[4], y[4];
-          *reinterpret_cast<float4*>(x) = *reinterpret_cast<const float4*>(&a[buf][kk][swz<BM>(kk, 4 * ty)]);
-          *reinterpret_cast<float4*>(y) = *reinterpret_cast<const float4*>(&b[buf][kk][swz<kCols>(kk, 4 * tx)]);
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) acc.v[i][j] = fmaf(x[i], y[j], acc.v[i][j]);
+          outer<4, 4>(acc.c, [&](int) { return &a[buf][kk][swz<BM>(kk, 4 * ty)]; },
+                      [&](int) { return &b[buf][kk][swz<kCols>(kk, 4 * tx)]; });
         }
         if ((k0 / kBK + 1) % (kChain / (kBK / kGroups)) == 0) acc.flush(nullptr);
       }

@@ -145,7 +145,7 @@ moe_status moe_experts_backward(const moe_cfg* cfg, int64_t rows, const int32_t*
   db.unit_base1 = at<int32_t>(ws, L.unit_base1);
   db.unit_base2 = at<int32_t>(ws, L.unit_base2);
   const bool tc = p.dtype == MOE_BF16;
-  const int bs = tc ? 0 : simt_tile(p), bc = simt_cols(bs);
+  const int bs = tc ? 0 : simt_bwd_tile(p), bc = simt_cols(bs);
   e = launch_group_tables(p, counts, db, tc ? kTcBM : bs, tc ? dh_tile(p) : bc, tc ? kTcBN2 : bc,
                           at<int>(ws, L.sched), s);
   if (e != cudaSuccess) return cuda_fail(e);
@@ -242,7 +242,7 @@ moe_status moe_route_backward(const moe_cfg* cfg, int64_t T, const void* x, cons
   one.F = p.d;
   one.N = 1;
   one.R = T;
-  const int bs = simt_tile(one), bc = simt_cols(bs);
+  const int bs = simt_bwd_tile(one), bc = simt_cols(bs);
   const int64_t units = (T + bs - 1) / bs * ((p.d + bc - 1) / bc);  // fp32 row tiles
   if (units > (1ll << 31) - 1) return MOE_ERR_UNSUPPORTED;
   RouteDzArgs z{};

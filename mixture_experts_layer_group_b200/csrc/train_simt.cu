@@ -1,6 +1,7 @@
-// Backward products of fp32 layers on CUDA cores: the grouped experts' three
-// stages and the router's two products, with fp32 accumulators.
+// The training forward and backward of fp32 layers on CUDA cores: the grouped
+// experts' products and the router's two, with fp32 accumulators.
 //
+//   gu     g = x W1^T, u = x W3^T; then h = silu(g) u and y = gate (h W2^T)
 //   dh     q = dy W2 per row, then per element (s = sigmoid(g), h = g s u)
 //            dgate += q h, du = gate q g s, dg = gate q u s (1 + g (1 - s)),
 //            gh = gate h
@@ -8,13 +9,15 @@
 //   dW     dW1 = dg^T x, dW3 = du^T x, dW2 = dy^T gh over a group's rows
 //
 // Bound by the FP32 pipes where the rows are many: 8 groups of 512 rows, d 1024,
-// d_ff 1024 take 1345 us (51.5 GFLOP, 38 TFLOP/s) in tiles of 128 x 128 (8 x 8
-// outputs per thread, four 16-byte shared loads for 64 multiply-adds). Few rows
-// leave SMs idle and make long chains of dependent blocks, so small products
-// take 32 x 32 tiles whose sum is split over four groups of threads: 16 groups of
-// 32 rows, d 256, d_ff 512 take 70 us (0.8 GFLOP; 85 us before the dx product and
-// the weight gradients, which need only dh, ran beside each other; 111 us before
-// that in tiles of 64 x 64).
+// d_ff 1024 take 661 us forward (25.8 GFLOP, 39 TFLOP/s) and 1290 us backward in
+// tiles of 128 x 128 (8 x 8 outputs per thread, four 16-byte shared loads for 32
+// packed multiply-adds of two; unpacked ones 704 and 1420 us). Few rows leave SMs
+// idle and make long chains of dependent blocks, so small products take tiles
+// of 32 x 32 or 8 x 32 whose sum is split over groups of threads: 16 groups of 32
+// rows, d 256, d_ff 512 take 46 us forward and 67 us backward (0.8 GFLOP); one
+// group of 3 rows of 7168 x 4096 takes 137 us forward (352 MB of weights, 2.6
+// TB/s). The weight gradients run beside the dx product, which like them needs
+// only dh (15 us of the smaller backward).
 #include <cmath>
 #include <type_traits>
 
@@ -371,17 +374,21 @@ cudaError_t launch_dgate_reduce(const float* part, int planes, int64_t rows, flo
   return launch_after(dgate_reduce_kernel, (unsigned)((rows + 31) / 32), 256, 0, s, part, planes, rows, dgate);
 }
 
-// The two row products' tiles: larger ones where they give every SM two of 128 or
-// four of 64. The whole backward (dx before the weight gradients, not beside them) with tiles of 128, 64 and 32: 8 groups of 512
-// rows (d 1024, d_ff 1024) 1390, 1510 and 1680 us, of 128 rows 669, 552 and 484
-// us; 16 groups of 256 rows (d 256, d_ff 512) 361, 257 and 290 us, of 32 rows
-// 234, 111 and 85 us.
-int simt_tile(const Problem& p) {
-  const int64_t cols = p.d + p.F, sms = device_sm_count();
+// The row products' tiles, by the columns of their outputs: larger ones where the
+// products give every SM two of 128 or four of 64. The whole backward (dx before
+// the weight gradients, not beside them) with tiles of 128, 64 and 32 rows: 8
+// groups of 512 rows (d 1024, d_ff 1024) 1390, 1510 and 1680 us, of 128 rows
+// 669, 552 and 484 us; 16 groups of 256 rows (d 256, d_ff 512) 361, 257 and 290
+// us, of 32 rows 234, 111 and 85 us. One group of 3 rows (d 7168, d_ff 4096)
+// with tiles of 32 and 8 rows: 462 and 314 us.
+int simt_tile(const Problem& p, int64_t cols) {
+  const int64_t sms = device_sm_count();
   if ((p.R + 127) / 128 * (cols / 128) >= 2 * sms) return 128;
   if ((p.R + 63) / 64 * (cols / 64) >= 4 * sms) return 64;
   return p.R <= 8 * (int64_t)p.N ? 8 : 32;
 }
+int simt_train_tile(const Problem& p) { return simt_tile(p, 2 * (int64_t)p.F + p.d); }
+int simt_bwd_tile(const Problem& p) { return simt_tile(p, (int64_t)p.F + p.d); }
 
 cudaError_t launch_dh(const DhParams& h, int tile, cudaStream_t s) {
   const unsigned sms = device_sm_count();
@@ -407,7 +414,7 @@ cudaError_t launch_fwd(const FwdParams& f, int tile, cudaStream_t s) {
 }
 
 cudaError_t launch_experts_train_simt(const Problem& p, const GemmArgs& a, cudaStream_t s) {
-  const int tile = simt_tile(p);
+  const int tile = simt_train_tile(p);
   const Groups g1{a.unit_base1, a.grp_row0, a.grp_rows, p.N}, g2{a.unit_base2, a.grp_row0, a.grp_rows, p.N};
   cudaError_t e = launch_fwd(FwdParams{g1, (const float*)a.x_perm, (const float*)a.W1, (const float*)a.W3, nullptr,
                                        (float*)a.gu, p.d, p.F}, tile, s);
@@ -421,7 +428,7 @@ cudaError_t launch_experts_train_simt(const Problem& p, const GemmArgs& a, cudaS
 }
 
 cudaError_t launch_experts_backward_simt(const Problem& p, const ExpertsBwdArgs& a, cudaStream_t s) {
-  const int tile = simt_tile(p);
+  const int tile = simt_bwd_tile(p);
   const Groups g1{a.unit_base1, a.grp_row0, a.grp_rows, p.N}, g2{a.unit_base2, a.grp_row0, a.grp_rows, p.N};
   DhParams h{g1, (const float*)a.dy_rows, (const float*)a.W2, (const float*)a.gu, a.gate_rows, (float*)a.dg,
              (float*)a.du, (float*)a.gh, a.dgate_rows ? a.dgate_part : nullptr, p.d, p.F, p.R};
@@ -459,7 +466,7 @@ cudaError_t launch_route_products_simt(const Problem& p, const RouteBwdArgs& a, 
   if (a.dx) {
     DxParams x{Groups{a.tables + kRtUnits, row0, rows, 1}, a.dz, nullptr, (const float*)a.W_r, nullptr,
                (float*)a.dx, p.d, p.N, a.ld};
-    e = launch_dx(x, simt_tile(one), s);
+    e = launch_dx(x, simt_bwd_tile(one), s);
   }
   if (e == cudaSuccess && a.dW_r) {
     const bool split = a.splits > 1;
