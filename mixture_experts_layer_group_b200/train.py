@@ -33,11 +33,14 @@ class TrainLayer:
     ABI; FP8 weights are not trained). grads: the weights' gradients by name,
     of grad_dtype ("f32" or "bf16"; None: the layer's type), written by each
     backward(), or added to by backward(accumulate=True) (fp32). max_tokens
-    bounds a call's tokens. All calls of one TrainLayer belong on one stream."""
+    bounds a call's tokens. All calls of one TrainLayer belong on one stream
+    of the current device."""
 
     def __init__(self, cfg: MoeCfg, weights: dict, max_tokens: int, grad_dtype=None, device="cuda"):
         self.cfg, self.w, self.max_tokens = cfg, weights, max_tokens
         self.grad_dtype = grad_dtype or {MOE_BF16: "bf16", MOE_F32: "f32"}[cfg.dtype]
+        if self.grad_dtype not in ("f32", "bf16") or (self.grad_dtype == "bf16" and cfg.dtype == MOE_F32):
+            raise ValueError(f"weight gradients are fp32, or bf16 in a bf16 layer: got {grad_dtype!r}")
         self.device = device
         self.dtype = _DTYPE[cfg.dtype]
         self.routed = _group_cfg(cfg, cfg.n_routed, cfg.d_ff)
@@ -49,20 +52,57 @@ class TrainLayer:
             sizes += [experts_workspace_size(self.shared, T), experts_backward_workspace_size(self.shared, T)]
         # the calls of a step follow one another, so one workspace serves them all
         self.ws = torch.empty(max(sizes), dtype=torch.uint8, device=device)
+        for n, shape in self._weight_shapes().items():
+            t = weights[n]
+            if tuple(t.shape) != shape or t.dtype != self.dtype or not t.is_contiguous():
+                raise ValueError(f"{n} is a contiguous {self.dtype} tensor {shape}: got {t.dtype} {tuple(t.shape)}")
         gdt = {"bf16": torch.bfloat16, "f32": torch.float32}[self.grad_dtype]
-        names = ["W_r", "W1", "W3", "W2"] + (["Ws1", "Ws3", "Ws2"] if self.shared is not None else [])
-        self.grads = {n: torch.zeros(weights[n].shape, dtype=gdt, device=device) for n in names}
+        self.grads = {n: torch.zeros(s, dtype=gdt, device=device) for n, s in self._weight_shapes().items()}
         self.grad_list = GradList(self.grads.values())
         self.clip_ws = torch.empty(grad_norm_workspace_size(self.grad_list), dtype=torch.uint8, device=device)
         self.sumsq = torch.zeros(1, dtype=torch.float64, device=device)
         self.norm = torch.zeros(1, dtype=torch.float32, device=device)
+        self.status = torch.zeros(1, dtype=torch.int32, device=device)
         self.saved = None
+
+    def _weight_shapes(self):
+        c = self.cfg
+        shapes = {"W_r": (c.n_routed, c.d), "W1": (c.n_routed, c.d_ff, c.d), "W3": (c.n_routed, c.d_ff, c.d),
+                  "W2": (c.n_routed, c.d, c.d_ff)}
+        if c.n_shared:
+            ff = c.n_shared * c.d_ff
+            shapes.update(Ws1=(ff, c.d), Ws3=(ff, c.d), Ws2=(c.d, ff))
+        return shapes
+
+    def _check_rows(self, name, t):
+        if t.dim() != 2 or t.shape[1] != self.cfg.d or t.dtype != self.dtype or not t.is_contiguous():
+            raise ValueError(f"{name} is a contiguous {self.dtype} tensor [T, {self.cfg.d}]: got {t.dtype} "
+                             f"{tuple(t.shape)}, strides {t.stride()}")
 
     def _new(self, shape, dtype=None):
         return torch.empty(shape, dtype=dtype or self.dtype, device=self.device)
 
+    def _note_status(self, T, stream):
+        """Keeps the device-status bits of the call before (the next one on the workspace clears them)."""
+        if T == 0:  # nothing ran
+            return
+        word = self.ws[:4].view(torch.int32)
+        if stream is None:
+            self.status.bitwise_or_(word)
+        else:
+            on = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(stream)
+            with torch.cuda.stream(on):
+                self.status.bitwise_or_(word)
+
+    def device_status(self) -> int:
+        """The MOE_DEV_* bits of the calls since the last device_status(), which are then cleared (synchronises)."""
+        bits = int(self.status)
+        self.status.zero_()
+        return bits
+
     def forward(self, x, stream=None):
         """y of the tokens x [T, d]; keeps what backward() needs."""
+        self._check_rows("x", x)
         cfg, w, T, k = self.cfg, self.w, x.shape[0], self.cfg.top_k
         if T > self.max_tokens:
             raise ValueError(f"{T} tokens exceed max_tokens {self.max_tokens}")
@@ -74,10 +114,12 @@ class TrainLayer:
         y_rows = self._new((R, cfg.d))
         offsets = self._new(cfg.n_routed + 1, i32)
         route_train(cfg, T, x, w["W_r"], w.get("b"), s["idx"], s["gates"], s["logits"], self.ws, stream=stream)
+        self._note_status(T, stream)
         dispatch_rows(cfg, T, s["idx"], s["gates"], x, s["counts"], offsets, s["slot_pos"], s["x_rows"],
                       s["gate_rows"], self.ws, stream=stream)
         experts_train(self.routed, R, s["counts"], s["x_rows"], s["gate_rows"], w["W1"], w["W3"], w["W2"], y_rows,
                       s["gu"], self.ws, stream=stream)
+        self._note_status(T, stream)
         y_shared = None
         if self.shared is not None:
             s["shared_counts"] = torch.full((1,), T, dtype=i32, device=self.device)
@@ -97,6 +139,7 @@ class TrainLayer:
         T, k = s["x"].shape[0], cfg.top_k
         if dy.shape != s["x"].shape:
             raise ValueError(f"dy has shape {tuple(dy.shape)}, the forward's tokens {tuple(s['x'].shape)}")
+        self._check_rows("dy", dy)
         R = T * k
         opt = dict(grad_dtype=self.grad_dtype, accumulate=accumulate, stream=stream)
         dy_rows, dx_rows = self._new((R, cfg.d)), self._new((R, cfg.d))
@@ -105,6 +148,7 @@ class TrainLayer:
         combine_backward(cfg, T, dy, s["slot_pos"], dy_rows, stream=stream)
         experts_backward(self.routed, R, s["counts"], s["x_rows"], s["gate_rows"], w["W1"], w["W3"], w["W2"], s["gu"],
                          dy_rows, dx_rows, dgate_rows, g["W1"], g["W3"], g["W2"], self.ws, **opt)
+        self._note_status(T, stream)
         if self.shared is not None:
             dx_shared = torch.empty_like(dy)
             experts_backward(self.shared, T, s["shared_counts"], s["x"], None, w["Ws1"], w["Ws3"], w["Ws2"],
@@ -127,5 +171,11 @@ class TrainLayer:
 
     def balance(self, gamma, stream=None):
         """The loss-free balancing step of the selection bias from the last forward's expert loads."""
+        if self.saved is None:
+            raise RuntimeError("balance() without a forward()")
+        if self.w.get("b") is None:
+            raise ValueError("the layer has no selection bias b")
         s = self.saved
+        if s["x"].shape[0] == 0:  # no loads to balance
+            return
         bias_update(self.cfg, s["x"].shape[0], s["counts"], gamma, self.w["b"], stream=stream)

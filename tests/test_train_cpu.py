@@ -8,6 +8,7 @@ import torch
 
 import mixture_experts_layer_group_b200 as moe
 from mixture_experts_layer_group_b200 import build as moe_build
+from mixture_experts_layer_group_b200.train import TrainLayer
 
 INVALID, UNSUPPORTED, WORKSPACE = 1, 2, 3
 A = 1 << 20  # an aligned address that is never touched: every call below is refused first
@@ -173,3 +174,46 @@ def test_grad_calls_refuse_bad_tables_and_limits():
 def test_grad_tensor_matches_header():
     assert ctypes.sizeof(moe.GradTensor) == 32
     assert [n for n, _ in moe.GradTensor._fields_] == ["src", "dst", "numel", "dtype", "reserved"]
+
+
+def train_layer(**kw):
+    c = cfg(n_shared=1)
+    w = dict(W_r=torch.zeros(8, 64), W1=torch.zeros(8, 32, 64), W3=torch.zeros(8, 32, 64), W2=torch.zeros(8, 64, 32),
+             Ws1=torch.zeros(32, 64), Ws3=torch.zeros(32, 64), Ws2=torch.zeros(64, 32))
+    w = {n: t.to(torch.bfloat16) for n, t in w.items()}
+    w.update(kw.pop("weights", {}))
+    return TrainLayer(c, w, max_tokens=4, device="cpu", **kw)
+
+
+def test_train_layer_refuses_weights_it_cannot_take():
+    train_layer()
+    for name, bad in (("W1", torch.zeros(8, 64, 32, dtype=torch.bfloat16)), ("W2", torch.zeros(8, 64, 32)),
+                      ("Ws1", torch.zeros(64, 32, dtype=torch.bfloat16).T)):
+        with pytest.raises(ValueError, match=name):
+            train_layer(weights={name: bad})
+    with pytest.raises(ValueError, match="gradients"):
+        train_layer(grad_dtype="f16")
+
+
+@pytest.mark.parametrize("bad", [
+    torch.zeros(4, 32, dtype=torch.bfloat16), torch.zeros(4, 64), torch.zeros(64, 4, dtype=torch.bfloat16).T,
+    torch.zeros(1, 64, dtype=torch.bfloat16).expand(4, 64), torch.zeros(2, 2, 64, dtype=torch.bfloat16)])
+def test_train_layer_refuses_rows_it_cannot_read(bad):
+    layer = train_layer()
+    with pytest.raises(ValueError, match="x is"):
+        layer.forward(bad)
+    layer.saved = dict(x=torch.zeros(tuple(bad.shape), dtype=torch.bfloat16))
+    with pytest.raises(ValueError, match="dy is"):
+        layer.backward(bad)
+
+
+def test_train_layer_steps_come_in_order():
+    layer = train_layer()
+    with pytest.raises(ValueError, match="max_tokens"):
+        layer.forward(torch.zeros(5, 64, dtype=torch.bfloat16))
+    for call in (lambda: layer.backward(torch.zeros(4, 64, dtype=torch.bfloat16)), lambda: layer.balance(1e-3)):
+        with pytest.raises(RuntimeError):
+            call()
+    layer.saved = dict(x=torch.zeros(4, 64, dtype=torch.bfloat16))
+    with pytest.raises(ValueError, match="bias"):
+        layer.balance(1e-3)

@@ -255,6 +255,17 @@ def test_experts_backward_accumulates(dtype):
     assert torch.equal(more["dx"], once["dx"]) and torch.equal(more["dgate"], once["dgate"])
 
 
+@pytest.mark.parametrize("counts,d,F", [([20, 0, 33, 7, 1, 64], 1032, 776), ([400, 0, 17], 1032, 1288)],
+                         ids=["kept", "streamed"])
+def test_experts_backward_accumulates_over_runs_of_tiles(counts, d, F):
+    b = Block(counts, d, F, "bf16", seed=23)
+    b.forward()
+    once = b.backward("f32")
+    twice = b.backward("f32", accumulate=True, start=0.5)
+    for n in ("dW1", "dW3", "dW2"):  # the old value is added to the sum, rounded once
+        assert torch.equal(twice[n], once[n] + 0.5), n
+
+
 def test_experts_backward_skips_what_is_not_asked_for():
     b = Block([33, 0, 70], 136, 264, seed=5)
     full = b.backward()
@@ -775,6 +786,53 @@ def test_training_step(T, d, F, N, ns, k, score, normalize, dtype):
         mean = T * k / N
         want_b = torch.where(layer.saved["counts"] > mean, b - 1e-3, torch.where(layer.saved["counts"] < mean, b + 1e-3, b))
         assert torch.equal(w["b"], want_b)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_training_step_without_tokens(dtype):
+    cfg, w, x, dy = layer_case(6, 64, 64, 8, 1, 2, "sigmoid", True, dtype)
+    layer = TrainLayer(cfg, w, max_tokens=6)
+    b = w["b"].clone()
+    y, dx = layer.forward(x[:0]), layer.backward(dy[:0])
+    assert y.shape == dx.shape == (0, 64)
+    for n, t in layer.grads.items():
+        assert not t.any(), n
+    assert float(layer.clip(1.0)) == 0.0
+    layer.balance(1e-3)
+    assert torch.equal(b, w["b"]) and layer.device_status() == 0
+
+
+def test_training_steps_on_two_streams_at_once():
+    """Two layers, each on a stream of its own, a dozen steps in flight: each step's results are those it has alone."""
+    cases = [layer_case(300, 256, 384, 16, 1, 4, "sigmoid", True, dt, seed=i) for i, dt in enumerate(("bf16", "f32"))]
+    layers = [TrainLayer(c, w, max_tokens=300) for c, w, _, _ in cases]
+    alone = []
+    for layer, (_, _, x, dy) in zip(layers, cases):
+        alone.append([layer.forward(x), layer.backward(dy), {n: t.clone() for n, t in layer.grads.items()}])
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in layers]
+    got = [None, None]
+    for _ in range(6):
+        for i, (layer, (_, _, x, dy)) in enumerate(zip(layers, cases)):
+            with torch.cuda.stream(streams[i]):
+                got[i] = [layer.forward(x), layer.backward(dy)]
+    torch.cuda.synchronize()
+    for i, layer in enumerate(layers):
+        assert torch.equal(got[i][0], alone[i][0]) and torch.equal(got[i][1], alone[i][1])
+        for n, t in layer.grads.items():
+            assert torch.equal(t, alone[i][2][n]), n
+        assert layer.device_status() == 0
+
+
+def test_training_step_keeps_the_status_of_its_calls():
+    cfg, w, x, dy = layer_case(40, 64, 64, 8, 0, 2, "sigmoid", True, "bf16")
+    layer = TrainLayer(cfg, w, max_tokens=40)
+    layer.forward(x), layer.backward(dy)
+    assert layer.device_status() == 0
+    x[3, 5] = float("nan")
+    layer.forward(x)
+    assert layer.device_status() & 16  # a token's logits were not finite
+    assert layer.device_status() == 0
 
 
 def test_training_step_in_a_graph():
