@@ -1,5 +1,6 @@
 /*
- * moe_b200.h -- C ABI of the B200 (sm_100a) DeepSeekMoE layer forward.
+ * moe_b200.h -- C ABI of the B200 (sm_100a) DeepSeekMoE layer: its forward, and
+ * the backward passes and gradient clipping of training.
  *
  * The layer (a DeepSeekMoE feed-forward block, as listed step by step on the
  * "DeepSeek-V3.2-Exp · Mixture of experts" page, section "All 19 steps"):

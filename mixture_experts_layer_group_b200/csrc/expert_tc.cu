@@ -21,6 +21,12 @@
 //                the shared MLP) -> bf16 row of the slot
 //                ("E_i = h W2", "y_routed = sum G_i E_i")
 //
+// The training modes (enum Mode) are the SwiGLU GEMM that also stores g and u,
+// and the backward's products dh and dx, which take the weights transposed
+// (MN-major tiles; see BwdParams). 57344 rows of 63 experts of 896 x 1280: SwiGLU
+// 268 us, down 145, dh 228, dx 221; 8192 rows of 32 of 2048 x 7168: 492, 232, 289
+// and 421 us (read of the weights alone 287, 143, 143 and 287 us).
+//
 // Groups 0..N-1 are the routed experts over their expert-contiguous token
 // rows; group N is the fused shared MLP over all T tokens, in the same
 // persistent launch. A group of more than 256 rows is cut into equal chunks.
@@ -33,7 +39,7 @@
 //
 // CTA roles (320 threads, one CTA per SM, persistent; the same roles in both
 // CTAs of a pair except the MMA issuer, which only the first CTA has):
-//   warp 0      TMA producer (one lane). In CTA 0 it also takes unit ids and
+//   warp 0      TMA producer (one elected lane). In CTA 0 it also takes unit ids and
 //               hands them to both CTAs through shared-memory rings (the
 //               peer's by an asynchronous store, see below). Stages
 //               are variable-size pieces of a 208 KB byte ring: per 64-wide
@@ -42,7 +48,7 @@
 //               cost is per box); the bytes of both CTAs complete on CTA 0's
 //               stage barrier; weights read by one unit only are evict-first
 //   warp 1      TMEM owner (both CTAs, pair allocation) + UMMA issuer (CTA 0,
-//               one lane): 2 x 4 pair MMAs (256 x N x 16) per stage. Each
+//               one elected lane): 2 x 4 pair MMAs (256 x N x 16) per stage. Each
 //               CTA's TMEM holds two buffers of 2 x 128 fp32 columns: a unit
 //               of <= 128 tokens takes one buffer (the next unit's MMAs
 //               overlap its epilogue), a larger unit takes both (2 x 256)

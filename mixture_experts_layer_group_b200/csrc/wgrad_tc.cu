@@ -12,15 +12,21 @@
 // operand, the rest for the tiles' own -- and keeps rows 128 r .. 128 r + 127
 // of a tile in its tensor memory, in one of two 256-column buffers.
 //
-// What bounds these sums is the operands' way from L2 (about 36 bytes per cycle
-// and SM), so a unit reuses the shared operand as its rows allow:
+// What bounds long sums is the operands' way from L2 (the SMs took 29 bytes per
+// cycle each on average, with the tensor pipe 60 % busy), and short ones the
+// writing of the result, so a unit reuses the shared operand as its rows allow:
 //   few rows (the shared operand's pieces hold them all): it is loaded once for
 //     the whole run, and each tile streams its own operand past it, 32 KB per
 //     pair and 512 cycles of pair MMAs; tiles alternate between the buffers
 //   many rows: the tiles go in twos, both fed by one pass over the rows, 96 KB
 //     per 1024 cycles; between two passes the first tile's MMAs of two stages run
 //     while the second tile is still being read
-// One tile at a time would take 64 KB per 512 cycles.
+// One tile at a time would take 64 KB per 512 cycles. Measured: the gradients of
+// 63 experts of 896 x 1280 over 57344 rows 350 us (395 GFLOP, 1.13 PFLOP/s), of
+// one of 2048 x 7168 over 4096 rows 247 us (1.46 PFLOP/s), of 32 of those over
+// 8192 rows 746 us: 2.8 GB written, 717 us at the 3.93 TB/s that a B200 writes
+// when it does nothing else. (The whole backward with tiles one by one: 946, 598
+// and 1622 us, in twos 911, 563 and 1548.)
 //
 // A group's last piece may hold up to 15 rows of the next group inside its
 // last K = 16 step. They would enter the sum, and a NaN there cannot be
