@@ -1675,7 +1675,9 @@ cudaError_t launch_experts_backward_tc(const Problem& p, const ExpertsBwdArgs& a
   }
   // (last: between the GEMMs its launch and its wait would stand in their way)
   auto reduce_dgate = [&] {
-    return a.dgate_rows ? launch_dgate_reduce(a.dgate_part, dgate_planes(p), p.R, a.dgate_rows, s) : cudaSuccess;
+    return a.dgate_rows ? launch_dgate_reduce(a.dgate_part, dgate_planes(p), p.R, a.unit_base1 + p.N + 1,
+                                              a.dgate_rows, s)
+                        : cudaSuccess;
   };
   if (!a.dW1) return reduce_dgate();
   WgradArgs w{};

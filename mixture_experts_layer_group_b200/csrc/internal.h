@@ -239,8 +239,10 @@ cudaError_t launch_experts_train_simt(const Problem& p, const GemmArgs& a, cudaS
 int dh_tile(const Problem& p);  // weight columns of a unit of the first GEMM: kTcBNh or kTcBN2
 cudaError_t launch_experts_backward_tc(const Problem& p, const ExpertsBwdArgs& a, cudaStream_t s);
 cudaError_t launch_experts_backward_simt(const Problem& p, const ExpertsBwdArgs& a, cudaStream_t s);
-// dgate[r] = sum over the planes of part[plane][r], in a fixed order.
-cudaError_t launch_dgate_reduce(const float* part, int planes, int64_t rows, float* dgate, cudaStream_t s);
+// dgate[r] = sum over the planes of part[plane][r], in a fixed order; nothing
+// where *units, the number of units that wrote them, is zero.
+cudaError_t launch_dgate_reduce(const float* part, int planes, int64_t rows, const int32_t* units, float* dgate,
+                                cudaStream_t s);
 
 // The gradient of the logits (see route_bwd.cu), and the row tables of the
 // two products that follow: ints written to `tables` from the parameters.

@@ -349,9 +349,10 @@ cudaError_t launch_dw(const DwParams& p, cudaStream_t s) {
 // 32 rows per CTA; warp w adds planes w, w + 8, ..., then the warps' sums are
 // added in order (so that a row's planes are eight short chains of loads).
 __global__ void __launch_bounds__(256) dgate_reduce_kernel(const float* __restrict__ part, int planes, int64_t rows,
-                                                           float* __restrict__ dgate) {
+                                                           const int32_t* __restrict__ units, float* __restrict__ dgate) {
   griddep_launch_dependents();
   griddep_wait();
+  if (__ldg(units) == 0) return;  // counts that do not add up: no row was computed
   __shared__ float sums[8][32];
   const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t r = (int64_t)blockIdx.x * 32 + lane;
@@ -370,8 +371,9 @@ __global__ void __launch_bounds__(256) dgate_reduce_kernel(const float* __restri
 
 }  // namespace
 
-cudaError_t launch_dgate_reduce(const float* part, int planes, int64_t rows, float* dgate, cudaStream_t s) {
-  return launch_after(dgate_reduce_kernel, (unsigned)((rows + 31) / 32), 256, 0, s, part, planes, rows, dgate);
+cudaError_t launch_dgate_reduce(const float* part, int planes, int64_t rows, const int32_t* units, float* dgate,
+                                cudaStream_t s) {
+  return launch_after(dgate_reduce_kernel, (unsigned)((rows + 31) / 32), 256, 0, s, part, planes, rows, units, dgate);
 }
 
 // The row products' tiles, by the columns of their outputs: larger ones where the
@@ -451,7 +453,8 @@ cudaError_t launch_experts_backward_simt(const Problem& p, const ExpertsBwdArgs&
     w.independent = a.dx_rows != nullptr;
     e = launch_dw(w, s);
   }
-  if (e == cudaSuccess && a.dgate_rows) e = launch_dgate_reduce(a.dgate_part, dgate_planes(p), p.R, a.dgate_rows, s);
+  if (e == cudaSuccess && a.dgate_rows)
+    e = launch_dgate_reduce(a.dgate_part, dgate_planes(p), p.R, a.unit_base1 + p.N + 1, a.dgate_rows, s);
   return e;
 }
 

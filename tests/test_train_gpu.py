@@ -300,7 +300,7 @@ def test_experts_backward_reports_counts_that_do_not_add_up(dtype):
     out = b.backward(expect=moe.MOE_DEV_BAD_EXPERT)
     for name in ("dW1", "dW3", "dW2"):
         assert not out[name].any(), name
-    assert bool((out["dx"] == 3.0).all())
+    assert bool((out["dx"] == 3.0).all()) and bool((out["dgate"] == 3.0).all())
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
