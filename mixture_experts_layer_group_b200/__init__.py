@@ -374,7 +374,8 @@ def route_backward(cfg, T, x, W_r, logits, topk_idx, dgates, slot_pos, dx, dW_r,
 class GradList:
     """The gradients of one grad_norm / grad_clip call: contiguous fp32 or
     bf16 tensors, and where their clipped forms go (dsts None: in place).
-    Holds references to the tensors; build it once and use it every step."""
+    Holds references to the tensors; build it once and use it every step. A
+    gradient is listed once: overlapping destinations are refused."""
 
     def __init__(self, srcs, dsts=None):
         import torch
@@ -391,6 +392,22 @@ class GradList:
                 raise ValueError("a gradient and its destination are contiguous and of one size")
             entry.src, entry.dst = src.data_ptr(), dst.data_ptr()
             entry.numel, entry.dtype = src.numel(), dtypes[src.dtype]
+        # a destination that another gradient is read from or written to would be scaled twice, or too early
+        spans = []
+        for i, (src, dst) in enumerate(zip(self.srcs, self.dsts)):
+            size = src.numel() * src.element_size()
+            if size:
+                spans.append((dst.data_ptr(), dst.data_ptr() + size, True, i))
+                if src.data_ptr() != dst.data_ptr():
+                    spans.append((src.data_ptr(), src.data_ptr() + size, False, i))
+        spans.sort()
+        end = {True: (0, -1), False: (0, -1)}  # of the destinations and sources so far: the furthest, and its gradient
+        for lo, hi, written, i in spans:
+            for kind, (past, j) in end.items():
+                if lo < past and (written or kind):
+                    raise ValueError(f"gradients {j} and {i} overlap where one of them is written")
+            if hi > end[written][0]:
+                end[written] = (hi, i)
 
     def __len__(self):
         return len(self.srcs)

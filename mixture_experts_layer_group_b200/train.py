@@ -10,6 +10,8 @@ into a CUDA graph.
 """
 from __future__ import annotations
 
+import contextlib
+
 import torch
 
 from . import (MOE_BF16, MOE_F32, GradList, MoeCfg, bias_update, combine, combine_backward, dispatch_backward,
@@ -26,6 +28,20 @@ def _group_cfg(cfg: MoeCfg, groups: int, d_ff: int) -> MoeCfg:
                   dtype=cfg.dtype)
 
 
+@contextlib.contextmanager
+def _on(stream, *tensors):
+    """Makes `stream` (None: leaves the current one) the stream that buffers belong to and calls run on; the
+    caller's tensors are kept until what it has queued has read them."""
+    if stream is None:
+        yield
+        return
+    on = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(stream)
+    with torch.cuda.stream(on):
+        yield
+    for t in tensors:
+        t.record_stream(on)
+
+
 class TrainLayer:
     """The layer with its gradients.
 
@@ -34,7 +50,8 @@ class TrainLayer:
     of grad_dtype ("f32" or "bf16"; None: the layer's type), written by each
     backward(), or added to by backward(accumulate=True) (fp32). max_tokens
     bounds a call's tokens. All calls of one TrainLayer belong on one stream
-    of the current device."""
+    of the current device: the current one, or `stream`, which the results
+    then belong to (the caller orders it after what wrote the arguments)."""
 
     def __init__(self, cfg: MoeCfg, weights: dict, max_tokens: int, grad_dtype=None, device="cuda"):
         self.cfg, self.w, self.max_tokens = cfg, weights, max_tokens
@@ -82,30 +99,29 @@ class TrainLayer:
     def _new(self, shape, dtype=None):
         return torch.empty(shape, dtype=dtype or self.dtype, device=self.device)
 
-    def _note_status(self, T, stream):
+    def _note_status(self, T):
         """Keeps the device-status bits of the call before (the next one on the workspace clears them)."""
         if T == 0:  # nothing ran
             return
-        word = self.ws[:4].view(torch.int32)
-        if stream is None:
-            self.status.bitwise_or_(word)
-        else:
-            on = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(stream)
-            with torch.cuda.stream(on):
-                self.status.bitwise_or_(word)
+        self.status.bitwise_or_(self.ws[:4].view(torch.int32))
 
-    def device_status(self) -> int:
+    def device_status(self, stream=None) -> int:
         """The MOE_DEV_* bits of the calls since the last device_status(), which are then cleared (synchronises)."""
-        bits = int(self.status)
-        self.status.zero_()
+        with _on(stream):
+            bits = int(self.status)
+            self.status.zero_()
         return bits
 
     def forward(self, x, stream=None):
         """y of the tokens x [T, d]; keeps what backward() needs."""
         self._check_rows("x", x)
+        if x.shape[0] > self.max_tokens:
+            raise ValueError(f"{x.shape[0]} tokens exceed max_tokens {self.max_tokens}")
+        with _on(stream, x):
+            return self._forward(x)
+
+    def _forward(self, x):
         cfg, w, T, k = self.cfg, self.w, x.shape[0], self.cfg.top_k
-        if T > self.max_tokens:
-            raise ValueError(f"{T} tokens exceed max_tokens {self.max_tokens}")
         R, i32, f32 = T * k, torch.int32, torch.float32
         s = dict(x=x, idx=self._new((T, k), i32), gates=self._new((T, k), f32), logits=self._new((T, cfg.n_routed), f32),
                  counts=self._new(cfg.n_routed, i32), slot_pos=self._new((T, k), i32), x_rows=self._new((R, cfg.d)),
@@ -113,21 +129,21 @@ class TrainLayer:
         y = torch.empty_like(x)
         y_rows = self._new((R, cfg.d))
         offsets = self._new(cfg.n_routed + 1, i32)
-        route_train(cfg, T, x, w["W_r"], w.get("b"), s["idx"], s["gates"], s["logits"], self.ws, stream=stream)
-        self._note_status(T, stream)
+        route_train(cfg, T, x, w["W_r"], w.get("b"), s["idx"], s["gates"], s["logits"], self.ws)
+        self._note_status(T)
         dispatch_rows(cfg, T, s["idx"], s["gates"], x, s["counts"], offsets, s["slot_pos"], s["x_rows"],
-                      s["gate_rows"], self.ws, stream=stream)
+                      s["gate_rows"], self.ws)
         experts_train(self.routed, R, s["counts"], s["x_rows"], s["gate_rows"], w["W1"], w["W3"], w["W2"], y_rows,
-                      s["gu"], self.ws, stream=stream)
-        self._note_status(T, stream)
+                      s["gu"], self.ws)
+        self._note_status(T)
         y_shared = None
         if self.shared is not None:
             s["shared_counts"] = torch.full((1,), T, dtype=i32, device=self.device)
             s["shared_gu"] = self._new((T, 2 * self.shared.d_ff))
             y_shared = self._new((T, cfg.d))
             experts_train(self.shared, T, s["shared_counts"], x, None, w["Ws1"], w["Ws3"], w["Ws2"], y_shared,
-                          s["shared_gu"], self.ws, stream=stream)
-        combine(cfg, T, y_rows, s["slot_pos"], y_shared, y, stream=stream)
+                          s["shared_gu"], self.ws)
+        combine(cfg, T, y_rows, s["slot_pos"], y_shared, y)
         self.saved = s
         return y
 
@@ -135,38 +151,44 @@ class TrainLayer:
         """dx of the last forward's tokens from dy [T, d]; the weights' gradients go to `grads`."""
         if self.saved is None:
             raise RuntimeError("backward() without a forward()")
-        cfg, w, g, s = self.cfg, self.w, self.grads, self.saved
-        T, k = s["x"].shape[0], cfg.top_k
-        if dy.shape != s["x"].shape:
-            raise ValueError(f"dy has shape {tuple(dy.shape)}, the forward's tokens {tuple(s['x'].shape)}")
+        x = self.saved["x"]
+        if dy.shape != x.shape:
+            raise ValueError(f"dy has shape {tuple(dy.shape)}, the forward's tokens {tuple(x.shape)}")
         self._check_rows("dy", dy)
+        with _on(stream, dy, x):
+            return self._backward(dy, accumulate)
+
+    def _backward(self, dy, accumulate):
+        cfg, w, g, s = self.cfg, self.w, self.grads, self.saved
+        T, k = dy.shape[0], cfg.top_k
         R = T * k
-        opt = dict(grad_dtype=self.grad_dtype, accumulate=accumulate, stream=stream)
+        opt = dict(grad_dtype=self.grad_dtype, accumulate=accumulate)
         dy_rows, dx_rows = self._new((R, cfg.d)), self._new((R, cfg.d))
         dgate_rows = self._new(R, torch.float32)
         dx, dx_router, dx_shared = torch.empty_like(dy), torch.empty_like(dy), None
-        combine_backward(cfg, T, dy, s["slot_pos"], dy_rows, stream=stream)
+        combine_backward(cfg, T, dy, s["slot_pos"], dy_rows)
         experts_backward(self.routed, R, s["counts"], s["x_rows"], s["gate_rows"], w["W1"], w["W3"], w["W2"], s["gu"],
                          dy_rows, dx_rows, dgate_rows, g["W1"], g["W3"], g["W2"], self.ws, **opt)
-        self._note_status(T, stream)
+        self._note_status(T)
         if self.shared is not None:
             dx_shared = torch.empty_like(dy)
             experts_backward(self.shared, T, s["shared_counts"], s["x"], None, w["Ws1"], w["Ws3"], w["Ws2"],
                              s["shared_gu"], dy, dx_shared, None, g["Ws1"], g["Ws3"], g["Ws2"], self.ws, **opt)
         route_backward(cfg, T, s["x"], w["W_r"], s["logits"], s["idx"], dgate_rows, s["slot_pos"], dx_router, g["W_r"],
                        self.ws, **opt)
-        dispatch_backward(cfg, T, dx_rows, s["slot_pos"], dx_shared, dx_router, dx, stream=stream)
+        dispatch_backward(cfg, T, dx_rows, s["slot_pos"], dx_shared, dx_router, dx)
         return dx
 
     def clip(self, max_norm, group=None, stream=None):
         """Scales the gradients in place to a global norm of at most max_norm;
         returns the norm before (an fp32 tensor of one element). group: a
         torch.distributed group over whose ranks the gradients are spread."""
-        grad_norm(self.grad_list, self.sumsq, self.clip_ws, stream=stream)
-        if group is not None:
-            import torch.distributed as dist
-            dist.all_reduce(self.sumsq, group=group)
-        grad_clip(self.grad_list, self.sumsq, max_norm, self.norm, stream=stream)
+        with _on(stream):
+            grad_norm(self.grad_list, self.sumsq, self.clip_ws)
+            if group is not None:
+                import torch.distributed as dist
+                dist.all_reduce(self.sumsq, group=group)
+            grad_clip(self.grad_list, self.sumsq, max_norm, self.norm)
         return self.norm
 
     def balance(self, gamma, stream=None):
@@ -178,4 +200,5 @@ class TrainLayer:
         s = self.saved
         if s["x"].shape[0] == 0:  # no loads to balance
             return
-        bias_update(self.cfg, s["x"].shape[0], s["counts"], gamma, self.w["b"], stream=stream)
+        with _on(stream):
+            bias_update(self.cfg, s["x"].shape[0], s["counts"], gamma, self.w["b"])

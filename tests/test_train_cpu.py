@@ -217,3 +217,14 @@ def test_train_layer_steps_come_in_order():
     layer.saved = dict(x=torch.zeros(4, 64, dtype=torch.bfloat16))
     with pytest.raises(ValueError, match="bias"):
         layer.balance(1e-3)
+
+
+def test_grad_lists_refuse_overlapping_destinations():
+    t, u = torch.zeros(64), torch.zeros(64)
+    moe.GradList([t[:32], t[32:], u])
+    moe.GradList([t, t], [u, torch.zeros(64)])                 # read twice, written apart
+    moe.GradList([t[:0], t[:0], t])
+    for srcs, dsts in (([t, u, t], None), ([t[:33], t[32:]], None), ([t, u], [u, torch.zeros(64)]),
+                       ([t[:32]], [t[16:48]]), ([t[:32], t[32:]], [u[:32], u[16:48]])):
+        with pytest.raises(ValueError, match="overlap"):
+            moe.GradList(srcs, dsts)

@@ -824,6 +824,28 @@ def test_training_steps_on_two_streams_at_once():
         assert layer.device_status() == 0
 
 
+@pytest.mark.parametrize("handle", [False, True])
+def test_training_step_on_a_stream_that_is_not_current(handle):
+    """Buffers of a step on another stream are not handed to the current stream's work while it runs."""
+    cfg, w, x, dy = layer_case(400, 256, 384, 16, 1, 4, "sigmoid", True, "bf16", seed=3)
+    alone = TrainLayer(cfg, w, max_tokens=400)
+    want = alone.forward(x), alone.backward(dy)
+    layer, side = TrainLayer(cfg, w, max_tokens=400), torch.cuda.Stream()
+    arg = side.cuda_stream if handle else side
+    torch.cuda.synchronize()
+    for _ in range(8):
+        y = layer.forward(x, stream=arg)
+        dx = layer.backward(dy, stream=arg)
+        norm = layer.clip(1e9, stream=arg)
+        for _ in range(40):  # the current stream overwrites whatever the allocator gives it
+            torch.full((400 * 4, 256), float("nan"), dtype=torch.bfloat16, device="cuda")
+    torch.cuda.synchronize()
+    assert torch.equal(y, want[0]) and torch.equal(dx, want[1])
+    assert torch.equal(norm, alone.clip(1e9))
+    for n, t in layer.grads.items():
+        assert torch.equal(t, alone.grads[n]), n
+
+
 def test_training_step_keeps_the_status_of_its_calls():
     cfg, w, x, dy = layer_case(40, 64, 64, 8, 0, 2, "sigmoid", True, "bf16")
     layer = TrainLayer(cfg, w, max_tokens=40)
