@@ -385,29 +385,32 @@ class GradList:
         if len(self.dsts) != len(self.srcs):
             raise ValueError(f"{len(self.srcs)} gradients but {len(self.dsts)} destinations")
         self.table = (GradTensor * len(self.srcs))()
-        for entry, src, dst in zip(self.table, self.srcs, self.dsts):
-            if src.dtype not in dtypes or dst.dtype != src.dtype:
-                raise ValueError(f"gradients are fp32 or bf16, clipped into the same type: got {src.dtype}, {dst.dtype}")
-            if not src.is_contiguous() or not dst.is_contiguous() or dst.numel() != src.numel():
-                raise ValueError("a gradient and its destination are contiguous and of one size")
-            entry.src, entry.dst = src.data_ptr(), dst.data_ptr()
-            entry.numel, entry.dtype = src.numel(), dtypes[src.dtype]
-        # a destination that another gradient is read from or written to would be scaled twice, or too early
         spans = []
-        for i, (src, dst) in enumerate(zip(self.srcs, self.dsts)):
-            size = src.numel() * src.element_size()
+        for i, (entry, src, dst) in enumerate(zip(self.table, self.srcs, self.dsts)):
+            dt, n = src.dtype, src.numel()
+            if dt not in dtypes or dst.dtype != dt:
+                raise ValueError(f"gradients are fp32 or bf16, clipped into the same type: got {dt}, {dst.dtype}")
+            if not src.is_contiguous() or dst is not src and (not dst.is_contiguous() or dst.numel() != n):
+                raise ValueError("a gradient and its destination are contiguous and of one size")
+            entry.src = at = src.data_ptr()
+            entry.dst = to = dst.data_ptr()
+            entry.numel, entry.dtype = n, dtypes[dt]
+            size = n * src.element_size()
             if size:
-                spans.append((dst.data_ptr(), dst.data_ptr() + size, True, i))
-                if src.data_ptr() != dst.data_ptr():
-                    spans.append((src.data_ptr(), src.data_ptr() + size, False, i))
+                spans.append((to, to + size, True, i))
+                if at != to:
+                    spans.append((at, at + size, False, i))
+        # a destination that another gradient is read from or written to would be scaled twice, or too early
         spans.sort()
-        end = {True: (0, -1), False: (0, -1)}  # of the destinations and sources so far: the furthest, and its gradient
+        past, past_written, of, of_written = 0, 0, -1, -1  # ends of the spans so far, and whose they are
         for lo, hi, written, i in spans:
-            for kind, (past, j) in end.items():
-                if lo < past and (written or kind):
-                    raise ValueError(f"gradients {j} and {i} overlap where one of them is written")
-            if hi > end[written][0]:
-                end[written] = (hi, i)
+            if lo < past_written or written and lo < past:
+                raise ValueError(f"gradients {of_written if lo < past_written else of} and {i} overlap where one of "
+                                 f"them is written")
+            if hi > past:
+                past, of = hi, i
+            if written and hi > past_written:
+                past_written, of_written = hi, i
 
     def __len__(self):
         return len(self.srcs)

@@ -883,6 +883,31 @@ def test_training_step_in_a_graph():
             assert torch.equal(layer.grads[n], eager.grads[n]), n
 
 
+def test_two_graphs_of_fp32_steps_share_a_layer():
+    """Two captures of one layer's step, of different token counts, replayed in turn on one workspace."""
+    cfg, w, x, dy = layer_case(600, 136, 264, 12, 1, 3, "softmax", False, "f32", seed=5)
+    layer, eager = (TrainLayer(cfg, w, max_tokens=600) for _ in range(2))
+    side = torch.cuda.Stream()
+    layer.forward(x), layer.backward(dy)
+    torch.cuda.synchronize()
+    graphs = []
+    for T in (600, 37):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            y = layer.forward(x[:T])
+            dx = layer.backward(dy[:T], accumulate=True)
+        graphs.append((T, graph, y, dx))
+    for g in (*layer.grads.values(), *eager.grads.values()):
+        g.zero_()
+    for T, graph, y, dx in graphs + graphs[::-1]:
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, eager.forward(x[:T])) and torch.equal(dx, eager.backward(dy[:T], accumulate=True))
+    for n in layer.grads:
+        assert torch.equal(layer.grads[n], eager.grads[n]), n
+    assert layer.device_status() == 0
+
+
 def test_combine_and_dispatch_backward_are_each_others_transpose():
     """<dispatch_backward(rows), v> = <rows, combine_backward(v)> exactly on small whole numbers, with
     dropped pairs (an invalid expert) left out of both."""
