@@ -240,6 +240,36 @@ def test_experts_backward_in_tiles_that_fill_the_gpu():
             moe.experts_backward_workspace_size(small.cfg, 3131))
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_experts_beyond_2_31_elements(dtype):
+    """The last rows of a block whose gu and scratch rows lie past 2^31 elements; the first group's rows are zero."""
+    R, tail, d, F = 530_000, 500, 64, 4104
+    b = Block([1, tail], d, F, dtype, seed=31)
+    b.forward()
+    dt = DT[dtype]
+    x, dy, y, dx = (torch.zeros((R, d), dtype=dt, device="cuda") for _ in range(4))
+    gate, dgate = torch.ones(R, device="cuda"), torch.empty(R, device="cuda")
+    x[-tail:], dy[-tail:], gate[-tail:] = b.x[1:], b.dy[1:], b.gate[1:]
+    gu = torch.empty((R, 2 * F), dtype=dt, device="cuda")
+    counts = torch.tensor([R - tail, tail], dtype=torch.int32, device="cuda")
+    ws = torch.empty(max(moe.experts_workspace_size(b.cfg, R), moe.experts_backward_workspace_size(b.cfg, R)),
+                     dtype=torch.uint8, device="cuda")
+    moe.experts_train(b.cfg, R, counts, x, gate, *b.weights(), y, gu, ws)
+    assert gu.numel() > 2 ** 32 and not gu[:R - tail].any() and not y[:R - tail].any()
+    small_y, small_gu = b.forward()
+    tol = BF16_TWO if dtype == "bf16" else 2 * (d + F + 16) * 2.0 ** -23  # two sums of the same terms, or a rounding
+    assert rel(gu[-tail:], small_gu[1:].double()) <= tol and rel(y[-tail:], small_y[1:].double()) <= tol
+    dW = [torch.empty_like(w) for w in b.weights()]
+    moe.experts_backward(b.cfg, R, counts, x, gate, *b.weights(), gu, dy, dx, dgate, *dW, ws)
+    assert moe.device_status(b.cfg, R, ws) == 0
+    b.gu = torch.cat([small_gu[:1], gu[-tail:]])
+    ref, mag = b.exact()
+    out = dict(dx=dx[-tail:], dgate=dgate[-tail:], dW1=dW[0][1], dW3=dW[1][1], dW2=dW[2][1])
+    part = lambda t: {n: v[1:] if v.shape[0] == tail + 1 else v[1] for n, v in t.items()}  # noqa: E731
+    check_block(b, out, part(ref), part(mag))
+    assert not dx[:R - tail].any() and not any(w[0].any() for w in dW)
+
+
 def test_experts_backward_without_gates():
     b = Block([33, 0, 70], 136, 264, gate=False, seed=3)
     check_block(b, b.backward(), *b.exact())
