@@ -229,7 +229,15 @@ struct WgradArgs {
   // not wait for it to end before its own work.
   bool independent;
   int max_pairs;     // CTA pairs to use at most (0: all)
+  bool beside;       // an independent kernel follows that may run beside this one
 };
+// How the router's two bf16 products share the CTA pairs: the token ranges of dW_r
+// (at most most_splits, whatever the tokens up to p.T), and the pairs of dx when it
+// runs beside dW_r (0: before it).
+struct RoutePlan {
+  int splits, most_splits, dx_pairs;
+};
+RoutePlan plan_route_products(const Problem& p);
 cudaError_t launch_wgrad_tc(const WgradArgs& a, cudaStream_t s);
 int dgate_planes(const Problem& p);
 int simt_train_tile(const Problem& p);  // fp32: rows of a tile of the training forward's products

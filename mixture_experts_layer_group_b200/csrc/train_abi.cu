@@ -58,20 +58,25 @@ RouteLayout make_route_layout(const Problem& p) {
   L.ld = (p.N + 7) / 8 * 8;
   L.ld_t = (p.T + 7) / 8 * 8;
   L.splits = 1;
-  // dW_r is N x d summed over all tokens: few tiles with a long sum. The tokens
-  // are split so that about one tile of 256 per CTA pair runs at a time (bf16,
-  // each over 256 tokens or more), or four tiles of 64 per SM (fp32).
-  const int side = tc ? 256 : 64, least = tc ? 256 : 64;
-  const int64_t tiles = (int64_t)((p.N + side - 1) / side) * ((p.d + side - 1) / side);
-  int64_t n = (tc ? kRouterTargetSms / 2 : 4 * kRouterTargetSms) / tiles;
-  if (n > p.T / least) n = p.T / least;
-  if (n > kMaxRouteSplits) n = kMaxRouteSplits;
-  if (n > 1) L.splits = (int)n;
+  int64_t planes = 1;
+  if (tc) {
+    const RoutePlan plan = plan_route_products(p);
+    L.splits = plan.splits;
+    planes = plan.most_splits;  // (a workspace for T tokens also holds a call of fewer)
+  } else {
+    // dW_r is N x d summed over all tokens, few tiles with a long sum: the tokens
+    // are split so that there are about four tiles of 64 x 64 per SM
+    const int64_t tiles = (int64_t)((p.N + 63) / 64) * ((p.d + 63) / 64);
+    planes = 4 * kRouterTargetSms / tiles;
+    if (planes > p.T / 64) planes = p.T / 64;
+    if (planes > kMaxRouteSplits) planes = kMaxRouteSplits;
+    if (planes > 1) L.splits = (int)planes;
+  }
   L.status = take(256);
   L.tables = take(kRouteTables * 4);
   L.dz = take((size_t)p.T * L.ld * p.elem);
   L.dz_t = take(tc ? (size_t)p.N * L.ld_t * 2 : 0);
-  L.planes = take(L.splits > 1 ? (size_t)L.splits * p.N * p.d * 4 : 0);
+  L.planes = take(planes > 1 ? (size_t)planes * p.N * p.d * 4 : 0);
   L.total = off;
   return L;
 }
