@@ -307,6 +307,14 @@ MOE_DEV void tmem_dealloc_pair(uint32_t taddr, uint32_t ncols) {
 // until the predecessor grid has completed and its writes are visible (a
 // no-op without the attribute); griddep_launch_dependents lets the
 // dependent grid start once every CTA of this grid has called it or exited.
+// (What a programmatic predecessor wrote is not read through __ldg or a const
+// __restrict__ pointer: the compiler may take such data as constant for the whole
+// kernel and move the read in front of the wait. Plain loads and this stay behind.)
+MOE_DEV int32_t ld_after_wait(const int32_t* p) {
+  int32_t v;
+  asm volatile("ld.global.s32 %0, [%1];" : "=r"(v) : "l"(p));
+  return v;
+}
 MOE_DEV void griddep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 MOE_DEV void griddep_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 

@@ -303,11 +303,11 @@ MOE_DEV Unit decode_unit(const TcParams& p, int u) {
   int lo = 0, hi = p.N;  // largest g with unit_base[g] <= u
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
-    if (__ldg(p.unit_base + mid) <= u) lo = mid;
+    if (ld_after_wait(p.unit_base + mid) <= u) lo = mid;
     else hi = mid - 1;
   }
-  const int local = u - __ldg(p.unit_base + lo);
-  const int rows = __ldg(p.grp_rows + lo);
+  const int local = u - ld_after_wait(p.unit_base + lo);
+  const int rows = ld_after_wait(p.grp_rows + lo);
   // a group's rows split into nc chunks of (almost) equal size, so the
   // chunks that share a weight tile run at the same pace and keep reading
   // its lines from L2 together
@@ -722,7 +722,7 @@ __global__ void __launch_bounds__(Plan<FP8>::kThreads, 1)
   if (!is_down(MODE)) griddep_wait();
   if constexpr (is_dx(MODE))
     if (p.beside && threadIdx.x == 0) griddep_launch_dependents();
-  const int total_units = __ldg(p.unit_base + p.N + 1);
+  const int total_units = ld_after_wait(p.unit_base + p.N + 1);
   const uint32_t tmem_base = sh.tmem_base;
   volatile int* abort_flag = &sh.abort_flag;
   auto peer = [&](const void* local) { return map_to_rank(smem_u32(local), rank ^ 1u); };
@@ -808,7 +808,7 @@ __global__ void __launch_bounds__(Plan<FP8>::kThreads, 1)
           un = decode_unit(p, u);
           for (int* v : {&un.g, &un.f, &un.tok0, &un.ntok, &un.nchunks}) *v = __shfl_sync(0xffffffffu, *v, 0);
           K = un.g == p.N ? p.k_shared : p.k_routed;
-          row0 = __shfl_sync(0xffffffffu, __ldg(p.grp_row0 + un.g), 0);
+          row0 = __shfl_sync(0xffffffffu, ld_after_wait(p.grp_row0 + un.g), 0);
         }
         const int seg = (K + kBK - 1) / kBK;  // K blocks of a segment
         const int nk = k_blocks<MODE>(seg);
@@ -1037,7 +1037,7 @@ __global__ void __launch_bounds__(Plan<FP8>::kThreads, 1)
             sh.epi_info[i & 1][1] = un.f;
             sh.epi_info[i & 1][2] = un.tok0;
             sh.epi_info[i & 1][3] = un.ntok;
-            sh.epi_info[i & 1][4] = un.g == p.N ? un.tok0 : __ldg(p.grp_row0 + un.g) + un.tok0;
+            sh.epi_info[i & 1][4] = un.g == p.N ? un.tok0 : ld_after_wait(p.grp_row0 + un.g) + un.tok0;
             uint32_t mask, base, stride;
             plan.place(mma_n<FP8>(un.ntok), mask, base, stride);
             bool ok = true;

@@ -271,8 +271,7 @@ __global__ void __launch_bounds__(kThreads + 32) square_sum_kernel(const __grid_
   if (threadIdx.x == 0) part[blockIdx.x] = sum;
 }
 
-__global__ void __launch_bounds__(kThreads) sum_parts_kernel(const double* __restrict__ part, int64_t n,
-                                                             double* __restrict__ sumsq) {
+__global__ void __launch_bounds__(kThreads) sum_parts_kernel(const double* part, int64_t n, double* sumsq) {
   griddep_launch_dependents();
   griddep_wait();
   double sum = 0.0;
@@ -311,8 +310,7 @@ MOE_DEV void scale_elements(const uint8_t* src, uint8_t* dst, int64_t from, int6
 
 template <int CAP>
 __global__ void __launch_bounds__(kThreads + 32) clip_kernel(const __grid_constant__ Table<CAP> t,
-                                                             const double* __restrict__ sumsq, float max_norm,
-                                                             float* __restrict__ norm_out) {
+                                                             const double* sumsq, float max_norm, float* norm_out) {
   griddep_wait();
   const double norm = sqrt(*sumsq);
   // a norm that is not finite leaves the gradients as they are

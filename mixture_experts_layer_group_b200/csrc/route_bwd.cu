@@ -150,14 +150,14 @@ __global__ void __launch_bounds__(kDzThreads) route_dz_kernel(const __grid_const
 
 // dW = sum over the planes in order, rounded once (or added to an fp32 dW): two
 // planes of 256 x 7168 4.7 us, mostly the launch and one round of loads from L2.
-__global__ void __launch_bounds__(256) join_planes_kernel(const float4* __restrict__ planes, int n, int64_t vecs,
-                                                          void* __restrict__ dW, int f32, int accumulate) {
+__global__ void __launch_bounds__(256) join_planes_kernel(const float4* planes, int n, int64_t vecs, void* dW, int f32,
+                                                          int accumulate) {
   griddep_wait();
   const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
   if (i >= vecs) return;
   float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
   for (int q = 0; q < n; ++q) {
-    const float4 w = __ldg(planes + q * vecs + i);
+    const float4 w = planes[q * vecs + i];
     v.x += w.x;
     v.y += w.y;
     v.z += w.z;

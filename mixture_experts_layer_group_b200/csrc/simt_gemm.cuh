@@ -44,7 +44,7 @@ struct Block {
       const int t = threadIdx.x + i * kThreads;
       const int r = r0 + (o.ks == 1 ? t / (BK / 4) : t % (ROWS / 4) * 4);
       const int k = k0 + (o.ks == 1 ? t % (BK / 4) * 4 : t / (ROWS / 4));
-      v[i] = t < kAll && r < o.rows && k < o.len ? __ldg(reinterpret_cast<const float4*>(o.p + r * o.rs + k * o.ks))
+      v[i] = t < kAll && r < o.rows && k < o.len ? *reinterpret_cast<const float4*>(o.p + r * o.rs + k * o.ks)
                                      : make_float4(0.f, 0.f, 0.f, 0.f);
     }
   }

@@ -209,7 +209,7 @@ __global__ void __launch_bounds__(kThreads, 2) fwd_simt_kernel(FwdParams p) {
 }
 
 // h = silu(g) u, four features per thread.
-__global__ void __launch_bounds__(256) swiglu_kernel(const float* __restrict__ gu, int F, int64_t vecs, float* __restrict__ h) {
+__global__ void __launch_bounds__(256) swiglu_kernel(const float* gu, int F, int64_t vecs, float* h) {
   griddep_launch_dependents();
   griddep_wait();
   const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
@@ -348,18 +348,18 @@ cudaError_t launch_dw(const DwParams& p, cudaStream_t s) {
 
 // 32 rows per CTA; warp w adds planes w, w + 8, ..., then the warps' sums are
 // added in order (so that a row's planes are eight short chains of loads).
-__global__ void __launch_bounds__(256) dgate_reduce_kernel(const float* __restrict__ part, int planes, int64_t rows,
-                                                           const int32_t* __restrict__ units, float* __restrict__ dgate) {
+__global__ void __launch_bounds__(256) dgate_reduce_kernel(const float* part, int planes, int64_t rows, const int32_t* units,
+                                                           float* dgate) {
   griddep_launch_dependents();
   griddep_wait();
-  if (__ldg(units) == 0) return;  // counts that do not add up: no row was computed
+  if (*units == 0) return;  // counts that do not add up: no row was computed
   __shared__ float sums[8][32];
   const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t r = (int64_t)blockIdx.x * 32 + lane;
   float v = 0.f;
   if (r < rows) {
 #pragma unroll 8
-    for (int i = w; i < planes; i += 8) v += __ldg(part + i * rows + r);
+    for (int i = w; i < planes; i += 8) v += part[i * rows + r];
   }
   sums[w][lane] = v;
   __syncthreads();

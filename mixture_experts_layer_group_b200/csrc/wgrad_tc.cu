@@ -111,8 +111,8 @@ MOE_DEV Unit decode(const Params& p, int u) {
   if (u >= p.units) return t;
   t.g = u / p.units_per_group;
   int left = u - t.g * p.units_per_group;
-  t.row0 = __ldg(p.grp_row0 + t.g);
-  t.rows = __ldg(p.grp_rows + t.g);
+  t.row0 = ld_after_wait(p.grp_row0 + t.g);
+  t.rows = ld_after_wait(p.grp_rows + t.g);
   while (t.mat < p.nmat - 1 && left >= p.mat[t.mat].mt * p.mat[t.mat].nt) {
     left -= p.mat[t.mat].mt * p.mat[t.mat].nt;
     ++t.mat;

@@ -379,6 +379,23 @@ def test_experts_backward_is_deterministic_and_takes_any_stream(dtype):
         assert torch.equal(first[name], second[name]), name
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("counts,d,F", [SHAPES[1], SHAPES[6], SHAPES[-1]], ids=[IDS[1], IDS[6], IDS[-1]])
+def test_experts_do_not_read_what_the_workspace_held(counts, d, F, dtype):
+    b = Block(counts, d, F, dtype, seed=41)
+    clean, full = (torch.full((max(b.ws().numel(), b.ws(False).numel()),), fill, dtype=torch.uint8, device="cuda")
+                   for fill in (0, 255))
+    got = []
+    for ws in (clean, full, full):
+        y, gu = torch.empty_like(b.x), torch.empty_like(b.gu)
+        moe.experts_train(b.cfg, b.R, b.dcounts, b.x, b.gate, *b.weights(), y, gu, ws)
+        got.append(dict(b.backward(ws=ws), y=y, gu=gu))
+        ws.fill_(255)
+    for other in got[1:]:
+        for name, t in got[0].items():
+            assert torch.equal(t, other[name]), name
+
+
 def test_experts_backward_in_a_graph():
     b = Block([300, 0, 17, 130], 264, 520, seed=9)
     want = b.backward()
@@ -662,6 +679,24 @@ def test_clip_at_odd_offsets(dtype, shift):
     _, norm = clip(srcs, max_norm, dsts)
     check_clip(srcs, dsts, before, norm, max_norm)
     assert bool((dst[~used] == 5.0).all())
+
+
+@pytest.mark.parametrize("n", [1000, 1 << 20, 1 << 26])
+def test_clip_reads_the_sum_of_its_own_norm(n):
+    """The clip's launch overlaps the norm's end: it must not read what the sum's buffer held before."""
+    t = torch.full((n,), 2.0 ** -10, device="cuda")
+    grads = moe.GradList([t], [torch.empty_like(t)])
+    ws = torch.empty(moe.grad_norm_workspace_size(grads), dtype=torch.uint8, device="cuda")
+    want = 2.0 ** -10 * n ** 0.5
+    for old in (float("nan"), 0.0, 1e30):
+        sumsq = torch.full((1,), old, dtype=torch.float64, device="cuda")
+        norm = torch.empty(1, device="cuda")
+        ws.fill_(255)
+        torch.cuda.synchronize()
+        moe.grad_norm(grads, sumsq, ws)
+        moe.grad_clip(grads, sumsq, want / 4, norm)
+        assert abs(float(norm) - want) <= 2.0 ** -20 * want, old
+        assert bool(((grads.dsts[0] - 2.0 ** -12).abs() <= 2.0 ** -30).all()), old
 
 
 def test_clip_mixes_types_and_is_deterministic():
