@@ -35,7 +35,10 @@ def _on(stream, *tensors):
     if stream is None:
         yield
         return
-    on = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(stream)
+    if isinstance(stream, torch.cuda.Stream):
+        on = stream
+    else:  # a handle; 0 is the default stream
+        on = torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream()
     with torch.cuda.stream(on):
         yield
     for t in tensors:

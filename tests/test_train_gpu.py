@@ -911,6 +911,18 @@ def test_training_step_on_a_stream_that_is_not_current(handle):
         assert torch.equal(t, alone.grads[n]), n
 
 
+def test_training_step_on_the_default_streams_handle():
+    cfg, w, x, dy = layer_case(40, 64, 64, 8, 1, 2, "sigmoid", True, "bf16", seed=4)
+    layer, other = TrainLayer(cfg, w, max_tokens=40), TrainLayer(cfg, w, max_tokens=40)
+    want = other.forward(x), other.backward(dy)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(torch.cuda.Stream()):
+        got = layer.forward(x, stream=0), layer.backward(dy, stream=0)
+        bits = layer.device_status(stream=0)
+    torch.cuda.synchronize()
+    assert bits == 0 and all(torch.equal(a, b) for a, b in zip(want, got))
+
+
 def test_training_step_keeps_the_status_of_its_calls():
     cfg, w, x, dy = layer_case(40, 64, 64, 8, 0, 2, "sigmoid", True, "bf16")
     layer = TrainLayer(cfg, w, max_tokens=40)
