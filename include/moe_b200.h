@@ -120,8 +120,9 @@ typedef struct moe_cfg {
 
 /*
  * Bytes of device workspace that moe_route, moe_dispatch and moe_forward
- * need for T tokens. Returns MOE_ERR_INVALID_ARG for an invalid cfg or
- * T < 0, MOE_ERR_UNSUPPORTED outside the implemented range.
+ * need for T tokens; a workspace of that size also holds calls of fewer.
+ * Returns MOE_ERR_INVALID_ARG for an invalid cfg or T < 0,
+ * MOE_ERR_UNSUPPORTED outside the implemented range.
  */
 MOE_API moe_status moe_workspace_size(const moe_cfg* cfg, int64_t T, size_t* bytes);
 

@@ -47,11 +47,13 @@ struct Layout {
   size_t grp_row0, grp_rows, unit_base1, unit_base2, perm, slot_pos, gate_perm;
   size_t x_perm, h_perm, h_sh, y_rows, x_stage[2], y_stage[2];
   size_t total, total_host;
+  size_t logits_bytes;
   int64_t n_chunks;
 };
 
 moe_status make_problem(const moe_cfg* cfg, int64_t T, Problem* p);
-Layout make_layout(const Problem& p);
+// `planes`: of partial logits; 0 for the router_k_splits(p) that a call of p.T tokens needs.
+Layout make_layout(const Problem& p, int planes = 0);
 
 struct DispatchBuffers {
   const int32_t* idx;
@@ -100,8 +102,11 @@ bool make_tmap_nd(CUtensorMap* m, const void* base, int elem_bytes, int rank, co
 // deterministic bits and equal S gives equal bits at any T. `status` (may be
 // null) receives MOE_DEV_* bits; logits_out [T, N] (may be null) the logits.
 constexpr int kRouterTargetSms = 148;
+constexpr int kMaxRouterSplits = 16;
+constexpr int kRouterTileTokens = 64;  // tokens per CTA tile: S changes with T in steps of these
 int router_k_splits(const Problem& p);
-size_t router_scratch_bytes(const Problem& p);
+// Tokens from which S is 1, however many more there are.
+int64_t router_unsplit_tokens(const Problem& p);
 cudaError_t launch_router(const Problem& p, const void* x, const void* W_r, const float* b,
                           float* logits, size_t logits_bytes, int32_t* idx, float* gates,
                           unsigned* status, cudaStream_t s, int splits = 0, float* logits_out = nullptr);

@@ -111,7 +111,7 @@ moe_status make_problem(const moe_cfg* cfg, int64_t T, Problem* p) {
   return MOE_OK;
 }
 
-Layout make_layout(const Problem& p) {
+Layout make_layout(const Problem& p, int planes) {
   Layout L{};
   size_t off = 0;
   auto take = [&](size_t bytes) {
@@ -123,7 +123,8 @@ Layout make_layout(const Problem& p) {
   L.n_chunks = (T + kChunkTokens - 1) / kChunkTokens;
   L.status = take(256);
   L.sched = take(256);
-  L.logits = take(router_scratch_bytes(p));
+  L.logits_bytes = (size_t)(planes > 0 ? planes : router_k_splits(p)) * (size_t)T * (size_t)N * sizeof(float);
+  L.logits = take(L.logits_bytes);
   L.idx = take((size_t)R * 4);
   L.gates = take((size_t)R * 4);
   L.chunk_counts = take((size_t)L.n_chunks * N * 4);
@@ -152,6 +153,25 @@ Layout make_layout(const Problem& p) {
 
 namespace {
 
+// Bytes that every call of at most p.T tokens fits in. A layout by itself does not
+// always grow with T: the router's planes get fewer where more tokens fill the GPU
+// (63 experts of d 1280: 17024 tokens take 36 MB more than 17056). Between those
+// steps it grows, so the last token of each tile is looked at, down to where
+// even the most planes would fit.
+size_t workspace_bytes(Problem p, size_t Layout::*total) {
+  size_t most = make_layout(p).*total;
+  int64_t t = (p.T - 1) / kRouterTileTokens * kRouterTileTokens;
+  const int64_t split = router_unsplit_tokens(p);
+  for (t = t < split ? t : split; t > 0; t -= kRouterTileTokens) {
+    p.T = t;
+    p.R = t * p.k;
+    if (make_layout(p, kMaxRouterSplits).*total <= most) break;
+    const size_t need = make_layout(p).*total;
+    if (need > most) most = need;
+  }
+  return most;
+}
+
 moe_status check_ws(const Layout& L, void* ws, size_t ws_bytes, size_t need) {
   if (!ws || ws_bytes < need || (reinterpret_cast<uintptr_t>(ws) & 255u)) return MOE_ERR_WORKSPACE;
   (void)L;
@@ -161,7 +181,7 @@ moe_status check_ws(const Layout& L, void* ws, size_t ws_bytes, size_t need) {
 moe_status run_router(const Problem& p, const Layout& L, const void* x, const void* W_r,
                       const float* b, int32_t* idx, float* gates, void* ws, cudaStream_t s,
                       float* logits_out = nullptr) {
-  cudaError_t e = launch_router(p, x, W_r, b, at<float>(ws, L.logits), router_scratch_bytes(p), idx, gates,
+  cudaError_t e = launch_router(p, x, W_r, b, at<float>(ws, L.logits), L.logits_bytes, idx, gates,
                                 at<unsigned>(ws, L.status), s, 0, logits_out);
   return e == cudaSuccess ? MOE_OK : cuda_fail(e);
 }
@@ -637,7 +657,7 @@ moe_status moe_workspace_size(const moe_cfg* cfg, int64_t T, size_t* bytes) {
   moe_status st = make_problem(cfg, T, &p);
   if (st != MOE_OK) return st;
   if (!bytes) return MOE_ERR_INVALID_ARG;
-  *bytes = make_layout(p).total;
+  *bytes = workspace_bytes(p, &Layout::total);
   return MOE_OK;
 }
 
@@ -646,7 +666,7 @@ moe_status moe_workspace_size_host(const moe_cfg* cfg, int64_t T, size_t* bytes)
   moe_status st = make_problem(cfg, T, &p);
   if (st != MOE_OK) return st;
   if (!bytes) return MOE_ERR_INVALID_ARG;
-  *bytes = make_layout(p).total_host;
+  *bytes = workspace_bytes(p, &Layout::total_host);
   return MOE_OK;
 }
 

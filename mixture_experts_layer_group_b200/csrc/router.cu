@@ -20,7 +20,7 @@
 namespace moe {
 namespace {
 
-constexpr int kLBT = 64;   // tokens per CTA tile
+constexpr int kLBT = kRouterTileTokens;
 constexpr int kLBN = 64;   // experts per CTA tile
 constexpr int kLBK = 32;   // K chunk (one shared-memory buffer)
 constexpr int kLCarry = 4; // chunks summed in fp32 before each fp64 carry (128 K elements)
@@ -398,7 +398,7 @@ int router_k_splits(const Problem& p) {
   const int64_t base = (int64_t)((p.N + kLBN - 1) / kLBN) * ((p.T + kLBT - 1) / kLBT);
   if (base <= 0) return 1;
   int64_t max_s = p.d / (4 * kLBK);
-  if (max_s > 16) max_s = 16;
+  if (max_s > kMaxRouterSplits) max_s = kMaxRouterSplits;
   int best = 1;
   double best_cost = 1e30;
   for (int64_t S = 1; S <= max_s; ++S) {
@@ -413,8 +413,11 @@ int router_k_splits(const Problem& p) {
   return best;
 }
 
-size_t router_scratch_bytes(const Problem& p) {
-  return (size_t)router_k_splits(p) * (size_t)p.T * (size_t)p.N * sizeof(float);
+int64_t router_unsplit_tokens(const Problem& p) {
+  // S splits cost at least base / slots waves per unit of K, one at most that and
+  // another: from 99 waves on none wins the 1 % asked for
+  const int64_t tiles = 99ll * kRouterTargetSms * kLCtasPerSm, experts = (p.N + kLBN - 1) / kLBN;
+  return (tiles + experts - 1) / experts * kLBT;
 }
 
 cudaError_t launch_router(const Problem& p, const void* x, const void* W_r, const float* b,
@@ -424,7 +427,7 @@ cudaError_t launch_router(const Problem& p, const void* x, const void* W_r, cons
   // hold one [T, N] plane of partial logits per split
   const size_t plane = (size_t)p.T * (size_t)p.N * sizeof(float);
   const int S = splits > 0 ? splits : router_k_splits(p);
-  if (S > 16 || (size_t)S * plane > logits_bytes) return cudaErrorInvalidValue;
+  if (S > kMaxRouterSplits || (size_t)S * plane > logits_bytes) return cudaErrorInvalidValue;
   const int k_len = ((p.d + S - 1) / S + kLBK - 1) / kLBK * kLBK;
   dim3 grid((unsigned)((p.N + kLBN - 1) / kLBN), (unsigned)((p.T + kLBT - 1) / kLBT), (unsigned)S);
   static std::mutex mu;
