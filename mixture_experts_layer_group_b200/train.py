@@ -19,6 +19,7 @@ from . import (MOE_BF16, MOE_F32, GradList, MoeCfg, bias_update, combine, combin
                experts_workspace_size, grad_clip, grad_norm, grad_norm_workspace_size, route_backward,
                route_backward_workspace_size, route_train, workspace_size)
 
+_STATUS_BYTES = 256  # of the status word at the head of a workspace, which is aligned to as many
 _DTYPE = {MOE_BF16: torch.bfloat16, MOE_F32: torch.float32}
 
 
@@ -66,12 +67,17 @@ class TrainLayer:
         self.routed = _group_cfg(cfg, cfg.n_routed, cfg.d_ff)
         self.shared = _group_cfg(cfg, 1, cfg.n_shared * cfg.d_ff) if cfg.n_shared else None
         T, R = max_tokens, max_tokens * cfg.top_k
-        sizes = [workspace_size(cfg, T), experts_workspace_size(self.routed, R),
-                 experts_backward_workspace_size(self.routed, R), route_backward_workspace_size(cfg, T)]
+        forward = [workspace_size(cfg, T), workspace_size(cfg, T), experts_workspace_size(self.routed, R)]
+        backward = [experts_backward_workspace_size(self.routed, R), route_backward_workspace_size(cfg, T)]
         if self.shared is not None:
-            sizes += [experts_workspace_size(self.shared, T), experts_backward_workspace_size(self.shared, T)]
-        # the calls of a step follow one another, so one workspace serves them all
-        self.ws = torch.empty(max(sizes), dtype=torch.uint8, device=device)
+            forward.append(experts_workspace_size(self.shared, T))
+            backward.append(experts_backward_workspace_size(self.shared, T))
+        # The calls of a step follow one another, so one buffer serves them all. Each call's workspace starts
+        # behind the status word of the call before, which therefore keeps what its call found.
+        sizes = forward + backward
+        self.ws = torch.empty(max(_STATUS_BYTES * i + n for i, n in enumerate(sizes)), dtype=torch.uint8, device=device)
+        self.call_ws = [self.ws[_STATUS_BYTES * i:] for i in range(len(sizes))]
+        self.forward_calls = len(forward)
         for n, shape in self._weight_shapes().items():
             t = weights[n]
             if tuple(t.shape) != shape or t.dtype != self.dtype or not t.is_contiguous():
@@ -82,7 +88,7 @@ class TrainLayer:
         self.clip_ws = torch.empty(grad_norm_workspace_size(self.grad_list), dtype=torch.uint8, device=device)
         self.sumsq = torch.zeros(1, dtype=torch.float64, device=device)
         self.norm = torch.zeros(1, dtype=torch.float32, device=device)
-        self.status = torch.zeros(1, dtype=torch.int32, device=device)
+        self.status = torch.zeros(len(sizes), dtype=torch.int32, device=device)  # bits seen so far, by call
         self.saved = None
 
     def _weight_shapes(self):
@@ -102,17 +108,21 @@ class TrainLayer:
     def _new(self, shape, dtype=None):
         return torch.empty(shape, dtype=dtype or self.dtype, device=self.device)
 
-    def _note_status(self, T):
-        """Keeps the device-status bits of the call before (the next one on the workspace clears them)."""
+    def _note_status(self, T, first, last):
+        """Keeps the device-status bits of calls first .. last - 1, which the next step's calls overwrite."""
         if T == 0:  # nothing ran
             return
-        self.status.bitwise_or_(self.ws[:4].view(torch.int32))
+        words = self.ws[:_STATUS_BYTES * last].view(torch.int32)[_STATUS_BYTES // 4 * first::_STATUS_BYTES // 4]
+        self.status[first:last].bitwise_or_(words)
 
     def device_status(self, stream=None) -> int:
         """The MOE_DEV_* bits of the calls since the last device_status(), which are then cleared (synchronises)."""
         with _on(stream):
-            bits = int(self.status)
+            words = self.status.tolist()
             self.status.zero_()
+        bits = 0
+        for w in words:
+            bits |= w
         return bits
 
     def forward(self, x, stream=None):
@@ -132,20 +142,20 @@ class TrainLayer:
         y = torch.empty_like(x)
         y_rows = self._new((R, cfg.d))
         offsets = self._new(cfg.n_routed + 1, i32)
-        route_train(cfg, T, x, w["W_r"], w.get("b"), s["idx"], s["gates"], s["logits"], self.ws)
-        self._note_status(T)
+        ws = self.call_ws[:self.forward_calls]
+        route_train(cfg, T, x, w["W_r"], w.get("b"), s["idx"], s["gates"], s["logits"], ws[0])
         dispatch_rows(cfg, T, s["idx"], s["gates"], x, s["counts"], offsets, s["slot_pos"], s["x_rows"],
-                      s["gate_rows"], self.ws)
+                      s["gate_rows"], ws[1])
         experts_train(self.routed, R, s["counts"], s["x_rows"], s["gate_rows"], w["W1"], w["W3"], w["W2"], y_rows,
-                      s["gu"], self.ws)
-        self._note_status(T)
+                      s["gu"], ws[2])
         y_shared = None
         if self.shared is not None:
             s["shared_counts"] = torch.full((1,), T, dtype=i32, device=self.device)
             s["shared_gu"] = self._new((T, 2 * self.shared.d_ff))
             y_shared = self._new((T, cfg.d))
             experts_train(self.shared, T, s["shared_counts"], x, None, w["Ws1"], w["Ws3"], w["Ws2"], y_shared,
-                          s["shared_gu"], self.ws)
+                          s["shared_gu"], ws[3])
+        self._note_status(T, 0, len(ws))
         combine(cfg, T, y_rows, s["slot_pos"], y_shared, y)
         self.saved = s
         return y
@@ -169,16 +179,17 @@ class TrainLayer:
         dy_rows, dx_rows = self._new((R, cfg.d)), self._new((R, cfg.d))
         dgate_rows = self._new(R, torch.float32)
         dx, dx_router, dx_shared = torch.empty_like(dy), torch.empty_like(dy), None
+        ws = self.call_ws[self.forward_calls:]
         combine_backward(cfg, T, dy, s["slot_pos"], dy_rows)
         experts_backward(self.routed, R, s["counts"], s["x_rows"], s["gate_rows"], w["W1"], w["W3"], w["W2"], s["gu"],
-                         dy_rows, dx_rows, dgate_rows, g["W1"], g["W3"], g["W2"], self.ws, **opt)
-        self._note_status(T)
+                         dy_rows, dx_rows, dgate_rows, g["W1"], g["W3"], g["W2"], ws[0], **opt)
+        route_backward(cfg, T, s["x"], w["W_r"], s["logits"], s["idx"], dgate_rows, s["slot_pos"], dx_router, g["W_r"],
+                       ws[1], **opt)
         if self.shared is not None:
             dx_shared = torch.empty_like(dy)
             experts_backward(self.shared, T, s["shared_counts"], s["x"], None, w["Ws1"], w["Ws3"], w["Ws2"],
-                             s["shared_gu"], dy, dx_shared, None, g["Ws1"], g["Ws3"], g["Ws2"], self.ws, **opt)
-        route_backward(cfg, T, s["x"], w["W_r"], s["logits"], s["idx"], dgate_rows, s["slot_pos"], dx_router, g["W_r"],
-                       self.ws, **opt)
+                             s["shared_gu"], dy, dx_shared, None, g["Ws1"], g["Ws3"], g["Ws2"], ws[2], **opt)
+        self._note_status(T, self.forward_calls, len(self.call_ws))
         dispatch_backward(cfg, T, dx_rows, s["slot_pos"], dx_shared, dx_router, dx)
         return dx
 

@@ -1,0 +1,72 @@
+"""TrainLayer's device status: what each call of a step finds reaches the caller."""
+import pytest
+import torch
+
+import mixture_experts_layer_group_b200 as moe
+from mixture_experts_layer_group_b200.train import TrainLayer
+
+pytestmark = pytest.mark.gpu
+T, D, F, N, K = 40, 64, 64, 8, 2
+
+
+@pytest.fixture(autouse=True)
+def _lib():
+    from mixture_experts_layer_group_b200 import build
+    build.build()
+    yield
+    torch.cuda.synchronize()
+
+
+def case(dtype):
+    gen = torch.Generator().manual_seed(1)
+    dt = {"bf16": torch.bfloat16, "f32": torch.float32}[dtype]
+
+    def new(*shape):
+        return (torch.randn(shape, generator=gen) * shape[-1] ** -0.5).to(dt).cuda()
+
+    cfg = moe.make_cfg(d=D, d_ff=F, n_routed=N, n_shared=1, top_k=K, score="sigmoid", normalize=True, dtype=dtype)
+    w = {"W_r": new(N, D), "W1": new(N, F, D), "W3": new(N, F, D), "W2": new(N, D, F), "Ws1": new(F, D),
+         "Ws3": new(F, D), "Ws2": new(D, F)}
+    return TrainLayer(cfg, w, max_tokens=T), new(T, D), new(T, D)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("spoil", ["idx", "counts", "shared_counts"])
+def test_status_of_the_backwards_calls(dtype, spoil):
+    """The router's backward, the routed block's and the shared one's each report what they were given."""
+    layer, x, dy = case(dtype)
+    layer.forward(x), layer.backward(dy)
+    assert layer.device_status() == 0
+    layer.forward(x)
+    if spoil == "idx":
+        layer.saved["idx"][7, 1] = -1  # no expert: this slot has no gradient
+    else:
+        layer.saved[spoil][0] += 1     # counts that do not add up: no row is computed
+    layer.backward(dy)
+    layer.forward(x), layer.backward(dy)  # a clean step afterwards does not hide it
+    assert layer.device_status() == moe.MOE_DEV_BAD_EXPERT
+    assert layer.device_status() == 0
+
+
+def test_status_in_a_graph():
+    layer, x, dy = case("bf16")
+    side = torch.cuda.Stream()
+    layer.forward(x), layer.backward(dy)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        layer.forward(x)
+        layer.backward(dy)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert layer.device_status() == 0
+    good = x.clone()
+    x[3, 5] = float("nan")
+    graph.replay()
+    x.copy_(good)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert layer.device_status() == moe.MOE_DEV_NONFINITE
+    graph.replay()
+    torch.cuda.synchronize()
+    assert layer.device_status() == 0
