@@ -601,8 +601,15 @@ MOE_API moe_status moe_grad_norm(const moe_grad_tensor* tensors, int32_t n, doub
  * gradients stay as they are and the caller sees it in norm_out. A tensor in
  * place that needs no scaling is not touched.
  *   max_norm   >= 0 (infinity: no clipping)
- *   norm_out   [1] fp32 device, or NULL: the norm before clipping
+ *   norm_out   [1] fp32 device, or NULL: the norm before clipping (infinity
+ *              where a finite one is beyond fp32; the gradients are scaled)
+ * A wait that runs out (what sets MOE_DEV_WAIT_TIMEOUT elsewhere) can leave
+ * parts of the gradients unscaled or unwritten: norm_out is then the quiet NaN
+ * with the bits MOE_NORM_INCOMPLETE, which no norm has. A call leaves that mark
+ * where an earlier one left it; the caller overwrites it to start again. In
+ * moe_grad_norm such a wait gives a NaN sumsq, so that nothing is scaled.
  */
+#define MOE_NORM_INCOMPLETE 0x7fc0c11bu
 MOE_API moe_status moe_grad_clip(const moe_grad_tensor* tensors, int32_t n, const double* sumsq, float max_norm,
                                  float* norm_out, void* stream);
 

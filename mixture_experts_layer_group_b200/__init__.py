@@ -20,6 +20,7 @@ MOE_F32, MOE_BF16 = 0, 1
 MOE_SOFTMAX, MOE_SIGMOID = 0, 1
 MOE_GROUP_TOP2_SUM, MOE_GROUP_MAX = 0, 1
 MOE_DEV_WAIT_TIMEOUT, MOE_DEV_BAD_EXPERT, MOE_DEV_DUP_EXPERT, MOE_DEV_TMEM_ALLOC, MOE_DEV_NONFINITE = 1, 2, 4, 8, 16
+MOE_NORM_INCOMPLETE = 0x7fc0c11b
 STATUS_NAMES = {0: "MOE_OK", 1: "MOE_ERR_INVALID_ARG", 2: "MOE_ERR_UNSUPPORTED", 3: "MOE_ERR_WORKSPACE",
                 4: "MOE_ERR_CUDA", 5: "MOE_ERR_DEVICE"}
 EXPORTS = ["moe_workspace_size", "moe_workspace_size_host", "moe_route", "moe_dispatch", "moe_forward",
@@ -433,7 +434,8 @@ def grad_norm(grads: GradList, sumsq, ws, ws_bytes=None, stream=None):
 
 def grad_clip(grads: GradList, sumsq, max_norm, norm_out=None, stream=None):
     """Every gradient times min(1, max_norm / sqrt(sumsq)), into its destination;
-    norm_out [1] fp32 receives the norm before clipping."""
+    norm_out [1] fp32 receives the norm before clipping, or, when a wait ran out and gradients may be
+    unscaled, a NaN with the bits MOE_NORM_INCOMPLETE (which later calls leave until it is overwritten)."""
     _check("moe_grad_clip", lib().moe_grad_clip(grads.table, len(grads), _ptr(sumsq), float(max_norm), _ptr(norm_out),
                                                 _stream(stream)))
 

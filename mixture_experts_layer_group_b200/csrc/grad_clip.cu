@@ -308,34 +308,45 @@ MOE_DEV void scale_elements(const uint8_t* src, uint8_t* dst, int64_t from, int6
   for (int64_t i = from; i < to; i += step) put_element<F32>(dst, i, element<F32>(src, i) * coef);
 }
 
+// A wait that runs out leaves chunks unscaled; norm_out then holds the mark
+// MOE_NORM_INCOMPLETE instead of the norm. CTAs that give up write it with
+// exchanges, and the one exchange that writes the norm puts the mark back when it
+// was there already: whichever order they run in, the mark stays. (So it also stays
+// from one call to the next, until the caller overwrites it.) `first`: this launch
+// writes the norm; it is one of several when the tensors take more tables.
 template <int CAP>
 __global__ void __launch_bounds__(kThreads + 32) clip_kernel(const __grid_constant__ Table<CAP> t,
-                                                             const double* sumsq, float max_norm, float* norm_out) {
+                                                             const double* sumsq, float max_norm, float* norm_out,
+                                                             int first) {
   griddep_wait();
   const double norm = sqrt(*sumsq);
   // a norm that is not finite leaves the gradients as they are
   const bool clip = norm > (double)max_norm && isfinite(norm);
   const float coef = clip ? (float)((double)max_norm / norm) : 1.f;
-  if (norm_out && blockIdx.x == 0 && threadIdx.x == 0) *norm_out = (float)norm;
-  if (!clip && t.inplace) return;
-  (void)stream_chunks(
-      t, true, [&](const Chunk& c) { return !clip && c.src == c.dst; },
-      [&](const Chunk& c) {  // source and destination sit differently within 16 bytes
-        return ((reinterpret_cast<uintptr_t>(c.src) ^ reinterpret_cast<uintptr_t>(c.dst)) & 15u) != 0;
-      },
-      [&](const Piece& p, const uint8_t* data) {
-        switch (p.kind) {
-          case kVecF32: scale_piece<true>(data, (int)p.count, reinterpret_cast<uint4*>(p.dst), coef); break;
-          case kVecBf16: scale_piece<false>(data, (int)p.count, reinterpret_cast<uint4*>(p.dst), coef); break;
-          case kElemF32: scale_elements<true>(p.src, p.dst, threadIdx.x, p.count, kThreads, coef); break;
-          default: scale_elements<false>(p.src, p.dst, threadIdx.x, p.count, kThreads, coef);
-        }
-      },
-      [&](const Chunk& c, int64_t from, int64_t to) {
-        const int64_t i = from + (threadIdx.x & 31);
-        if (c.f32) scale_elements<true>(c.src, c.dst, i, to, 32, coef);
-        else scale_elements<false>(c.src, c.dst, i, to, 32, coef);
-      });
+  unsigned* out = reinterpret_cast<unsigned*>(norm_out);
+  unsigned held = 0;
+  if (out && first && blockIdx.x == 0 && threadIdx.x == 0) held = atomicExch(out, __float_as_uint((float)norm));
+  bool ok = true;
+  if (clip || !t.inplace)
+    ok = stream_chunks(
+        t, true, [&](const Chunk& c) { return !clip && c.src == c.dst; },
+        [&](const Chunk& c) {  // source and destination sit differently within 16 bytes
+          return ((reinterpret_cast<uintptr_t>(c.src) ^ reinterpret_cast<uintptr_t>(c.dst)) & 15u) != 0;
+        },
+        [&](const Piece& p, const uint8_t* data) {
+          switch (p.kind) {
+            case kVecF32: scale_piece<true>(data, (int)p.count, reinterpret_cast<uint4*>(p.dst), coef); break;
+            case kVecBf16: scale_piece<false>(data, (int)p.count, reinterpret_cast<uint4*>(p.dst), coef); break;
+            case kElemF32: scale_elements<true>(p.src, p.dst, threadIdx.x, p.count, kThreads, coef); break;
+            default: scale_elements<false>(p.src, p.dst, threadIdx.x, p.count, kThreads, coef);
+          }
+        },
+        [&](const Chunk& c, int64_t from, int64_t to) {
+          const int64_t i = from + (threadIdx.x & 31);
+          if (c.f32) scale_elements<true>(c.src, c.dst, i, to, 32, coef);
+          else scale_elements<false>(c.src, c.dst, i, to, 32, coef);
+        });
+  if (out && (!ok || held == MOE_NORM_INCOMPLETE)) atomicExch(out, MOE_NORM_INCOMPLETE);
 }
 
 // Runs `go(table, chunks, tensors before it)` over batches of the tensors.
@@ -413,8 +424,8 @@ moe_status clip_batches(const moe_grad_tensor* x, int32_t n, const double* sumsq
   return for_batches<CAP>(x, n, [&](const Table<CAP>& t, int chunks) {
     cudaError_t e = allow_ring<clip_kernel<CAP>>();
     if (e == cudaSuccess)
-      e = launch_after(clip_kernel<CAP>, ctas(chunks), kThreads + 32, kRingBytes, s, t, sumsq, max_norm,
-                       *launched ? nullptr : norm_out);
+      e = launch_after(clip_kernel<CAP>, ctas(chunks), kThreads + 32, kRingBytes, s, t, sumsq, max_norm, norm_out,
+                       (int)!*launched);
     *launched = true;
     return e;
   });
@@ -474,7 +485,7 @@ moe_status moe_grad_clip(const moe_grad_tensor* tensors, int32_t n, const double
     t.chunk0[0] = 0;
     cudaError_t e = allow_ring<clip_kernel<kSmallTable>>();
     if (e == cudaSuccess)
-      e = launch_after(clip_kernel<kSmallTable>, 1, kThreads + 32, kRingBytes, s, t, sumsq, max_norm, norm_out);
+      e = launch_after(clip_kernel<kSmallTable>, 1, kThreads + 32, kRingBytes, s, t, sumsq, max_norm, norm_out, 1);
     if (e != cudaSuccess) return cuda_fail(e);
   }
   return MOE_OK;

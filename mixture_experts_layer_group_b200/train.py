@@ -14,9 +14,9 @@ import contextlib
 
 import torch
 
-from . import (MOE_BF16, MOE_F32, GradList, MoeCfg, bias_update, combine, combine_backward, dispatch_backward,
-               dispatch_rows, experts_backward, experts_backward_workspace_size, experts_train,
-               experts_workspace_size, grad_clip, grad_norm, grad_norm_workspace_size, route_backward,
+from . import (MOE_BF16, MOE_DEV_WAIT_TIMEOUT, MOE_F32, MOE_NORM_INCOMPLETE, GradList, MoeCfg, bias_update, combine,
+               combine_backward, dispatch_backward, dispatch_rows, experts_backward, experts_backward_workspace_size,
+               experts_train, experts_workspace_size, grad_clip, grad_norm, grad_norm_workspace_size, route_backward,
                route_backward_workspace_size, route_train, workspace_size)
 
 _STATUS_BYTES = 256  # of the status word at the head of a workspace, which is aligned to as many
@@ -120,6 +120,10 @@ class TrainLayer:
         with _on(stream):
             words = self.status.tolist()
             self.status.zero_()
+            norm = self.norm.view(torch.int32)
+            if int(norm) == MOE_NORM_INCOMPLETE:  # a clip that gave up since: the mark stays until it is cleared
+                words.append(MOE_DEV_WAIT_TIMEOUT)
+                norm.zero_()
         bits = 0
         for w in words:
             bits |= w
@@ -195,8 +199,10 @@ class TrainLayer:
 
     def clip(self, max_norm, group=None, stream=None):
         """Scales the gradients in place to a global norm of at most max_norm;
-        returns the norm before (an fp32 tensor of one element). group: a
-        torch.distributed group over whose ranks the gradients are spread."""
+        returns the norm before (an fp32 tensor of one element; NaN where the
+        gradients may be unscaled because a wait ran out, which device_status()
+        then reports). group: a torch.distributed group over whose ranks the
+        gradients are spread."""
         with _on(stream):
             grad_norm(self.grad_list, self.sumsq, self.clip_ws)
             if group is not None:

@@ -95,3 +95,31 @@ def test_the_calls_workspaces_hold_what_the_calls_need():
         assert len(layer.call_ws) == len(need)
         for ws, n in zip(layer.call_ws, need):
             assert ws.numel() >= n
+
+
+def test_device_status_reports_a_clip_that_gave_up(monkeypatch):
+    """The norm's buffer keeps the mark over later clips until device_status() has reported it."""
+    layer, gave_up, norms = layer_of(0), [False, True, False], iter((1.0, 2.0, 3.0, 4.0))
+
+    def grad_clip(grads, sumsq, max_norm, norm_out):
+        bits = norm_out.view(torch.int32)
+        held = int(bits) == moe.MOE_NORM_INCOMPLETE
+        norm_out.fill_(next(norms))
+        if held or (gave_up and gave_up.pop(0)):
+            bits.fill_(moe.MOE_NORM_INCOMPLETE)
+
+    monkeypatch.setattr(train, "grad_norm", lambda *args: None)
+    monkeypatch.setattr(train, "grad_clip", grad_clip)
+    assert float(layer.clip(1.0)) == 1.0 and layer.device_status() == 0
+    assert torch.isnan(layer.clip(1.0)).all()
+    assert torch.isnan(layer.clip(1.0)).all()
+    assert layer.device_status() == moe.MOE_DEV_WAIT_TIMEOUT
+    assert layer.device_status() == 0
+    assert float(layer.clip(1.0)) == 4.0 and layer.device_status() == 0
+
+
+def test_the_mark_of_an_incomplete_clip_is_a_quiet_nan():
+    mark = torch.tensor([moe.MOE_NORM_INCOMPLETE], dtype=torch.int32).view(torch.float32)
+    assert torch.isnan(mark).all() and moe.MOE_NORM_INCOMPLETE & 0x7fc00000 == 0x7fc00000
+    with open("include/moe_b200.h") as f:
+        assert f"#define MOE_NORM_INCOMPLETE {moe.MOE_NORM_INCOMPLETE:#010x}u" in f.read()

@@ -70,3 +70,49 @@ def test_status_in_a_graph():
     graph.replay()
     torch.cuda.synchronize()
     assert layer.device_status() == 0
+
+
+def mark_of(norm):
+    return int(norm.view(torch.int32)) == moe.MOE_NORM_INCOMPLETE
+
+
+@pytest.mark.parametrize("sizes", [[], [5], [40000, 16385, 2], [513] * 700], ids=len)
+@pytest.mark.parametrize("inplace,limit", [(True, 0.5), (True, 2.0), (False, 0.5)])
+def test_a_norm_buffer_keeps_the_mark_of_an_incomplete_clip(sizes, inplace, limit):
+    """The kernel writes the norm over anything but the mark, which it leaves, whatever else the call does."""
+    srcs = [torch.full((n,), 2.0 ** -5, device="cuda") for n in sizes]
+    dsts = srcs if inplace else [torch.empty_like(t) for t in srcs]
+    grads = moe.GradList(srcs, None if inplace else dsts)
+    want = 2.0 ** -5 * sum(sizes) ** 0.5
+    ws = torch.empty(moe.grad_norm_workspace_size(grads), dtype=torch.uint8, device="cuda")
+    sumsq = torch.empty(1, dtype=torch.float64, device="cuda")
+    norm = torch.full((1,), float("nan"), device="cuda")
+
+    def clip():
+        moe.grad_norm(grads, sumsq, ws)
+        moe.grad_clip(grads, sumsq, limit * want, norm)
+
+    clip()
+    assert abs(float(norm) - want) <= 2.0 ** -20 * want and not mark_of(norm)
+    for t in srcs:
+        t.fill_(2.0 ** -5)
+    norm.view(torch.int32).fill_(moe.MOE_NORM_INCOMPLETE)
+    for _ in range(2):
+        clip()
+        assert mark_of(norm)
+    for t in dsts:  # the gradients are clipped all the same (a second time in place: within the limit)
+        assert bool(((t - 2.0 ** -5 * min(1.0, limit)).abs() <= 2.0 ** -24).all())
+    norm.zero_()
+    clip()
+    assert not mark_of(norm) and float(norm) <= want * (1 + 2.0 ** -20)
+
+
+def test_a_layer_reports_an_incomplete_clip_once():
+    layer, x, dy = case("bf16")
+    layer.forward(x), layer.backward(dy)
+    before = float(layer.clip(1e9))
+    assert layer.device_status() == 0
+    layer.norm.view(torch.int32).fill_(moe.MOE_NORM_INCOMPLETE)  # as a wait that ran out leaves it
+    assert torch.isnan(layer.clip(1e9)).all()
+    assert layer.device_status() == moe.MOE_DEV_WAIT_TIMEOUT and layer.device_status() == 0
+    assert float(layer.clip(1e9)) == before
