@@ -199,7 +199,7 @@ class TrainLayer:
 
     def clip(self, max_norm, group=None, stream=None):
         """Scales the gradients in place to a global norm of at most max_norm;
-        returns the norm before (an fp32 tensor of one element; NaN where the
+        returns the norm before (a new fp32 tensor of one element; NaN where the
         gradients may be unscaled because a wait ran out, which device_status()
         then reports). group: a torch.distributed group over whose ranks the
         gradients are spread."""
@@ -209,7 +209,7 @@ class TrainLayer:
                 import torch.distributed as dist
                 dist.all_reduce(self.sumsq, group=group)
             grad_clip(self.grad_list, self.sumsq, max_norm, self.norm)
-        return self.norm
+            return self.norm.clone()  # (the buffer is the next clip's)
 
     def balance(self, gamma, stream=None):
         """The loss-free balancing step of the selection bias from the last forward's expert loads."""

@@ -118,6 +118,14 @@ def test_device_status_reports_a_clip_that_gave_up(monkeypatch):
     assert float(layer.clip(1.0)) == 4.0 and layer.device_status() == 0
 
 
+def test_the_norms_of_two_clips_keep_their_values(monkeypatch):
+    layer, values = layer_of(0), iter((1.0, 2.0))
+    monkeypatch.setattr(train, "grad_norm", lambda *args: None)
+    monkeypatch.setattr(train, "grad_clip", lambda grads, sumsq, max_norm, norm_out: norm_out.fill_(next(values)))
+    a, b = layer.clip(1.0), layer.clip(1.0)
+    assert (float(a), float(b)) == (1.0, 2.0)
+
+
 def test_the_mark_of_an_incomplete_clip_is_a_quiet_nan():
     mark = torch.tensor([moe.MOE_NORM_INCOMPLETE], dtype=torch.int32).view(torch.float32)
     assert torch.isnan(mark).all() and moe.MOE_NORM_INCOMPLETE & 0x7fc00000 == 0x7fc00000

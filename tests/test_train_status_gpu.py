@@ -116,3 +116,13 @@ def test_a_layer_reports_an_incomplete_clip_once():
     assert torch.isnan(layer.clip(1e9)).all()
     assert layer.device_status() == moe.MOE_DEV_WAIT_TIMEOUT and layer.device_status() == 0
     assert float(layer.clip(1e9)) == before
+
+
+def test_the_norms_of_two_clips_keep_their_values():
+    layer, x, dy = case("bf16")
+    layer.forward(x), layer.backward(dy)
+    first = layer.clip(1e9)
+    for g in layer.grads.values():
+        g.mul_(4.0)
+    second = layer.clip(1e9, stream=torch.cuda.current_stream())
+    assert float(second) == 4.0 * float(first) > 0.0
