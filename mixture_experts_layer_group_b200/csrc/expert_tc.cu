@@ -260,6 +260,7 @@ struct BwdParams : TcParams {
   int64_t ld_g;
   const __nv_bfloat16* gu;   // [R, 2 F] (kDh)
   float* part;               // [ceil(F / 32), R] partial gate gradients, or null (kDh)
+  int* publish;              // the flag of publish_waited(), or null (kDx)
   int beside;                // the next kernel runs beside this one (kDx)
 };
 template <int MODE>
@@ -720,8 +721,12 @@ __global__ void __launch_bounds__(Plan<FP8>::kThreads, 1)
   // is read only after it has finished; the down GEMM's tables are older than
   // its predecessor and its producer alone waits)
   if (!is_down(MODE)) griddep_wait();
-  if constexpr (is_dx(MODE))
-    if (p.beside && threadIdx.x == 0) griddep_launch_dependents();
+  if constexpr (is_dx(MODE)) {
+    if (threadIdx.x == 64) {  // (not the producer: the release takes about 1 us)
+      if (p.publish && blockIdx.x == 0) publish_waited(p.publish);
+      if (p.beside) griddep_launch_dependents();
+    }
+  }
   const int total_units = ld_after_wait(p.unit_base + p.N + 1);
   const uint32_t tmem_base = sh.tmem_base;
   volatile int* abort_flag = &sh.abort_flag;
@@ -1667,6 +1672,7 @@ cudaError_t launch_experts_backward_tc(const Problem& p, const ExpertsBwdArgs& a
     x.chunk_rows = cm;
     x.tok_rows_routed = x.out_rows_routed = p.R;
     x.a_rows_routed = p.d;
+    x.publish = a.dW1 ? a.sched + kSchedReady : nullptr;
     x.beside = beside;
     const int grid = grid_of(p.d, kTcBN2);
     const int ctas = beside && grid > dx_pairs ? dx_pairs : grid;
@@ -1692,7 +1698,7 @@ cudaError_t launch_experts_backward_tc(const Problem& p, const ExpertsBwdArgs& a
   w.grad_dtype = a.grad_dtype;
   w.accumulate = a.accumulate;
   w.status = a.status;
-  w.independent = a.dx_rows != nullptr;  // of the dx GEMM, which has waited for the dh GEMM
+  w.ready = a.dx_rows ? a.sched + kSchedReady : nullptr;  // the dx GEMM has waited for the dh GEMM
   w.max_pairs = beside ? pairs - dx_pairs : 0;
   err = launch_wgrad_tc(w, s);
   return err == cudaSuccess ? reduce_dgate() : err;

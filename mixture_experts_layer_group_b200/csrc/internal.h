@@ -119,9 +119,10 @@ cudaError_t launch_dispatch(const Problem& p, const DispatchBuffers& db, int bm,
 // Tables of the grouped GEMMs straight from per-group row counts [p.N]
 // (groups in order, rows contiguous): grp_row0, grp_rows and unit bases in db.
 // Counts that are negative or do not sum to p.T set MOE_DEV_BAD_EXPERT and
-// give empty groups; db.status and the kSchedCounters counters of `sched` are
+// give empty groups; db.status and the kSchedCounters counters of `sched` (unit
+// counters, and at kSchedReady the flag from dx to the weight gradients) are
 // cleared first.
-constexpr int kSchedCounters = 4;
+constexpr int kSchedReady = 2, kSchedCounters = 4;
 cudaError_t launch_group_tables(const Problem& p, const int32_t* counts, const DispatchBuffers& db, int bm, int bn1,
                                 int bn2, int* sched, cudaStream_t s);
 
@@ -228,11 +229,11 @@ struct WgradArgs {
   int grad_dtype;
   bool accumulate;   // fp32 only
   unsigned* status;
-  // The kernel before this one in the stream only starts after everything that
-  // this one reads is complete (it waited for that itself before it let its
-  // dependents start), and the two write different buffers: this one then need
-  // not wait for it to end before its own work.
-  bool independent;
+  // Null, or: the kernel before this one in the stream has itself waited for all
+  // that this one reads, sets this flag then (see publish_waited()), and the two
+  // write different buffers. This one need not wait for its end before its own work.
+  const int* ready;
+  int* publish;      // null, or the flag to set for such a kernel behind this one
   int max_pairs;     // CTA pairs to use at most (0: all)
   bool beside;       // an independent kernel follows that may run beside this one
 };
@@ -267,7 +268,8 @@ enum RouteTable : int {
   kRtExperts = 7,                            // [1] N
   kRtSplit0 = 8,                             // [kMaxRouteSplits] token ranges of the split dW_r
   kRtSplitRows = kRtSplit0 + kMaxRouteSplits,
-  kRouteTables = kRtSplitRows + kMaxRouteSplits
+  kRtReady = kRtSplitRows + kMaxRouteSplits, // [1] 0: the flag between the two products
+  kRouteTables
 };
 struct RouteDzArgs {
   const float* logits;      // [T, N]
@@ -303,7 +305,7 @@ struct RouteBwdArgs {
   const __nv_bfloat16* dz16;
   const __nv_bfloat16* dz16_t;
   int64_t ld, ld_t;
-  const int32_t* tables;
+  int32_t* tables;
   int splits;        // token ranges of dW_r, summed from the planes when above 1
   float* planes;     // [splits, N, d] fp32
 };

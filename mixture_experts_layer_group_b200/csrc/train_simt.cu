@@ -230,6 +230,7 @@ struct DxParams {
   float* dx;        // [R, d]
   int d, F;
   int64_t ld;       // a multiple of 4; columns F .. ld - 1 are zero
+  int* publish;     // the flag of publish_waited(), or null
 };
 
 template <int kB>
@@ -238,7 +239,10 @@ __global__ void __launch_bounds__(kThreads, 2) dx_simt_kernel(DxParams p) {
   constexpr int kBN = simt_cols(kB);
   T& sm = tile_smem<T>();
   griddep_wait();
-  griddep_launch_dependents();  // (only now: the weight gradients read what dx waited for)
+  if (threadIdx.x == 0) {  // (only now: the weight gradients read what dx waited for)
+    if (p.publish && blockIdx.x == 0) publish_waited(p.publish);
+    griddep_launch_dependents();
+  }
   const int total = p.gr.unit_base[p.gr.N + 1];
   for (int u = blockIdx.x; u < total; u += gridDim.x) {
     int g, f, m;
@@ -284,14 +288,21 @@ struct DwParams {
   const int32_t* grp_row0;
   const int32_t* grp_rows;
   int accumulate;
-  int independent;  // runs beside its predecessor, whose own predecessor wrote what it reads
+  const int* ready;  // null, or the predecessor's flag: it has waited for what this reads, which runs beside it
+  unsigned* status;
 };
 
 template <class T, int kB>
 __global__ void __launch_bounds__(kThreads, 2) dw_simt_kernel(DwParams p, int units) {
   T& sm = tile_smem<T>();
   griddep_launch_dependents();
-  if (!p.independent) griddep_wait();
+  if (p.ready) {
+    const bool go = threadIdx.x > 0 || take_published(p.ready);
+    if (!go) set_status(p.status, MOE_DEV_WAIT_TIMEOUT);
+    if (!__syncthreads_and(go)) units = 0;
+  } else {
+    griddep_wait();
+  }
   for (int u = blockIdx.x; u < units; u += gridDim.x) {
     int i0 = 0, left = u;
     while (i0 < p.nmat - 1 && left >= p.per_group[i0] * p.groups) left -= p.per_group[i0++] * p.groups;
@@ -320,7 +331,7 @@ __global__ void __launch_bounds__(kThreads, 2) dw_simt_kernel(DwParams p, int un
         *o = v;
       }
   }
-  if (p.independent) griddep_wait();  // this grid ends after its predecessor
+  if (p.ready) griddep_wait();  // this grid ends after its predecessor
 }
 
 template <class T, int kB>
@@ -437,7 +448,7 @@ cudaError_t launch_experts_backward_simt(const Problem& p, const ExpertsBwdArgs&
   cudaError_t e = launch_dh(h, tile, s);
   if (e == cudaSuccess && a.dx_rows) {
     DxParams x{g2, (const float*)a.dg, (const float*)a.du, (const float*)a.W1, (const float*)a.W3, (float*)a.dx_rows,
-               p.d, p.F, p.F};
+               p.d, p.F, p.F, a.dW1 ? a.sched + kSchedReady : nullptr};
     e = launch_dx(x, tile, s);
   }
   if (e == cudaSuccess && a.dW1) {
@@ -450,7 +461,8 @@ cudaError_t launch_experts_backward_simt(const Problem& p, const ExpertsBwdArgs&
     w.grp_row0 = a.grp_row0;
     w.grp_rows = a.grp_rows;
     w.accumulate = a.accumulate;
-    w.independent = a.dx_rows != nullptr;
+    w.ready = a.dx_rows ? a.sched + kSchedReady : nullptr;
+    w.status = a.status;
     e = launch_dw(w, s);
   }
   if (e == cudaSuccess && a.dgate_rows)
@@ -468,7 +480,7 @@ cudaError_t launch_route_products_simt(const Problem& p, const RouteBwdArgs& a, 
   cudaError_t e = cudaSuccess;
   if (a.dx) {
     DxParams x{Groups{a.tables + kRtUnits, row0, rows, 1}, a.dz, nullptr, (const float*)a.W_r, nullptr,
-               (float*)a.dx, p.d, p.N, a.ld};
+               (float*)a.dx, p.d, p.N, a.ld, a.dW_r ? a.tables + kRtReady : nullptr};
     e = launch_dx(x, simt_bwd_tile(one), s);
   }
   if (e == cudaSuccess && a.dW_r) {
@@ -480,7 +492,8 @@ cudaError_t launch_route_products_simt(const Problem& p, const RouteBwdArgs& a, 
     w.grp_row0 = a.tables + kRtSplit0;
     w.grp_rows = a.tables + kRtSplitRows;
     w.accumulate = !split && a.accumulate;
-    w.independent = a.dx != nullptr;
+    w.ready = a.dx ? a.tables + kRtReady : nullptr;
+    w.status = a.status;
     e = launch_dw_tile<MidTile, 64>(w, s);
     if (e == cudaSuccess && split)
       e = launch_join_planes(a.planes, a.splits, (int64_t)p.N * p.d, a.dW_r, a.grad_dtype, a.accumulate, s);

@@ -82,7 +82,9 @@ struct Params {
   const int32_t* grp_rows;
   int accumulate;
   unsigned* status;
-  int independent, beside;  // see WgradArgs
+  const int* ready;  // see WgradArgs
+  int* publish;
+  int beside;
 };
 
 struct Shared {
@@ -95,6 +97,7 @@ struct Shared {
   uint32_t tmem_base;
   uint32_t sink;               // target of CTA 1's signalling stores (never read)
   int abort_flag;
+  int go;                      // what is read may be read
 };
 static_assert(sizeof(Shared) <= 512, "barrier block");
 
@@ -208,6 +211,10 @@ __global__ void __launch_bounds__(kThreads, 1) wgrad_tc_kernel(const __grid_cons
     sh.abort_flag = 0;
     fence_barrier_init();
   }
+  if (threadIdx.x == 64) {
+    sh.go = !p.ready || take_published(p.ready);
+    if (!sh.go) set_status(p.status, MOE_DEV_WAIT_TIMEOUT);
+  }
   if (warp == 1) {
     tmem_alloc_pair(&sh.tmem_base, kTmemCols);
     tmem_relinquish_pair();
@@ -215,8 +222,20 @@ __global__ void __launch_bounds__(kThreads, 1) wgrad_tc_kernel(const __grid_cons
   tc_fence_before();
   cluster_sync();
   tc_fence_after();
-  if (!p.independent) griddep_wait();
-  if (p.beside && threadIdx.x == 0) griddep_launch_dependents();
+  if (!p.ready) griddep_wait();
+  else fence_proxy_async_global();
+  // (the vote keeps what follows warp-uniform for the compiler: read as it is, the flag
+  // moved the walks out of uniform registers, 154 -> 168 of them and spills)
+  if (!__any_sync(0xffffffffu, sh.go)) {  // nothing may be read; the waits of the other CTA run out
+    griddep_wait();
+    cluster_sync();
+    if (warp == 1) tmem_dealloc_pair(sh.tmem_base, kTmemCols);
+    return;
+  }
+  if (threadIdx.x == 64) {  // (not a producer: the release takes about 1 us)
+    if (p.publish && blockIdx.x == 0) publish_waited(p.publish);
+    if (p.beside) griddep_launch_dependents();
+  }
   Walk walk(p, (int)(blockIdx.x >> 1), (int)(gridDim.x >> 1));
   Unit t;
   Buffers buf;
@@ -570,7 +589,7 @@ __global__ void __launch_bounds__(kThreads, 1) wgrad_tc_kernel(const __grid_cons
       }
     }
   }
-  if (p.independent) griddep_wait();  // this grid ends after its predecessor
+  if (p.ready) griddep_wait();  // this grid ends after its predecessor
   tc_fence_before();
   cluster_sync();  // neither CTA leaves while the other may still touch its shared memory
   if (warp == 1) {
@@ -651,7 +670,8 @@ cudaError_t launch_wgrad_tc(const WgradArgs& a, cudaStream_t s) {
   p.grp_rows = a.grp_rows;
   p.accumulate = a.accumulate;
   p.status = a.status;
-  p.independent = a.independent;
+  p.ready = a.ready;
+  p.publish = a.publish;
   p.beside = a.beside;
   if (p.units == 0) return cudaSuccess;
 
@@ -742,6 +762,7 @@ cudaError_t launch_route_products_tc(const Problem& p, const RouteBwdArgs& a, cu
     x.grad_dtype = MOE_BF16;
     x.status = a.status;
     x.max_pairs = dx_pairs;
+    x.publish = a.dW_r ? a.tables + kRtReady : nullptr;
     x.beside = dx_pairs > 0;
     const cudaError_t e = launch_wgrad_tc(x, s);
     if (e != cudaSuccess) return e;
@@ -758,7 +779,7 @@ cudaError_t launch_route_products_tc(const Problem& p, const RouteBwdArgs& a, cu
   w.grad_dtype = split ? (int)MOE_F32 : a.grad_dtype;
   w.accumulate = !split && a.accumulate;
   w.status = a.status;
-  w.independent = a.dx != nullptr;  // of the dx product, which has waited for dz
+  w.ready = a.dx ? a.tables + kRtReady : nullptr;  // the dx product has waited for dz
   w.max_pairs = dx_pairs > 0 ? device_sm_count() / 2 - dx_pairs : 0;
   const cudaError_t e = launch_wgrad_tc(w, s);
   if (e != cudaSuccess || !split) return e;

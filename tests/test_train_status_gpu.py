@@ -126,3 +126,87 @@ def test_the_norms_of_two_clips_keep_their_values():
         g.mul_(4.0)
     second = layer.clip(1e9, stream=torch.cuda.current_stream())
     assert float(second) == 4.0 * float(first) > 0.0
+
+
+# Calls that follow one another without a wait of the host, on one workspace, with other row counts, selections
+# and values each time: a kernel that read what the call before left there would give that call's results.
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d,f", [(72, 136), (520, 264)])
+def test_block_backwards_in_a_row_read_what_is_their_own(dtype, d, f):
+    gen = torch.Generator().manual_seed(d)
+    dt = {"bf16": torch.bfloat16, "f32": torch.float32}[dtype]
+
+    def new(*shape):
+        return torch.randn(shape, generator=gen).to(dt).cuda()
+
+    counts = [[17, 0, 40, 3], [0, 58, 1, 1], [15, 15, 15, 15], [60, 0, 0, 0]]
+    R, E = 60, 4
+    cfg = moe.make_cfg(d, f, E, 0, 1, dtype=dtype)
+    ws = torch.empty(moe.experts_backward_workspace_size(cfg, R), dtype=torch.uint8, device="cuda")
+    calls = []
+    for c in counts:
+        ins = [torch.tensor(c, dtype=torch.int32, device="cuda"), new(R, d), torch.rand(R, generator=gen).cuda(),
+               new(E, f, d), new(E, f, d), new(E, d, f), new(R, 2 * f), new(R, d)]
+        outs = [torch.empty(R, d, dtype=dt, device="cuda"), torch.empty(R, device="cuda")]
+        outs += [torch.empty_like(w) for w in ins[3:6]]
+        calls.append((ins, outs))
+
+    def run(ins, outs):
+        moe.experts_backward(cfg, R, *ins, *outs, ws)
+
+    want = []
+    for ins, outs in calls:
+        ws.fill_(255)
+        run(ins, outs)
+        torch.cuda.synchronize()
+        want.append([t.clone() for t in outs])
+        for t in outs:
+            t.fill_(7.0)
+    for turn in range(30):
+        for i in range(len(calls)):
+            run(*calls[(i * (turn % 3 + 1)) % len(calls)])
+    for ins, outs in calls:
+        run(ins, outs)
+    torch.cuda.synchronize()
+    for (_, outs), ref in zip(calls, want):
+        for got, t in zip(outs, ref):
+            assert torch.equal(got, t)
+    assert moe.device_status(cfg, R, ws) == 0
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T", [40, 700])
+def test_router_backwards_in_a_row_read_what_is_their_own(dtype, T):
+    gen = torch.Generator().manual_seed(T)
+    dt = {"bf16": torch.bfloat16, "f32": torch.float32}[dtype]
+    d, n, k = 264, 24, 3
+    cfg = moe.make_cfg(d, 8, n, 0, k, score="sigmoid", normalize=True, dtype=dtype)
+    ws = torch.empty(moe.route_backward_workspace_size(cfg, T), dtype=torch.uint8, device="cuda")
+    calls = []
+    for _ in range(3):
+        logits = torch.randn(T, n, generator=gen).cuda()
+        ins = [torch.randn(T, d, generator=gen).to(dt).cuda(), torch.randn(n, d, generator=gen).to(dt).cuda(), logits,
+               torch.topk(logits, k).indices.to(torch.int32), torch.randn(T, k, generator=gen).cuda()]
+        calls.append((ins, [torch.empty_like(ins[0]), torch.empty_like(ins[1])]))
+
+    def run(ins, outs):
+        moe.route_backward(cfg, T, *ins, None, *outs, ws)
+
+    want = []
+    for ins, outs in calls:
+        ws.fill_(255)
+        run(ins, outs)
+        torch.cuda.synchronize()
+        want.append([t.clone() for t in outs])
+    for turn in range(30):
+        for i in range(len(calls)):
+            run(*calls[(i * (turn % 2 + 1)) % len(calls)])
+    for ins, outs in calls:
+        run(ins, outs)
+    torch.cuda.synchronize()
+    for (_, outs), ref in zip(calls, want):
+        for got, t in zip(outs, ref):
+            assert torch.equal(got, t)
+    assert moe.device_status(cfg, T, ws) == 0
