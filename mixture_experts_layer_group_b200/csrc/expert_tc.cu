@@ -717,10 +717,9 @@ __global__ void __launch_bounds__(Plan<FP8>::kThreads, 1)
   tc_fence_before();
   cluster_sync();  // barriers and tensor memory of both CTAs are ready
   tc_fence_after();
-  // (programmatic launch: what a predecessor wrote, the unit tables among it,
-  // is read only after it has finished; the down GEMM's tables are older than
-  // its predecessor and its producer alone waits)
-  if (!is_down(MODE)) griddep_wait();
+  // (programmatic launch: what a predecessor wrote, and what grids before it wrote, the
+  // unit tables among that, is read only after it has finished)
+  griddep_wait();
   if constexpr (is_dx(MODE)) {
     if (threadIdx.x == 64) {  // (not the producer: the release takes about 1 us)
       if (p.publish && blockIdx.x == 0) publish_waited(p.publish);
@@ -738,9 +737,6 @@ __global__ void __launch_bounds__(Plan<FP8>::kThreads, 1)
     // ------------------------------------------------- scheduler + producer --
     // (the whole warp runs the loop, one elected lane issues: see elect_one())
     {
-      // the down GEMM may start while the SwiGLU GEMM drains (programmatic
-      // launch): nothing it loads may be read before that grid has finished
-      if (is_down(MODE)) griddep_wait();
       // a weight tile read by one unit only is streamed once: evict it first;
       // tiles shared by the chunks of a large group, and the token rows (read
       // by every feature tile of their group), are kept in L2 as long as possible

@@ -210,3 +210,42 @@ def test_router_backwards_in_a_row_read_what_is_their_own(dtype, T):
         for got, t in zip(outs, ref):
             assert torch.equal(got, t)
     assert moe.device_status(cfg, T, ws) == 0
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("train", [False, True])
+def test_block_forwards_in_a_row_read_what_is_their_own(dtype, train):
+    gen = torch.Generator().manual_seed(5)
+    dt = {"bf16": torch.bfloat16, "f32": torch.float32}[dtype]
+
+    def new(*shape):
+        return torch.randn(shape, generator=gen).to(dt).cuda()
+
+    R, E, d, f = 60, 4, 520, 264
+    cfg = moe.make_cfg(d, f, E, 0, 1, dtype=dtype)
+    ws = torch.empty(moe.experts_workspace_size(cfg, R), dtype=torch.uint8, device="cuda")
+    calls = []
+    for c in ([17, 0, 40, 3], [0, 58, 1, 1], [60, 0, 0, 0]):
+        ins = [torch.tensor(c, dtype=torch.int32, device="cuda"), new(R, d), torch.rand(R, generator=gen).cuda(),
+               new(E, f, d), new(E, f, d), new(E, d, f)]
+        calls.append((ins, [torch.empty_like(ins[1])] + ([new(R, 2 * f)] if train else [])))
+
+    def run(ins, outs):
+        (moe.experts_train if train else moe.experts)(cfg, R, *ins, *outs, ws)
+
+    want = []
+    for ins, outs in calls:
+        ws.fill_(255)
+        run(ins, outs)
+        torch.cuda.synchronize()
+        want.append([t.clone() for t in outs])
+    for turn in range(40):
+        for i in range(len(calls)):
+            run(*calls[(i * (turn % 2 + 1)) % len(calls)])
+    for ins, outs in calls:
+        run(ins, outs)
+    torch.cuda.synchronize()
+    for (_, outs), ref in zip(calls, want):
+        for got, t in zip(outs, ref):
+            assert torch.equal(got, t)
+    assert moe.device_status(cfg, R, ws) == 0
