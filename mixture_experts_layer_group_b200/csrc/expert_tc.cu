@@ -511,9 +511,13 @@ struct GuBlock {
 // features of each half, q from tensor memory, g and u from gu. Per element,
 // with s = sigma(g), act = g s, h = act u, dh = gate q:
 //   dgate += q h   du = dh act   dg = dh u (s + s (g - act))   gh = gate h
-// in packed fp32 pairs (two tokens). Per block a thread spends 64 special
-// function operations, which bound it: about 1000 cycles for the two warps
-// of a scheduler. The next block's g and u load meanwhile; the tiles of the
+// in packed fp32 pairs (two tokens). This is what bounds the product with K = 1280
+// (57344 rows of 63 experts of 896 features): the warps never wait for an
+// accumulator, and a block takes one about 5500 cycles, four blocks of a unit's
+// 28,000 (its MMAs are 10,200). Of a block, issuing the next one's loads of g and u
+// takes 1800, the move from tensor memory and the gate 1100, the arithmetic 1300
+// (64 special-function operations per thread are 1000 for the two warps of a
+// scheduler), the stores 600. The next block's g and u load meanwhile; the tiles of the
 // three results are written in place of g and u (one TMA store each), and the
 // sum over the block's features of q h is folded over the lanes after them.
 MOE_DEV void dh_epilogue(const BwdParams& p, const Unit& un, int64_t row_base, uint32_t t_q, uint32_t stride, int halves,
@@ -1454,7 +1458,7 @@ cudaError_t launch_one(const typename ParamsOf<MODE>::type& prm, int max_units, 
 
 // Whether the last unit of a matrix of this width takes one half. 57344 rows of
 // 896 features, d 1280 (units of 512, 512 and 256 columns): the training forward
-// 429 us without, 413 with; the backward 895 and 864.
+// 433 us without, 402 with; the backward 825 and 803 (the best of 40 calls each).
 bool edge_halves(int cols, int tile) { return (cols + tile / 2 - 1) / (tile / 2) % 2 == 1; }
 
 }  // namespace

@@ -1,5 +1,6 @@
 // Router backward: the gradient of the logits from the gradients of the
-// gates, per token (one warp), and what joins the split weight gradient.
+// gates, per token (half a warp; a warp for the dense softmax pass), and what
+// joins the split weight gradient.
 //
 // With s the scores, S the selected experts, c = route_scale, Z = sum_S s:
 //   normalised gates    ds_j = (c / Z) (dG_j - sum_S dG_i s_i / Z), j in S

@@ -235,7 +235,7 @@ struct SplitTile {
       }
     }
   }
-  // The four groups' sums, in order, as this thread's part of the tile.
+  // The kGroups groups' sums, in order, as this thread's part of the tile.
   MOE_DEV void finish(Acc& acc, float (&out)[4]) {
     const int t = threadIdx.x % kPart, g = threadIdx.x / kPart, tx = t & 7, ty = t >> 3;
     acc.total(nullptr);

@@ -24,7 +24,7 @@
 // One tile at a time would take 64 KB per 512 cycles. Measured: the gradients of
 // 63 experts of 896 x 1280 over 57344 rows 350 us (395 GFLOP, 1.13 PFLOP/s), of
 // one of 2048 x 7168 over 4096 rows 247 us (1.46 PFLOP/s), of 32 of those over
-// 8192 rows 746 us: 2.8 GB written, 717 us at the 3.93 TB/s that a B200 writes
+// 8192 rows 746 us: 2.8 GB written, 724 us at the 3.89 TB/s that a B200 writes
 // when it does nothing else. (The whole backward with tiles one by one: 946, 598
 // and 1622 us, in twos 911, 563 and 1548.)
 //
@@ -722,11 +722,13 @@ cudaError_t launch_wgrad_tc(const WgradArgs& a, cudaStream_t s) {
 // summed over the experts, many tiles with a short one. Run beside each other the
 // two hide each other's fixed costs (launch, first loads, last stores), and where
 // that leaves dW_r one token range its planes and their join are saved as well. In
-// tenths of a microsecond, as measured: a tile of dx 24, 64 tokens of a tile of
-// dW_r 7, joining planes 50, and 60 before the second of two launches one after
-// the other ends its first loads. The whole router backward, one after the other
-// and beside: T 4096, N 256, d 7168 58 and 48; T 8192, N 63, d 1280 40 and 34;
-// T 512, N 256, d 7168 33 and 22 us.
+// tenths of a microsecond, as measured: a tile of dx 24 (of 63 to 256 experts: most of it
+// is the store and fixed costs, so fewer or more experts are priced alike), 64 tokens of a
+// tile of dW_r 7, joining planes 50, and 60 before the second of two launches one
+// after the other ends its first loads. The whole router backward, one after the other
+// and beside: T 4096, N 256, d 7168 58 and 48; T 8192, N 63, d 1280 40 and 34; T 512,
+// N 256, d 7168 33 and 22 us (without the flag between them, which adds up to 1 us).
+// These three shapes are all that the prices were held against.
 RoutePlan plan_route_products(const Problem& p) {
   const int64_t pairs = device_sm_count() / 2, column_tiles = (p.d + kTile - 1) / kTile;
   const int64_t dw_tiles = (p.N + kTile - 1) / kTile * column_tiles, dx_tiles = (p.T + kTile - 1) / kTile * column_tiles;

@@ -130,7 +130,9 @@ class TrainLayer:
         return bits
 
     def forward(self, x, stream=None):
-        """y of the tokens x [T, d]; keeps what backward() needs."""
+        """y of the tokens x [T, d]; keeps what backward() needs. x itself is kept, not a copy (the routed
+        experts' rows are one): it and the weights stay as they are until backward() has run, or the gradients
+        of the router and the shared block mix two inputs."""
         self._check_rows("x", x)
         if x.shape[0] > self.max_tokens:
             raise ValueError(f"{x.shape[0]} tokens exceed max_tokens {self.max_tokens}")
