@@ -502,8 +502,9 @@ MOE_API moe_status moe_experts_train(const moe_cfg* cfg, int64_t rows, const int
  * rounding each, as the forward rounds h). dgate is not rounded below fp32, but
  * not as good as a product of fp32 multiply-adds: the tensor cores drop the bits
  * below an fp32 accumulator's last at each of the d / 16 steps of q, always towards
- * zero, so that the error does not average out over rows (measured 1e-6 of
- * dgate at d = 1280 and 8e-6 at 7168, where fp32 multiply-adds are off by 9e-7). rows == 0
+ * zero, so that the error does not average out over rows (measured 1.3e-6 of
+ * dgate at d = 1280 and 8e-6 at 7168, where fp32 multiply-adds are off by 3e-7 and
+ * 9e-7; seven eighths of it is the same share of every row's). rows == 0
  * zeroes the weight gradients (unless accumulating). Workspace:
  * moe_experts_backward_workspace_size(cfg, rows) bytes; the device-status
  * word as for moe_experts (counts that do not sum to rows: MOE_DEV_BAD_EXPERT,
